@@ -23,6 +23,7 @@ __all__ = [
     "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_quant", "fp8r_quantize_rows", "fp8r_gemm",
     "nvfp4_linear", "nvfp4_linear_dynamic", "nvfp4_linear_workspace_bytes", "nvfp4_linear_noalloc",
     "nvfp4_linear_noalloc_max_bytes", "fp8r_linear", "fp8r_linear_workspace_bytes",
+    "nvfp4_gemv", "fp8kv_append", "fp8kv_attention", "fp8kv_attention_workspace_bytes",
     "nvfp4_global_scale", "nvfp4_sf_convert", "nvfp4_sf_bytes", "nvfp4_dequantize",
     "bsp_last_device_status", "bsp_set_wait_limit_ms", "bsp_status_string", "bsp_version",
     "bsp_testing_gemm_stall", "bsp_testing_set_gemm_kernel", "bsp_testing_set_quant_kernel",
@@ -59,6 +60,16 @@ _SIGS = {
     "fp8r_linear_workspace_bytes": ([_c_i64, _c_i64], _c_i64),
     "fp8r_gemm": ([_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
                   _c_int),
+    "nvfp4_gemv": ([_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
+                   _c_int),
+    "fp8kv_append": ([_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_int,
+                      ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp,
+                      _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp],
+                     _c_int),
+    "fp8kv_attention": ([_c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp,
+                         _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                         ctypes.c_float, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp], _c_int),
+    "fp8kv_attention_workspace_bytes": ([_c_i64, _c_i64, _c_i64, _c_i64], _c_i64),
     "nvfp4_global_scale": ([_c_vp, _c_i64, _c_vp, _c_vp], _c_int),
     "nvfp4_sf_convert": ([_c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_int, _c_vp], _c_int),
     "nvfp4_dequantize": ([_c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp], _c_int),
@@ -381,6 +392,143 @@ def fp8r_gemm(a_q, a_row_scale, w_q, w_row_scale, bias=None, out=None, stream=No
            lib().fp8r_gemm(_ptr(a_q), _ptr(a_row_scale), _ptr(w_q), _ptr(w_row_scale),
                            _ptr(bias), _ptr(out), M, N, K, _stream(stream)))
     return out
+
+
+def nvfp4_gemv(x: torch.Tensor, w_codes, w_sf, w_scale, bias=None, out=None, stream=None):
+    """Y[M, N] bf16 = x [M, K] times an NVFP4 weight (operands as nvfp4_gemm's), x kept in
+    bf16: the weight-only form for 1 to 32 rows."""
+    M, K = _mat(x, torch.bfloat16, "x")
+    N, _ = _mat(w_codes, torch.uint8, "w_codes", K // 2)
+    _nvfp4_operands(0, N, K, None, None, w_sf, w_scale, bias)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _buf(out, torch.bfloat16, "out", M * N)
+    _check("nvfp4_gemv",
+           lib().nvfp4_gemv(_ptr(x), _ptr(w_codes), _ptr(w_sf), _ptr(w_scale), _ptr(bias),
+                            _ptr(out), M, N, K, _stream(stream)))
+    return out
+
+
+def _heads(t, what, T=None, D=None):
+    """bf16 [T, heads, D] whose heads lie side by side (a token's row may be part of a longer
+    one): returns (T, heads, D, elements between tokens)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    _dtype(t, torch.bfloat16, what)
+    if t.dim() != 3 or (T is not None and t.shape[0] != T) or (D is not None and t.shape[2] != D):
+        raise BSPError(f"argument check ({what} must be [T, heads, D], got {tuple(t.shape)})", -1)
+    n, h, d = t.shape
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and h > 1):
+        raise BSPError(f"argument check ({what}: the heads of a token must be contiguous)", -1)
+    return n, h, d, (s[0] if n > 1 else h * d)
+
+
+def _rows_ptr(t):
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise BSPError("argument check (tensor not on a CUDA device)", -1)
+    _require_current_device(t.device.index)
+    return t.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv_len):
+    """Checks of the arrays that fp8kv_append and fp8kv_attention share; returns
+    (pages, Hkv, page_size, D, B, max_pages)."""
+    for x, dt, what in ((k_cache, torch.uint8, "k_cache"), (v_cache, torch.uint8, "v_cache"),
+                        (k_scale, torch.uint8, "k_scale"), (v_scale, torch.uint8, "v_scale"),
+                        (block_table, torch.int32, "block_table"),
+                        (cu_new, torch.int32, "cu_new"), (kv_len, torch.int32, "kv_len")):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
+        _dtype(x, dt, what)
+    if k_cache.dim() != 4:
+        raise BSPError("argument check (k_cache must be [pages, heads, page_size, D], got "
+                       f"{tuple(k_cache.shape)})", -1)
+    pages, Hkv, page, D = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise BSPError("argument check (v_cache must have k_cache's shape)", -1)
+    B, max_pages = _mat(block_table, torch.int32, "block_table")
+    _buf(k_scale, torch.uint8, "k_scale", pages * Hkv * (page // 16))
+    _buf(v_scale, torch.uint8, "v_scale", pages * Hkv * (page // 16))
+    _buf(cu_new, torch.int32, "cu_new", B + 1)
+    _buf(kv_len, torch.int32, "kv_len", B)
+    return pages, Hkv, page, D, B, max_pages
+
+
+def fp8kv_append(k: torch.Tensor, v: torch.Tensor, k_cache, v_cache, k_scale, v_scale,
+                 block_table, cu_new, kv_len, q=None, q_out=None, inv_freq=None,
+                 interleaved: bool = False, rope_scale: float = 1.0, stream=None):
+    """Rotates the new tokens' k (and q, if given) by their positions and stores k and v in the
+    paged E4M3 cache (see fp8kv_append in bsp.h).  k, v: bf16 [T, Hkv, D], q: bf16 [T, Hq, D],
+    each possibly a slice of one projection's output; inv_freq: fp32 [rot / 2] or None for no
+    rotation.  Returns the rotated q (q_out), or None when no q is given."""
+    pages, Hkv, page, D, B, max_pages = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                  cu_new, kv_len)
+    T, hk, _, ks = _heads(k, "k", None, D)
+    _, hv, _, vs = _heads(v, "v", T, D)
+    if hk != Hkv or hv != Hkv:
+        raise BSPError(f"argument check (k and v must have the cache's {Hkv} heads)", -1)
+    rot = 0
+    if inv_freq is not None:
+        _buf(inv_freq, torch.float32, "inv_freq", 0)
+        rot = 2 * inv_freq.numel()
+    Hq = qs = 0
+    if q is not None:
+        _, Hq, _, qs = _heads(q, "q", T, D)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        _buf(q_out, torch.bfloat16, "q_out", T * Hq * D)
+    else:
+        q_out = None
+    _check("fp8kv_append",
+           lib().fp8kv_append(_rows_ptr(q), qs, _rows_ptr(k), ks, _rows_ptr(v), vs,
+                              _ptr(inv_freq), rot, int(interleaved), rope_scale, _ptr(q_out),
+                              _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages,
+                              page, _ptr(block_table), max_pages, _ptr(cu_new), _ptr(kv_len), B,
+                              T, Hq, Hkv, D, _stream(stream)))
+    return q_out
+
+
+def fp8kv_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
+    n = lib().fp8kv_attention_workspace_bytes(T, Hq, Hkv, D)
+    if n < 0:
+        raise BSPError("fp8kv_attention_workspace_bytes", int(n))
+    return int(n)
+
+
+def fp8kv_attention(q: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_table, cu_new,
+                    kv_len, sm_scale: float | None = None, window: int = 0, out=None, lse=None,
+                    return_lse: bool = False, workspace=None, stream=None):
+    """Attention of the new tokens' q (bf16 [T, Hq, D]) over the paged E4M3 cache, which already
+    holds their keys and values (see fp8kv_attention in bsp.h).  sm_scale defaults to D ** -0.5;
+    window 0 means none.  `workspace` (uint8, at least fp8kv_attention_workspace_bytes(T, Hq,
+    Hkv, D) bytes) is allocated here when not given.  Returns out (bf16 [T, Hq, D]), or
+    (out, lse) with return_lse."""
+    pages, Hkv, page, D, B, max_pages = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                  cu_new, kv_len)
+    T, Hq, _, qs = _heads(q, "q", None, D)
+    if Hq % Hkv != 0:
+        raise BSPError(f"argument check (q's {Hq} heads are no multiple of the cache's {Hkv})", -1)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    _buf(out, torch.bfloat16, "out", T * Hq * D)
+    if lse is None and return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    _buf(lse, torch.float32, "lse", T * Hq)
+    if workspace is None:
+        workspace = torch.empty((fp8kv_attention_workspace_bytes(T, Hq, Hkv, D),),
+                                dtype=torch.uint8, device=q.device)
+    _buf(workspace, torch.uint8, "workspace", 0)
+    _check("fp8kv_attention",
+           lib().fp8kv_attention(_rows_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                 _ptr(v_scale), pages, page, _ptr(block_table), max_pages,
+                                 _ptr(cu_new), _ptr(kv_len), B, T, Hq, Hkv, D,
+                                 D ** -0.5 if sm_scale is None else sm_scale, window, _ptr(out),
+                                 _ptr(lse), _ptr(workspace), workspace.numel(),
+                                 _stream(stream)))
+    return (out, lse) if return_lse else out
 
 
 def nvfp4_global_scale(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:

@@ -1,0 +1,355 @@
+// fp8kv_append.cu -- rotary positions on the new tokens' q and k, then k and v into the paged
+// block-scaled E4M3 cache, in one launch.
+//
+//   theta(p, j) = p * inv_freq[j], (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin) * rope_scale
+//   block of 16 tokens and head: e = max(e_old, ceil(log2(amax / 448))), code = E4M3(x * 2^-e)
+//
+// The work is memory traffic: q is read and written once in bf16, k and v are read once and
+// leave a quarter or half as many bytes.  One CTA takes one unit, the part of a sequence's
+// 16-token block that is new, and some of the heads; one warp takes one head of it, holds the
+// block in registers (amax and encode need no second read) and owns the block's scale, so no
+// atomics are needed.  The angles are the same for every head: the CTA makes them once, in
+// shared memory.  They are multiplied and reduced to [-pi, pi] in 64 bits (a position near
+// 2^20 times an fp32 frequency leaves no correct digit of the angle in 32), then sincosf.
+#include <cuda_bf16.h>
+
+#include "fp8kv_common.cuh"
+
+namespace bsp {
+namespace {
+
+struct AppendParams {
+    KvCache c;
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* q_out;
+    int64_t q_stride, k_stride, v_stride;
+    const float* inv_freq;
+    int32_t rot;
+    int32_t interleaved;
+    float rope_scale;
+    int* status;
+};
+
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&x)[16], int at)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[at + 2 * i] = bf16lo_to_f32(u[i]);
+        x[at + 2 * i + 1] = bf16hi_to_f32(u[i]);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&b);
+}
+
+// One lane's 16 elements of one token: two groups of 8 at element offsets o1, o2, and the
+// cos / sin pair index j0 of the first (-1: not rotated).
+struct Slot {
+    int token, o1, o2, j0;
+};
+
+__device__ __forceinline__ Slot slot_of(const AppendParams& p, int s, int per_token)
+{
+    const int token = s / per_token, c = s - token * per_token;
+    const int rs = p.rot >> 4;
+    Slot r;
+    r.token = token;
+    if (c < rs && !p.interleaved) {
+        r.o1 = 8 * c;
+        r.o2 = 8 * c + (p.rot >> 1);
+    } else {
+        r.o1 = 16 * c;
+        r.o2 = 16 * c + 8;
+    }
+    r.j0 = c < rs ? 8 * c : -1;
+    return r;
+}
+
+// Multiplications and sums are kept apart (no contraction), so the result does not depend on
+// which of the two products a compiler fuses.
+__device__ __forceinline__ void turn(float2 a, float& x1, float& x2)
+{
+    const float r1 = __fsub_rn(__fmul_rn(x1, a.x), __fmul_rn(x2, a.y));
+    const float r2 = __fadd_rn(__fmul_rn(x2, a.x), __fmul_rn(x1, a.y));
+    x1 = r1;
+    x2 = r2;
+}
+
+__device__ __forceinline__ void rotate(const AppendParams& p, const Slot& s, const float2* cs,
+                                       float (&x)[16])
+{
+    if (s.j0 < 0) return;
+    const float2* t = cs + s.token * (p.rot >> 1) + s.j0;
+    if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(t[i], x[2 * i], x[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(t[i], x[i], x[i + 8]);
+    }
+}
+
+// NS: slots of one lane in a block (ceil(D / 32) rounded up to a power of two).
+template <int NS>
+__global__ void __launch_bounds__(kAppendThreads) fp8kv_append_kernel(const AppendParams p)
+{
+    extern __shared__ float2 cs[];                       // [16][rot / 2]
+    const KvCache& c = p.c;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    int64_t begin;
+    const int64_t u = blockIdx.x;
+    const int b = kv_find_sequence(c, u, 1, 2, begin);
+    const KvRows rows = kv_rows(c, b);
+    const int32_t len = kv_length(c, b);
+    const int32_t start = len - rows.n;                  // position of the first new token
+    if (start < 0 && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
+    if (rows.n == 0 || start < 0 || u < begin) return;     // u < begin: cu_new descends
+    const int64_t block = start / kKvBlock + (u - begin);
+    const int64_t pos0 = block * kKvBlock;
+    if (pos0 >= len) return;
+    const int lo = start > pos0 ? static_cast<int>(start - pos0) : 0;     // new: [lo, hi)
+    const int hi = len - pos0 < kKvBlock ? static_cast<int>(len - pos0) : kKvBlock;
+    const int64_t row0 = rows.first + (pos0 - start);    // row of the block's token 0
+
+    const int half = p.rot >> 1;
+    for (int i = threadIdx.x; i < kKvBlock * half; i += kAppendThreads) {
+        const int t = i / half, j = i - t * half;
+        if (t < lo || t >= hi) continue;
+        const double x = static_cast<double>(pos0 + t) * static_cast<double>(__ldg(p.inv_freq + j));
+        const double n = rint(x * 0.15915494309189535);                 // 1 / (2 pi)
+        double r = fma(-n, 6.283185307179586, x);                       // 2 pi in two doubles
+        r = fma(-n, 2.4492935982947064e-16, r);
+        float sn, cn;
+        sincosf(static_cast<float>(r), &sn, &cn);
+        cs[i] = make_float2(__fmul_rn(cn, p.rope_scale), __fmul_rn(sn, p.rope_scale));
+    }
+    __syncthreads();
+
+    const int lane = threadIdx.x & 31;
+    const int per_token = c.D >> 4;
+    const int slots = kKvBlock * per_token;
+    const int nq = p.q ? c.Hq : 0;
+    const int tasks = nq + 2 * c.Hkv;
+    const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages +
+                               block / c.page_blocks);
+    const bool page_ok = page >= 0 && page < c.pages;
+    if (!page_ok && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
+
+    for (int task = blockIdx.y * (kAppendThreads / 32) + (threadIdx.x >> 5); task < tasks;
+         task += gridDim.y * (kAppendThreads / 32)) {
+        const bool is_q = task < nq;
+        const bool is_k = !is_q && task < nq + c.Hkv;
+        const int h = is_q ? task : (is_k ? task - nq : task - nq - c.Hkv);
+        const __nv_bfloat16* src = is_q ? p.q : (is_k ? p.k : p.v);
+        const int64_t stride = is_q ? p.q_stride : (is_k ? p.k_stride : p.v_stride);
+        src += row0 * stride + static_cast<int64_t>(h) * c.D;
+        if (!is_q && !page_ok) continue;
+
+        float x[NS][16];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int s = lane + 32 * i;
+            const Slot w = slot_of(p, s, per_token);
+            if (s >= slots || w.token < lo || w.token >= hi) continue;
+            const __nv_bfloat16* row = src + w.token * stride;
+            unpack8(*reinterpret_cast<const uint4*>(row + w.o1), x[i], 0);
+            unpack8(*reinterpret_cast<const uint4*>(row + w.o2), x[i], 8);
+            if (is_q || is_k) rotate(p, w, cs, x[i]);
+            // a NaN keeps no say in the scale
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t a = __float_as_uint(x[i][j]) & 0x7FFFFFFFu;
+                amax = a <= 0x7F800000u && a > amax ? a : amax;
+            }
+        }
+        if (is_q) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int s = lane + 32 * i;
+                const Slot w = slot_of(p, s, per_token);
+                if (s >= slots || w.token < lo || w.token >= hi) continue;
+                __nv_bfloat16* out = p.q_out + ((row0 + w.token) * c.Hq + h) * c.D;
+                uint4 a, d;
+                a = make_uint4(pack2(x[i][0], x[i][1]), pack2(x[i][2], x[i][3]),
+                               pack2(x[i][4], x[i][5]), pack2(x[i][6], x[i][7]));
+                d = make_uint4(pack2(x[i][8], x[i][9]), pack2(x[i][10], x[i][11]),
+                               pack2(x[i][12], x[i][13]), pack2(x[i][14], x[i][15]));
+                *reinterpret_cast<uint4*>(out + w.o1) = a;
+                *reinterpret_cast<uint4*>(out + w.o2) = d;
+            }
+            continue;
+        }
+        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+        const int64_t group = static_cast<int64_t>(page) * c.Hkv + h;
+        const int in_page = static_cast<int>(block % c.page_blocks);
+        uint8_t* scale = (is_k ? c.k_scale : c.v_scale) + group * c.page_blocks + in_page;
+        uint8_t* codes =
+            (is_k ? c.k : c.v) + (group * c.page_blocks + in_page) * kKvBlock * c.D;
+        int e = kv_scale_exp(amax);
+        if (lo > 0) {                                    // the block holds earlier tokens
+            const int old = min(static_cast<int>(*scale), kKvMaxExp);
+            if (e > old) {
+                const int d = e - old;                   // their codes times 2^-d, rounded once
+                const float f = d < 126 ? kv_pow2(127 - d) : 0.0f;
+                for (int i = lane; i < lo * c.D / 4; i += 32) {
+                    uint32_t* at = reinterpret_cast<uint32_t*>(codes) + i;
+                    uint32_t a, d2;
+                    e4m3x4_to_f16(*at, a, d2);
+                    float y0, y1, y2, y3;
+                    f16x2_to_f32(a, y0, y1);
+                    f16x2_to_f32(d2, y2, y3);
+                    *at = cvt_e4m3x2(y0 * f, y1 * f) | cvt_e4m3x2(y2 * f, y3 * f) << 16;
+                }
+            }
+            e = max(e, old);
+        }
+        __syncwarp();
+        if (lane == 0) *scale = static_cast<uint8_t>(e);
+        // 2^(127 - e), as two factors: either alone is a normal number
+        const float f1 = kv_pow2(127 + (127 - e) / 2), f2 = kv_pow2(127 + (127 - e) - (127 - e) / 2);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int s = lane + 32 * i;
+            const Slot w = slot_of(p, s, per_token);
+            if (s >= slots || w.token < lo || w.token >= hi) continue;
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[j] = cvt_e4m3x2(x[i][4 * j] * f1 * f2, x[i][4 * j + 1] * f1 * f2) |
+                       cvt_e4m3x2(x[i][4 * j + 2] * f1 * f2, x[i][4 * j + 3] * f1 * f2) << 16;
+            uint8_t* out = codes + w.token * c.D;
+            *reinterpret_cast<uint2*>(out + w.o1) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2*>(out + w.o2) = make_uint2(o[2], o[3]);
+        }
+    }
+}
+
+}  // namespace
+
+int kv_check_cache(KvCache& c, const void* k_cache, const void* v_cache, const void* k_scale,
+                   const void* v_scale, int64_t pages, int64_t page_size, const int32_t* table,
+                   int64_t max_pages, const int32_t* cu_new, const int32_t* kv_len, int64_t B,
+                   int64_t T, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    if (B < 0 || T < 0 || Hq < 0 || Hkv <= 0 || D <= 0 || pages < 0 || max_pages < 0 ||
+        page_size <= 0)
+        return BSP_ERR_INVALID_ARG;
+    constexpr int64_t kMost = int64_t{1} << 30;
+    if (D % 16 != 0 || D > 256 || page_size % kKvBlock != 0 || page_size > 4096 ||
+        Hq % Hkv != 0 || Hkv > 4096 || Hq > 4096 || B > (1 << 20) || T > kMost / 64 ||
+        pages > kMost || max_pages > kMost || T * Hq > kMost)
+        return BSP_ERR_UNSUPPORTED_SHAPE;
+    c.k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+    c.v = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+    c.k_scale = static_cast<uint8_t*>(const_cast<void*>(k_scale));
+    c.v_scale = static_cast<uint8_t*>(const_cast<void*>(v_scale));
+    c.table = table;
+    c.cu_new = cu_new;
+    c.kv_len = kv_len;
+    c.max_pages = max_pages;
+    c.pages = static_cast<int32_t>(pages);
+    c.page_blocks = static_cast<int32_t>(page_size / kKvBlock);
+    c.B = static_cast<int32_t>(B);
+    c.T = static_cast<int32_t>(T);
+    c.Hq = static_cast<int32_t>(Hq);
+    c.Hkv = static_cast<int32_t>(Hkv);
+    c.D = static_cast<int32_t>(D);
+    return BSP_OK;
+}
+
+int kv_check_pointers(const KvCache& c)
+{
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale || !c.table || !c.cu_new || !c.kv_len)
+        return BSP_ERR_INVALID_ARG;
+    const auto a4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (!aligned16(c.k) || !aligned16(c.v) || !a4(c.table) || !a4(c.cu_new) || !a4(c.kv_len))
+        return BSP_ERR_MISALIGNED;
+    return BSP_OK;
+}
+
+}  // namespace bsp
+
+extern "C" int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16,
+                            int64_t k_stride, const void* v_bf16, int64_t v_stride,
+                            const float* inv_freq, int64_t rot, int interleaved, float rope_scale,
+                            void* q_out_bf16, uint8_t* k_cache, uint8_t* v_cache,
+                            uint8_t* k_scale, uint8_t* v_scale, int64_t pages, int64_t page_size,
+                            const int32_t* block_table, int64_t max_pages, const int32_t* cu_new,
+                            const int32_t* kv_len, int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                            int64_t D, bsp_stream_t stream)
+{
+    using namespace bsp;
+    AppendParams p = {};
+    int st = kv_check_cache(p.c, k_cache, v_cache, k_scale, v_scale, pages, page_size, block_table,
+                            max_pages, cu_new, kv_len, B, T, Hq, Hkv, D);
+    if (st != BSP_OK) return st;
+    if (rot < 0 || (interleaved != 0 && interleaved != 1)) return BSP_ERR_INVALID_ARG;
+    if (rot % 16 != 0 || rot > D) return BSP_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0 || B == 0) return BSP_OK;
+    if (!k_bf16 || !v_bf16 || (rot > 0 && !inv_freq) || (q_bf16 && (!q_out_bf16 || Hq == 0)))
+        return BSP_ERR_INVALID_ARG;
+    if (k_stride < Hkv * D || v_stride < Hkv * D || (q_bf16 && q_stride < Hq * D))
+        return BSP_ERR_INVALID_ARG;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || (q_bf16 && q_stride % 8 != 0))
+        return BSP_ERR_UNSUPPORTED_SHAPE;
+    if (pages == 0 || max_pages == 0) return BSP_ERR_INVALID_ARG;
+    st = kv_check_pointers(p.c);
+    if (st != BSP_OK) return st;
+    if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(q_out_bf16) ||
+        (reinterpret_cast<uintptr_t>(inv_freq) & 3u))
+        return BSP_ERR_MISALIGNED;
+    int dev = 0, sms = 0;
+    st = check_device(&dev, &sms);
+    if (st != BSP_OK) return st;
+    p.q = static_cast<const __nv_bfloat16*>(q_bf16);
+    p.k = static_cast<const __nv_bfloat16*>(k_bf16);
+    p.v = static_cast<const __nv_bfloat16*>(v_bf16);
+    p.q_out = static_cast<__nv_bfloat16*>(q_out_bf16);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.inv_freq = inv_freq;
+    p.rot = static_cast<int32_t>(rot);
+    p.interleaved = interleaved;
+    p.rope_scale = rope_scale;
+    p.status = device_status_ptr(dev);
+
+    // room for each sequence's blocks: it touches at most floor(n / 16) + 2 of them
+    const int64_t units = T / kKvBlock + 2 * B;
+    const int64_t tasks = (q_bf16 ? Hq : 0) + 2 * Hkv;
+    constexpr int kWarps = kAppendThreads / 32;
+    const int64_t groups = (tasks + kWarps - 1) / kWarps;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>(groups), 1);
+    cfg.blockDim = dim3(kAppendThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(kKvBlock) * (rot / 2) * sizeof(float2);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    if (D <= 64)
+        e = cudaLaunchKernelEx(&cfg, fp8kv_append_kernel<2>, p);
+    else if (D <= 128)
+        e = cudaLaunchKernelEx(&cfg, fp8kv_append_kernel<4>, p);
+    else
+        e = cudaLaunchKernelEx(&cfg, fp8kv_append_kernel<8>, p);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return BSP_ERR_CUDA;
+    }
+    return launch_status();
+}

@@ -1,0 +1,127 @@
+// fp8kv_common.cuh -- what the kernels of the block-scaled 8-bit key/value cache share:
+// the cache's geometry, the ragged batch, and the E4M3 / E8M0 arithmetic of one block.
+//
+// A cache holds E4M3 codes [pages][Hkv][page_size][D] and, for every block of 16 tokens and
+// head, one E8M0 byte e (scale 2^(e - 127)) in [pages][Hkv][page_size / 16].  A power of two
+// costs E4M3 no precision, leaves the decode exact, and lets a later token raise a block's
+// scale: the earlier codes then only move their exponent (they are re-rounded where they
+// become subnormal, below 2^-6 of the new scale).
+#pragma once
+
+#include <cstdint>
+
+#include "bsp_internal.h"
+#include "bsp_ptx.cuh"
+
+namespace bsp {
+
+constexpr int kKvBlock = 16;        // tokens that share one scale
+constexpr int kKvMaxExp = 246;      // largest scale byte: 448 * 2^119 is the last finite multiple
+
+struct KvCache {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    const int32_t* table;           // [B][max_pages] page numbers
+    const int32_t* cu_new;          // [B + 1] rows of the new tokens
+    const int32_t* kv_len;          // [B] lengths, the new tokens included
+    int64_t max_pages;
+    int32_t pages;
+    int32_t page_blocks;            // page_size / 16
+    int32_t B, T, Hq, Hkv, D;
+};
+
+// Rows [first, first + n) of sequence b; whatever cu_new holds, they lie in [0, T).
+struct KvRows {
+    int32_t first, n;
+};
+
+__device__ __forceinline__ int32_t kv_clamp_row(int32_t r, int32_t T)
+{
+    return r < 0 ? 0 : (r > T ? T : r);
+}
+
+__device__ __forceinline__ KvRows kv_rows(const KvCache& c, int b)
+{
+    const int32_t lo = kv_clamp_row(__ldg(c.cu_new + b), c.T);
+    const int32_t hi = kv_clamp_row(__ldg(c.cu_new + b + 1), c.T);
+    return {lo, hi > lo ? hi - lo : 0};
+}
+
+// kv_len[b], cut to what the table's row can address.
+__device__ __forceinline__ int32_t kv_length(const KvCache& c, int b)
+{
+    const int64_t cap = c.max_pages * c.page_blocks * kKvBlock;
+    const int32_t l = __ldg(c.kv_len + b);
+    return l < 0 ? 0 : (l > cap ? static_cast<int32_t>(cap) : l);
+}
+
+// The sequence whose work units contain unit u, when sequence b's begin at
+// floor(cu_new[b] * per / 16) + extra * b: the last b that begins at or before u.  Called by
+// every thread of the CTA (the CTA counts the beginnings, so the cost is one load and one
+// barrier for each blockDim.x sequences, not a chain of dependent loads).
+__device__ __forceinline__ int kv_find_sequence(const KvCache& c, int64_t u, int per, int extra,
+                                                int64_t& begin)
+{
+    int b = -1;
+    for (int base = 0; base < c.B; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        bool in = false;
+        if (i < c.B) {
+            const int64_t at =
+                static_cast<int64_t>(kv_clamp_row(__ldg(c.cu_new + i), c.T)) * per / kKvBlock +
+                static_cast<int64_t>(extra) * i;
+            in = at <= u;
+        }
+        b += __syncthreads_count(in);
+    }
+    if (b < 0) b = 0;
+    begin = static_cast<int64_t>(kv_clamp_row(__ldg(c.cu_new + b), c.T)) * per / kKvBlock +
+            static_cast<int64_t>(extra) * b;
+    return b;
+}
+
+// Smallest scale byte whose 448 multiples reach amax (bits of a non-negative fp32):
+// e = ceil(log2(amax / 448)) + 127, within [0, kKvMaxExp].  448 = 1.75 * 2^8.
+__device__ __forceinline__ int kv_scale_exp(uint32_t amax_bits)
+{
+    const int e = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u);
+    return e < 0 ? 0 : (e > kKvMaxExp ? kKvMaxExp : e);
+}
+
+// 2^(e - 127) for e in [0, 254]; e == 0 is the subnormal 2^-127.
+__device__ __forceinline__ float kv_pow2(int e)
+{
+    return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
+}
+
+// Four E4M3 bytes -> two pairs of f16 (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ void f16x2_to_f32(uint32_t h, float& lo, float& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.f32.f16 %0, a;\n\t"
+        "cvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+}
+
+// Device status word: a page outside the pool, or a length below the new tokens' count (first
+// writer wins).
+__device__ __forceinline__ void kv_report_bad_batch(int* status)
+{
+    if (atomicCAS(status, 0, BSP_ERR_INVALID_ARG) == 0) atomicCAS(status + 1, 0, 200);
+}
+
+}  // namespace bsp

@@ -8,7 +8,9 @@ row, and quantizes its activations per row at run time.  The scheme is read from
 tensors present, as that page's loader does.
 
 The module only marshals: forward() is one nvfp4_linear call (activation quantizer +
-FP4 GEMM) or fp8r_quantize_rows + fp8r_gemm, all in libbsp.so.  `weight_scale` is kept
+FP4 GEMM) or fp8r_quantize_rows + fp8r_gemm, all in libbsp.so.  An nvfp4 module with
+`weight_only_rows` = r > 0 sends inputs of at most r rows (single tokens of a decode step)
+to nvfp4_gemv instead, which reads the same weight and does not quantize the activations.  `weight_scale` is kept
 in the checkpoint's row-major [N][K/16] layout (the state-dict form); the tensor-core
 layout the GEMM reads is built from it on the device once and rebuilt after a load.
 """
@@ -16,8 +18,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (SF_LINEAR, SF_MMA, BSPError, fp8r_gemm, fp8r_quantize_rows, nvfp4_global_scale,
-               nvfp4_linear, nvfp4_linear_workspace_bytes, nvfp4_quantize_act, nvfp4_sf_convert)
+from . import (SF_LINEAR, SF_MMA, BSPError, fp8r_gemm, fp8r_quantize_rows, nvfp4_gemv,
+               nvfp4_global_scale, nvfp4_linear, nvfp4_linear_workspace_bytes,
+               nvfp4_quantize_act, nvfp4_sf_convert)
 
 __all__ = ["QuantLinear"]
 
@@ -32,10 +35,13 @@ class QuantLinear(torch.nn.Module):
     """y = x W^T (+ bias) with W stored as nvfp4 or fp8r; x is bf16 [..., in_features]."""
 
     def __init__(self, in_features: int, out_features: int, scheme: str = "nvfp4",
-                 bias: bool = True, device=None):
+                 bias: bool = True, device=None, weight_only_rows: int = 0):
         super().__init__()
         if scheme not in ("nvfp4", "fp8r"):
             raise ValueError(f"unknown scheme {scheme!r} (nvfp4 or fp8r)")
+        if not 0 <= weight_only_rows <= (32 if scheme == "nvfp4" else 0):
+            raise ValueError("weight_only_rows must be 0 .. 32 (0 for fp8r)")
+        self.weight_only_rows = weight_only_rows     # 0: activations are always quantized
         K, N = in_features, out_features
         if scheme == "nvfp4" and K % 64 != 0:
             raise ValueError("nvfp4 needs in_features % 64 == 0 (16-element blocks, four per "
@@ -136,6 +142,10 @@ class QuantLinear(torch.nn.Module):
             if self._sf_mma is None:
                 self._sf_mma = nvfp4_sf_convert(_u8(self.weight_scale).contiguous(), N, K,
                                                 SF_LINEAR, SF_MMA)
+            if M <= self.weight_only_rows:
+                nvfp4_gemv(x2, self.weight, self._sf_mma, self.weight_scale_2, bias=self.bias,
+                           out=y)
+                return y.reshape(*lead, N)
             need = nvfp4_linear_workspace_bytes(M, K)
             if self._workspace is None or self._workspace.numel() < need \
                     or self._workspace.device != x.device:

@@ -302,6 +302,98 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int layout,
                      bsp_stream_t stream);
 
 /*
+ * nvfp4_gemv -- a few rows of bf16 activations against an NVFP4 weight, the activations NOT
+ * quantized: the product of the dequantise-only path ("BFL (fp8r / nvfp4)", closing paragraph
+ * of the "Kernels" section) for single tokens, read straight from the 4-bit weight.
+ *   x_bf16  [M][K] bf16, 1 <= M <= 32 (M == 0 returns BSP_OK).
+ *   w_codes [N][K/2], w_sf (BSP_SF_MMA, rows = N), w_scale (device, 1 fp32), bias_bf16 [N] or
+ *           NULL, out_bf16 [M][N]: as nvfp4_gemm.
+ *   Y[m][n] = bf16( w_scale * sum_k x[m][k] * e2m1(w[n][k]) * e4m3(sf[n][k/16]) + bias[n] ),
+ *   products exact, sums in fp32.
+ * Constraints: K % 64 == 0, K >= 64; N % 8 == 0; M <= 32 (BSP_ERR_UNSUPPORTED_SHAPE).  The time
+ * is that of reading the weight; above 32 rows nvfp4_linear is the faster form.
+ */
+int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
+               const float* w_scale, const void* bias_bf16, void* out_bf16, int64_t M, int64_t N,
+               int64_t K, bsp_stream_t stream);
+
+/*
+ * The block-scaled 8-bit key/value cache.  One cache (one layer) is four device arrays:
+ *   k_cache, v_cache  E4M3 codes [pages][Hkv][page_size][D]
+ *   k_scale, v_scale  E8M0 bytes [pages][Hkv][page_size / 16]: one power of two 2^(byte - 127)
+ *                     for each block of 16 tokens and head; value = code * scale.
+ * and the ragged batch of a step is described, for both calls, by
+ *   block_table [B][max_pages] int32: token t of sequence b lies in page
+ *               block_table[b][t / page_size], slot t % page_size;
+ *   cu_new      [B + 1] int32, ascending from 0: the new tokens of sequence b are rows
+ *               cu_new[b] .. cu_new[b + 1) of q, k, v and out (none, one or many); rows from
+ *               cu_new[B] to T are neither read nor written;
+ *   kv_len      [B] int32: the sequence's length INCLUDING its new tokens, whose positions are
+ *               kv_len[b] - n .. kv_len[b] - 1.
+ * Lengths, rows and pages are read on the device, so a captured graph can be replayed while
+ * they change.  The kernels keep every access inside the arrays whatever these hold: rows
+ * outside [0, T) and lengths outside [0, max_pages * page_size] are cut off, a page outside
+ * [0, pages) is not touched (its tokens are neither stored nor attended to) and is reported by
+ * bsp_last_device_status() as BSP_ERR_INVALID_ARG.  Table entries of pages that a call does not
+ * reach are not read.
+ * Constraints: D % 16 == 0, D <= 256; page_size % 16 == 0, page_size <= 4096; Hq % Hkv == 0,
+ * Hq and Hkv <= 4096; B <= 2^20, T <= 2^24, T * Hq <= 2^30.
+ */
+
+/*
+ * fp8kv_append -- rotary positions on the new tokens' q and k, then k and v into the cache, in
+ * one launch.
+ *   q_bf16   [T][Hq][D] or NULL (nothing is rotated into q_out then), k_bf16, v_bf16 [T][Hkv][D];
+ *            *_stride: elements between tokens (% 8 == 0, at least heads * D), so that the three
+ *            may lie in one projection's output.
+ *   inv_freq [rot / 2] fp32 (device), rot % 16 == 0, 0 <= rot <= D: the first rot elements of each
+ *            head are rotated by theta = position * inv_freq[j], taken in 64 bits; any scaling for
+ *            long contexts is in the frequencies.  Pairs are (j, j + rot / 2), or (2j, 2j + 1) with
+ *            interleaved = 1.  cos and sin are multiplied by rope_scale.
+ *   q_out    [T][Hq][D] bf16, contiguous; may be q itself when that is contiguous.
+ * For each block of 16 tokens and head (x: the rotated keys in fp32, or the values):
+ *   e = ceil(log2(amax / 448)) + 127 over the new tokens, within [0, 246] (0 when amax is 0); a
+ *   block that already holds tokens keeps the larger of e and its own, and codes that it holds
+ *   move to a raised scale by one rounding; code = E4M3(x * 2^(127 - e)), to nearest even,
+ *   saturating at +-448.  Infinities store as +-448 * 2^119, a NaN stores as NaN (only its own
+ *   element).
+ * Tokens of the block after the last new one are left as they are.  A page that is appended to
+ * must belong to one sequence of the batch; a sequence with kv_len[b] < n is left out and reported.
+ */
+int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
+                 const void* v_bf16, int64_t v_stride, const float* inv_freq, int64_t rot,
+                 int interleaved, float rope_scale, void* q_out_bf16, uint8_t* k_cache,
+                 uint8_t* v_cache, uint8_t* k_scale, uint8_t* v_scale, int64_t pages,
+                 int64_t page_size, const int32_t* block_table, int64_t max_pages,
+                 const int32_t* cu_new, const int32_t* kv_len, int64_t B, int64_t T, int64_t Hq,
+                 int64_t Hkv, int64_t D, bsp_stream_t stream);
+
+/*
+ * fp8kv_attention -- attention of the new tokens over the cache (which already holds them):
+ *   out[r][h] = sum_t p_t v_t / sum_t p_t, p_t = exp(sm_scale * q[r][h] . k_t), head h reading key
+ *   head h / (Hq / Hkv), over the tokens t <= pos(r), and t > pos(r) - window when window > 0.
+ *   q_bf16  [T][Hq][D], q_stride elements between tokens (% 8 == 0).
+ *   out     [T][Hq][D] bf16, contiguous; lse [T][Hq] fp32 or NULL: log of sum_t p_t.
+ *   A row that sees no token gives zeros and lse = -infinity.  Softmax statistics and sums are
+ *   fp32; the weights p are rounded once to 11 bits.  What masked tokens hold (NaN, stale
+ *   bytes, stale scales of blocks behind the end) has no effect.
+ *   workspace  device buffer of at least fp8kv_attention_workspace_bytes(T, Hq, Hkv, D) bytes,
+ *              16-byte aligned, any contents; not shared by calls that can run at the same time.
+ * Meant for one to a few new tokens per sequence: every 16 rows (new tokens * Hq / Hkv) of a
+ * sequence read its keys and values once more.
+ */
+int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache,
+                    const uint8_t* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                    int64_t pages, int64_t page_size, const int32_t* block_table,
+                    int64_t max_pages, const int32_t* cu_new, const int32_t* kv_len, int64_t B,
+                    int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale,
+                    int64_t window, void* out_bf16, float* lse, void* workspace,
+                    int64_t workspace_bytes, bsp_stream_t stream);
+
+/* Workspace bytes fp8kv_attention needs; negative on bad arguments. */
+int64_t fp8kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D);
+
+/*
  * nvfp4_sf_convert -- re-lay block scales between BSP_SF_LINEAR and BSP_SF_MMA
  * (rows x K/16 bytes; padding of an MMA-layout destination is written as 0).
  * Constraints: K % 64 == 0.  src and dst must not overlap.
