@@ -19,7 +19,9 @@
 //   * running maximum and sum in fp32; the output is rescaled only when a maximum moves.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <mutex>
+
+#include <algorithm>
+#include <atomic>
 
 #include "fp8kv_common.cuh"
 
@@ -43,10 +45,16 @@ struct AttnParams {
     int32_t window;          // 0: none
     int32_t G;
     int* status;
+    float* parts;            // [2 * ctas][slot_rows][D + 2]: output, maximum, sum of a part
+    int32_t slot_rows;
 };
 
 constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kRows = 16;
+constexpr int kTile = kAttnWarps * kKvBlock;     // tokens of one tile: a block for each warp
+constexpr int kMaxCtas = 640;                    // 148 SMs x 4, rounded up
+constexpr int kMinTiles = 2;                     // tiles a CTA takes at least
 constexpr int kPShift = 13;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -71,6 +79,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// log of the sum l of weights exp2(s - m)
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return m == -INFINITY && l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // 0x80 in each byte of w that is an E4M3 NaN
@@ -99,6 +113,119 @@ __device__ __forceinline__ void mma_v(float (&o)[NT][4], const uint32_t (&vr)[4]
     }
 }
 
+// ---- how the work is split.  An item is one row tile of one key head of a sequence; sequence b
+// has items(b) = row tiles * Hkv of tiles(b) token tiles each.  All tiles of all items in a row
+// are cut into equal runs, one for each CTA, whatever the lengths are: a run may end one item,
+// hold whole ones and begin another.  Only the first and the last item of a run can be cut, so a
+// CTA leaves at most two parts; fp8kv_join_kernel adds the parts of a cut item in order.
+struct SeqWork {
+    int32_t first, n, len;       // rows, new tokens, length
+    int32_t row_tiles, tile0, tiles;
+};
+
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
+{
+    SeqWork s;
+    const KvRows r = kv_rows(p.c, b);
+    s.first = r.first;
+    s.n = r.n;
+    s.len = kv_length(p.c, b);
+    s.row_tiles = (s.n * p.G + kRows - 1) / kRows;
+    const int32_t lo = p.window ? max(0, s.len - s.n - p.window + 1) : 0;
+    s.tile0 = lo / kTile;
+    s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
+    return s;
+}
+
+__device__ __forceinline__ int64_t seq_tiles(const AttnParams& p, int b)
+{
+    const SeqWork s = seq_work(p, b);
+    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * s.tiles;
+}
+
+// Where tile `at` of the whole row lies.  total is the row's length.
+struct Place {
+    int b;
+    int64_t before;              // tiles of the sequences before b
+};
+
+struct SplitShared {
+    int64_t warp_sum[kAttnWarps];
+    int64_t before;
+    int b;
+};
+
+__device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_t& chunk)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = inc;
+    __syncthreads();
+    chunk = 0;
+    int64_t pre = 0;
+#pragma unroll
+    for (int i = 0; i < kAttnWarps; ++i) {
+        if (i < warp) pre += sh.warp_sum[i];
+        chunk += sh.warp_sum[i];
+    }
+    return pre + inc - w;        // tiles before this thread's sequence, in this chunk
+}
+
+// Total number of tiles, and (through `pick`, which maps the total to a tile) the sequence that
+// holds that tile.  Called by every thread; Place is valid where pick's tile is below the total.
+template <typename Pick>
+__device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& sh, Pick pick,
+                                             Place& place)
+{
+    int64_t total = 0, w = 0, excl = 0, chunk = 0;
+    for (int base = 0; base < p.c.B; base += kAttnThreads) {
+        const int i = base + threadIdx.x;
+        w = i < p.c.B ? seq_tiles(p, i) : 0;
+        excl = chunk_scan(w, sh, chunk);
+        total += chunk;
+    }
+    const int64_t at = pick(total);
+    if (threadIdx.x == 0) {
+        sh.b = 0;
+        sh.before = 0;
+    }
+    __syncthreads();
+    if (p.c.B <= kAttnThreads) {                 // one chunk: it is still in registers
+        if (at >= excl && at < excl + w) {
+            sh.b = threadIdx.x;
+            sh.before = excl;
+        }
+    } else {
+        int64_t carry = 0;
+        for (int base = 0; base < p.c.B; base += kAttnThreads) {
+            const int i = base + threadIdx.x;
+            w = i < p.c.B ? seq_tiles(p, i) : 0;
+            excl = chunk_scan(w, sh, chunk) + carry;
+            if (at >= excl && at < excl + w) {
+                sh.b = i;
+                sh.before = excl;
+            }
+            carry += chunk;
+        }
+    }
+    __syncthreads();
+    place.b = sh.b;
+    place.before = sh.before;
+    return total;
+}
+
+__device__ __forceinline__ int64_t run_length(int64_t total, int ctas)
+{
+    const int64_t per = (total + ctas - 1) / ctas;
+    return per < kMinTiles ? kMinTiles : per;
+}
+
 // DP: head dimension rounded up to 64, 128 or 256.
 template <int DP>
 struct Dims {
@@ -109,7 +236,7 @@ struct Dims {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kAttnWarps * 32) fp8kv_attention_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kAttnThreads) fp8kv_attention_kernel(const AttnParams p)
 {
     using S = Dims<DP>;
     extern __shared__ uint4 smem[];
@@ -119,28 +246,50 @@ __global__ void __launch_bounds__(kAttnWarps * 32) fp8kv_attention_kernel(const 
     __shared__ float stat_m[kAttnWarps][kRows], stat_l[kAttnWarps][kRows];
     __shared__ int stat_e[kAttnWarps];
 
+    __shared__ SplitShared split;
+
     const KvCache& c = p.c;
     griddep_wait();
     griddep_launch_dependents();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    int64_t begin;
-    const int b = kv_find_sequence(c, blockIdx.x, p.G, 1, begin);
-    const KvRows rows = kv_rows(c, b);
-    const int row_base = static_cast<int>(blockIdx.x - begin) * kRows;
-    const int nrows = min(kRows, rows.n * p.G - row_base);
-    if (nrows <= 0 || blockIdx.x < begin) return;            // the latter: cu_new descends
-    const int h = blockIdx.y;
-    const int32_t len = kv_length(c, b);
-    const int32_t start = len - rows.n;                          // position of the first new token
+    Place place;
+    const int ctas = gridDim.x;
+    const int64_t total = find_tile(
+        p, split, [&](int64_t n) { return blockIdx.x * run_length(n, ctas); }, place);
+    const int64_t per = run_length(total, ctas);
+    int64_t at = blockIdx.x * per;
+    const int64_t end = min(at + per, total);
+    int b = place.b;
+    int64_t before = place.before;
+
+  while (at < end) {
+    SeqWork sw = seq_work(p, b);
+    int64_t mine = static_cast<int64_t>(sw.row_tiles) * c.Hkv * sw.tiles;
+    while (at >= before + mine && b + 1 < c.B) {
+        before += mine;
+        sw = seq_work(p, ++b);
+        mine = static_cast<int64_t>(sw.row_tiles) * c.Hkv * sw.tiles;
+    }
+    const int64_t item = (at - before) / sw.tiles;
+    const int seg0 = static_cast<int>((at - before) - item * sw.tiles);
+    const int seg1 = static_cast<int>(min(static_cast<int64_t>(sw.tiles), seg0 + (end - at)));
+    at += seg1 - seg0;
+    const bool whole = seg0 == 0 && seg1 == sw.tiles;
+    const int h = static_cast<int>(item / sw.row_tiles);
+    const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * kRows;
+    const int nrows = min(kRows, sw.n * p.G - row_base);
+    const int32_t len = sw.len;
+    const int32_t start = len - sw.n;                            // position of the first new token
+    __syncthreads();                                             // the shared buffers are free
 
     // ---- q: f16 fragments in shared memory
     for (int i = 0; i < kRows / kAttnWarps; ++i) {
         const int r = warp * (kRows / kAttnWarps) + i;
         const int rr = row_base + r, tok = rr / p.G, head = rr - tok * p.G;
         const bool ok = r < nrows;
-        const __nv_bfloat16* src = p.q + (rows.first + tok) * p.q_stride +
+        const __nv_bfloat16* src = p.q + (sw.first + tok) * p.q_stride +
                                    static_cast<int64_t>(h * p.G + head) * c.D;
         uint32_t w[DP / 64];
         uint32_t amax = 0;
@@ -171,7 +320,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32) fp8kv_attention_kernel(const 
     const int pos1 = start + (row_base + min(g + 8, nrows - 1)) / p.G;
     const int pos_lo = start + row_base / p.G, pos_hi = start + (row_base + nrows - 1) / p.G;
     const int first_tok = p.window ? max(0, pos_lo - p.window + 1) : 0;
-    const int blk_begin = first_tok / kKvBlock, blk_end = (pos_hi + kKvBlock) / kKvBlock;
+    const int blk_begin = max(first_tok / kKvBlock, (sw.tile0 + seg0) * kAttnWarps);
+    const int blk_end = min((pos_hi + kKvBlock) / kKvBlock, (sw.tile0 + seg1) * kAttnWarps);
 
     float o[S::kNT][4];
 #pragma unroll
@@ -400,7 +550,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32) fp8kv_attention_kernel(const 
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int rr = row_base + r, tok = rr / p.G, head = h * p.G + rr - tok * p.G;
-        const int64_t at = static_cast<int64_t>(rows.first + tok) * c.Hq + head;
+        const int64_t row = static_cast<int64_t>(sw.first + tok) * c.Hq + head;
+        float* part = p.parts + (static_cast<int64_t>(2 * blockIdx.x + (seg0 == 0)) * p.slot_rows +
+                                 r) * (c.D + 2);
         for (int d = 2 * lane; d < c.D; d += 64) {
             float x = 0.0f, y = 0.0f;
 #pragma unroll
@@ -410,29 +562,119 @@ __global__ void __launch_bounds__(kAttnWarps * 32) fp8kv_attention_kernel(const 
                 x += ow[0] * f1 * f2;
                 y += ow[1] * f1 * f2;
             }
-            *reinterpret_cast<__nv_bfloat162*>(p.out + at * c.D + d) = __floats2bfloat162_rn(x, y);
+            if (whole)
+                *reinterpret_cast<__nv_bfloat162*>(p.out + row * c.D + d) =
+                    __floats2bfloat162_rn(x, y);
+            else
+                *reinterpret_cast<float2*>(part + d) = make_float2(x, y);
         }
-        if (p.lse && lane == 0)
-            p.lse[at] = m == -INFINITY && l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (lane == 0) {
+            if (!whole) {
+                part[c.D] = m;
+                part[c.D + 1] = l;
+            } else if (p.lse) {
+                p.lse[row] = lse_of(m, l);
+            }
+        }
     }
+  }
+}
+
+// Adds the parts of the item that CTA blockIdx.x of the attention kernel began and did not end
+// (if it did): part i weighs l_i 2^(m_i - m), in the order of the tokens.  One warp takes one row.
+__global__ void __launch_bounds__(kAttnThreads)
+    fp8kv_join_kernel(const AttnParams p)
+{
+    __shared__ SplitShared split;
+    const KvCache& c = p.c;
+    const int ctas = gridDim.x;
+    Place place;
+    int64_t last = 0;
+    const int64_t total = find_tile(
+        p, split,
+        [&](int64_t n) {
+            last = min((blockIdx.x + int64_t{1}) * run_length(n, ctas), n) - 1;
+            return last;
+        },
+        place);
+    const int64_t per = run_length(total, ctas);
+    const int64_t begin = blockIdx.x * per;
+    griddep_wait();
+    if (begin >= total) return;
+    const SeqWork sw = seq_work(p, place.b);
+    const int64_t item = (last - place.before) / sw.tiles;
+    const int64_t s0 = place.before + item * sw.tiles, s1 = s0 + sw.tiles;   // the item's tiles
+    if (s0 < begin || s1 <= last + 1) return;
+    const int parts = static_cast<int>((s1 - 1) / per - blockIdx.x) + 1;
+    const int h = static_cast<int>(item / sw.row_tiles);
+    const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * kRows;
+    const int r = blockIdx.y * kAttnWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= min(kRows, sw.n * p.G - row_base)) return;
+    const int64_t step = static_cast<int64_t>(2) * p.slot_rows * (c.D + 2);
+    // part 0 is the second slot of this CTA, part i > 0 the first slot of CTA blockIdx.x + i
+    const float* first = p.parts + (static_cast<int64_t>(2 * blockIdx.x + 1) * p.slot_rows + r) *
+                                       (c.D + 2);
+    const float* rest = p.parts + (static_cast<int64_t>(2 * blockIdx.x) * p.slot_rows + r) *
+                                      (c.D + 2);
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, (i ? rest + i * step : first)[c.D]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float z = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, x[8] = {};
+    for (int i = 0; i < parts; ++i) {
+        const float* part = i ? rest + i * step : first;
+        const float w = part[c.D + 1] * ex2(part[c.D] - z);
+        l += w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int d = 2 * lane + 64 * j;
+            if (d >= c.D) break;
+            const float2 v = *reinterpret_cast<const float2*>(part + d);
+            x[2 * j] = fmaf(w, v.x, x[2 * j]);
+            x[2 * j + 1] = fmaf(w, v.y, x[2 * j + 1]);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int rr = row_base + r, tok = rr / p.G, head = h * p.G + rr - tok * p.G;
+    const int64_t row = static_cast<int64_t>(sw.first + tok) * c.Hq + head;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int d = 2 * lane + 64 * j;
+        if (d >= c.D) break;
+        *reinterpret_cast<__nv_bfloat162*>(p.out + row * c.D + d) =
+            __floats2bfloat162_rn(x[2 * j] * inv, x[2 * j + 1] * inv);
+    }
+    if (p.lse && lane == 0) p.lse[row] = lse_of(m, l);
 }
 
 template <int DP>
-int launch_attention(const AttnParams& p, unsigned units, cudaStream_t s)
+int launch_attention(const AttnParams& p, int sms, cudaStream_t s)
 {
-    static std::once_flag once[kMaxDevices];
+    // kernel attribute and CTAs per SM, once per device; 0 = not asked yet
+    static std::atomic<int> occupancy[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
-    cudaError_t e = cudaSuccess;
-    std::call_once(once[dev], [&] {
-        e = cudaFuncSetAttribute(fp8kv_attention_kernel<DP>,
+    int occ = occupancy[dev].load(std::memory_order_acquire);
+    if (occ == 0) {
+        if (cudaFuncSetAttribute(fp8kv_attention_kernel<DP>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(Dims<DP>::kSmem));
-    });
-    if (e != cudaSuccess) {
+                                 static_cast<int>(Dims<DP>::kSmem)) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fp8kv_attention_kernel<DP>,
+                                                          kAttnThreads,
+                                                          Dims<DP>::kSmem) != cudaSuccess ||
+            occ < 1) {
+            cudaGetLastError();
+            return BSP_ERR_CUDA;
+        }
+        occupancy[dev].store(occ, std::memory_order_release);
+    }
+    const unsigned ctas = static_cast<unsigned>(std::min(sms * occ, kMaxCtas));
+    if (launch_kernel(fp8kv_attention_kernel<DP>, ctas, kAttnThreads, Dims<DP>::kSmem, s, true,
+                      p) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
@@ -440,14 +682,12 @@ int launch_attention(const AttnParams& p, unsigned units, cudaStream_t s)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(units, static_cast<unsigned>(p.c.Hkv), 1);
-    cfg.blockDim = dim3(kAttnWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = Dims<DP>::kSmem;
+    cfg.gridDim = dim3(ctas, kRows / kAttnWarps, 1);
+    cfg.blockDim = dim3(kAttnThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fp8kv_attention_kernel<DP>, p);
-    if (e != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, fp8kv_join_kernel, p) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
@@ -463,7 +703,8 @@ int64_t fp8kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int6
 {
     if (T < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return BSP_ERR_INVALID_ARG;
     if (D % 16 != 0 || D > 256) return BSP_ERR_UNSUPPORTED_SHAPE;
-    return 16;
+    const int64_t rows = std::min<int64_t>(bsp::kRows, T * (Hq / Hkv));
+    return 2 * bsp::kMaxCtas * rows * (D + 2) * static_cast<int64_t>(sizeof(float));
 }
 
 int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache,
@@ -502,11 +743,12 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     p.window = window > (int64_t{1} << 30) ? 0 : static_cast<int32_t>(window);
     p.G = static_cast<int32_t>(Hq / Hkv);
     p.status = device_status_ptr(dev);
-    const unsigned units = static_cast<unsigned>(T * p.G / kRows + B);
+    p.parts = static_cast<float*>(workspace);
+    p.slot_rows = static_cast<int32_t>(std::min<int64_t>(kRows, T * p.G));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (D <= 64) return launch_attention<64>(p, units, s);
-    if (D <= 128) return launch_attention<128>(p, units, s);
-    return launch_attention<256>(p, units, s);
+    if (D <= 64) return launch_attention<64>(p, sms, s);
+    if (D <= 128) return launch_attention<128>(p, sms, s);
+    return launch_attention<256>(p, sms, s);
 }
 
 }  // extern "C"
