@@ -49,12 +49,7 @@ struct GemvParams {
     int32_t steps;            // of K in all
     int32_t cta_steps;        // of one CTA
     int32_t stage_steps;      // of x in shared memory at a time, even
-    int32_t wide;             // codes are 32-byte aligned
-};
-
-struct StepData {
-    uint4 c[4][2];            // 64 codes of each of four rows
-    uint4 s;                  // 4 scales of each
+    int32_t tiles, groups;    // row tiles, and clusters that share them
 };
 
 __device__ __forceinline__ float pow2_biased(int e)     // 2^(e - 127), e in [0, 254]
@@ -74,20 +69,21 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
         : "r"(w));
 }
 
-// four E4M3 scales -> each twice in an f16 pair
-__device__ __forceinline__ void scales_to_f16(uint32_t w, uint32_t (&h)[4])
+// the E4M3 scale in the low byte, twice in an f16 pair
+__device__ __forceinline__ uint32_t scale_to_f16(uint32_t w)
 {
-    uint32_t lo, hi;
+    uint32_t r;
     asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-    h[0] = __byte_perm(lo, lo, 0x1010);
-    h[1] = __byte_perm(lo, lo, 0x3232);
-    h[2] = __byte_perm(hi, hi, 0x1010);
-    h[3] = __byte_perm(hi, hi, 0x3232);
+        "mov.b32 {a, b}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+        : "=r"(r)
+        : "r"(__byte_perm(w, 0, 0x0000)));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word_of(uint4 v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
@@ -114,35 +110,94 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 
-// Codes and scales of step s for the warp's rows row0 + 32 q + g, q = 0 .. 3.
-__device__ __forceinline__ void load_step(const GemvParams& p, int s, int row0, int g, int t,
-                                          StepData& d)
+// A lane's loads of a step: half 0 or 1 of its 64 codes of the rows row + 32 q, and the four
+// scales of each.  Outside the weight they are zeros.
+__device__ __forceinline__ void load_codes(const GemvParams& p, int s, int row, int t, int half,
+                                           uint4 (&c)[4])
 {
     const int kt = s * 4 + t;
-    const bool in = kt * 64 < p.K;
-    const int64_t row_bytes = p.K / 2;
-    const int row = row0 + g;
+    const uint8_t* a = p.codes + static_cast<int64_t>(row) * (p.K / 2) + kt * 32 + 16 * half;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const bool ok = in && row + 32 * q < p.N;
-        const uint8_t* a = p.codes + (row + 32 * q) * row_bytes + kt * 32;
-        d.c[q][0] = d.c[q][1] = make_uint4(0, 0, 0, 0);
-        if (ok && p.wide) {
-            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(d.c[q][0].x), "=r"(d.c[q][0].y), "=r"(d.c[q][0].z),
-                           "=r"(d.c[q][0].w), "=r"(d.c[q][1].x), "=r"(d.c[q][1].y),
-                           "=r"(d.c[q][1].z), "=r"(d.c[q][1].w)
-                         : "l"(a));
-        } else if (ok) {
-            d.c[q][0] = __ldg(reinterpret_cast<const uint4*>(a));
-            d.c[q][1] = __ldg(reinterpret_cast<const uint4*>(a) + 1);
+        c[q] = make_uint4(0, 0, 0, 0);
+        if (kt * 64 < p.K && row + 32 * q < p.N)
+            c[q] = __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(16 * q) * p.K));
+    }
+}
+
+__device__ __forceinline__ uint4 load_scales(const GemvParams& p, int s, int row, int t)
+{
+    const int kt = s * 4 + t;
+    if (kt * 64 >= p.K) return make_uint4(0, 0, 0, 0);
+    return __ldg(reinterpret_cast<const uint4*>(
+        p.sf + (static_cast<int64_t>(row / kTileRows) * (p.K / 64) + kt) * 512 + (row & 31) * 16));
+}
+
+// Biased exponent that a row of x goes by: the row is multiplied by 2^(14 - (e - 127)).
+__device__ __forceinline__ int x_exponent(uint32_t amax_bits)
+{
+    return max(15, static_cast<int>(amax_bits >> 23));
+}
+
+// Steps [a0, a1) of x to shared memory in f16, in the order in which the products read them:
+// [x tile][step][eighth of a lane's 64 elements][lane quarter t][row].  amax: bits of the largest
+// |x| of each row so far.  Every thread calls; the stage is readable on return.
+template <int NT>
+__device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, int mp, uint4* xs,
+                                        uint32_t* amax)
+{
+    constexpr int kBatch = 4;                   // loads of a thread in flight
+    const int lane = threadIdx.x & 31;
+    const int rows = p.M <= 1 ? 1 : 1 << (32 - __clz(p.M - 1));     // a power of two
+    const int m = threadIdx.x & (rows - 1), first = threadIdx.x / rows, stride = kThreads / rows;
+    const int chunks = (a1 - a0) * (kStepK / 8), valid = p.K / 8 - a0 * (kStepK / 8);
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m) * p.K +
+                                                      static_cast<int64_t>(a0) * kStepK);
+    uint4 v[kBatch];
+    const auto load = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * stride;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (m < p.M && i < chunks && i < valid) v[j] = __ldg(src + i);
+        }
+    };
+    uint32_t top = 0;
+    for (int i0 = first; i0 < chunks; i0 += kBatch * stride) {
+        load(i0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint32_t a =
+                max_bf16x2(max_bf16x2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
+                           max_bf16x2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu));
+            top = max(top, max(a << 16, a & 0xFFFF0000u));
         }
     }
-    d.s = make_uint4(0, 0, 0, 0);
-    if (in)
-        d.s = __ldg(reinterpret_cast<const uint4*>(
-            p.sf + (static_cast<int64_t>(row / kTileRows) * (p.K / 64) + kt) * 512 +
-            (row & 31) * 16));
+    for (int o = 16; o >= rows; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (m < p.M && lane < rows) atomicMax(&amax[m], top);
+    __syncthreads();
+    if (m < p.M) {
+        const int e = x_exponent(amax[m]);
+        const float up = pow2_biased(268 - e);                 // 2^(14 - (e - 127))
+        const bool once = chunks <= kBatch * stride;           // still in registers
+        for (int i0 = first; i0 < chunks; i0 += kBatch * stride) {
+            if (!once) load(i0);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * stride;
+                if (i >= chunks) break;
+                uint4 h;
+                h.x = pack_f16(bf16lo_to_f32(v[j].x) * up, bf16hi_to_f32(v[j].x) * up);
+                h.y = pack_f16(bf16lo_to_f32(v[j].y) * up, bf16hi_to_f32(v[j].y) * up);
+                h.z = pack_f16(bf16lo_to_f32(v[j].z) * up, bf16hi_to_f32(v[j].z) * up);
+                h.w = pack_f16(bf16lo_to_f32(v[j].w) * up, bf16hi_to_f32(v[j].w) * up);
+                const int at = (((m >> 3) * p.stage_steps + (i >> 5)) * 8 + (i & 7)) * 4 +
+                               ((i >> 3) & 3);
+                xs[at * mp + (m & 7)] = h;
+            }
+        }
+    }
+    __syncthreads();
 }
 
 // NT: 8-row tiles of x.
@@ -161,119 +216,105 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
     uint32_t rank, pieces;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(pieces));
-    const int tile = blockIdx.x / pieces;
-    const int row0 = tile * kTileRows + oct * 8;
+    int tile = blockIdx.x / pieces;
     const int c0 = rank * p.cta_steps, c1 = min(c0 + p.cta_steps, p.steps);
 
-    StepData cur;
-    int s = c0 + kw;
-    if (s < c1) load_step(p, s, row0, g, t, cur);
+    // in registers: the codes of the step at hand in two halves, each replaced by the next
+    // step's as soon as it is used, and the scales
+    uint4 c[2][4], sf;
+    if (c0 + kw < c1) {
+        const int row = tile * kTileRows + oct * 8 + g;
+        load_codes(p, c0 + kw, row, t, 0, c[0]);
+        sf = load_scales(p, c0 + kw, row, t);
+        load_codes(p, c0 + kw, row, t, 1, c[1]);
+    }
+    if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
+    __syncthreads();
 
     const int mp = p.M < 8 ? p.M : 8;           // rows of an x tile in shared memory
-    const int rows_pow2 = p.M <= 1 ? 1 : 1 << (32 - __clz(p.M - 1));
-    const int xm = threadIdx.x & (rows_pow2 - 1), xc = threadIdx.x / rows_pow2;
-    const int xstep = kThreads / rows_pow2;
-    if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
+    const float gs = __ldg(p.scale);
 
+  for (; tile < p.tiles; tile += p.groups) {
+    const int row = tile * kTileRows + oct * 8 + g;
+    int s = c0 + kw;
     float acc[2][NT][4] = {};
-    int e_acc[NT][2];                           // biased exponents that the columns' sums go by
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) e_acc[nt][0] = e_acc[nt][1] = 15;
-
     for (int a0 = c0; a0 < c1; a0 += p.stage_steps) {
         const int a1 = min(a0 + p.stage_steps, c1);
-        const int chunks = (a1 - a0) * (kStepK / 8), valid = p.K / 8 - a0 * (kStepK / 8);
-        const uint4* xrow = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(xm) * p.K +
-                                                           static_cast<int64_t>(a0) * kStepK);
-        __syncthreads();                        // amax is set, the last stage is read
-        uint32_t top = 0;
-        if (xm < p.M)
-            for (int i = xc; i < min(chunks, valid); i += xstep) {
-                const uint4 v = __ldg(xrow + i);
-                const uint32_t a = max_bf16x2(max_bf16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                              max_bf16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-                top = max(top, max(a << 16, a & 0xFFFF0000u));
+        // x stays in shared memory from one tile to the next when its piece fits there
+        if (tile == static_cast<int>(blockIdx.x / pieces) || c1 - c0 > p.stage_steps) {
+            int e_old[NT][2];                   // biased exponents that the columns' sums go by
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    e_old[nt][i] = a0 == c0 ? 0 : x_exponent(amax[nt * 8 + 2 * t + i]);
+            __syncthreads();                    // the last stage and its exponents are read
+            if (a0 == c0 && tile != static_cast<int>(blockIdx.x / pieces)) {
+                if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
+                __syncthreads();
             }
-        for (int o = 16; o >= rows_pow2; o >>= 1)
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if (xm < p.M && lane < rows_pow2) atomicMax(&amax[xm], top);
-        __syncthreads();
-        if (xm < p.M) {
-            const int e = max(15, static_cast<int>(amax[xm] >> 23));
-            const float up = pow2_biased(268 - e);             // 2^(14 - (e - 127))
-            for (int i = xc; i < chunks; i += xstep) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (i < valid) v = __ldg(xrow + i);
-                uint4 h;
-                h.x = pack_f16(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up);
-                h.y = pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up);
-                h.z = pack_f16(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up);
-                h.w = pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up);
-                // chunk i: step i / 32, lane quarter (i / 8) % 4, eighth i % 8
-                const int at = (((xm >> 3) * p.stage_steps + (i >> 5)) * 8 + (i & 7)) * 4 +
-                               ((i >> 3) & 3);
-                xs[at * mp + (xm & 7)] = h;
+            stage_x<NT>(p, a0, a1, mp, xs, amax);
+            if (a0 != c0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int d = x_exponent(amax[nt * 8 + 2 * t + i]) - e_old[nt][i];
+                        const float f = d < 127 ? pow2_biased(127 - d) : 0.0f;
+                        acc[0][nt][i] *= f;
+                        acc[0][nt][i + 2] *= f;
+                        acc[1][nt][i] *= f;
+                        acc[1][nt][i + 2] *= f;
+                    }
             }
         }
-        // the sums so far move to this stage's exponents
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = max(15, static_cast<int>(amax[nt * 8 + 2 * t + i] >> 23));
-                const int d = e - e_acc[nt][i];
-                e_acc[nt][i] = e;
-                const float f = d < 127 ? pow2_biased(127 - d) : 0.0f;
-                acc[0][nt][i] *= f;
-                acc[0][nt][i + 2] *= f;
-                acc[1][nt][i] *= f;
-                acc[1][nt][i + 2] *= f;
-            }
-        __syncthreads();
 
         for (; s < a1; s += 2) {
-            StepData next;
-            if (s + 2 < c1) load_step(p, s + 2, row0, g, t, next);
-            uint32_t sc[4][4];
-            scales_to_f16(cur.s.x, sc[0]);
-            scales_to_f16(cur.s.y, sc[1]);
-            scales_to_f16(cur.s.z, sc[2]);
-            scales_to_f16(cur.s.w, sc[3]);
+            // the step after the last is the next tile's first
+            const bool wrap = s + 2 >= c1;
+            const int s_next = wrap ? c0 + kw : s + 2;
+            const int row_next = row + (wrap ? p.groups * kTileRows : 0);
+            const bool more = !wrap || tile + p.groups < p.tiles;
+            uint4 sf_next;
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
-                uint4 b[NT];
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int at = ((nt * p.stage_steps + (s - a0)) * 8 + jj) * 4 + t;
-                    b[nt] = make_uint4(0, 0, 0, 0);
-                    if (nt * 8 + g < p.M) b[nt] = xs[at * mp + g];
+                for (int j = 0; j < 4; ++j) {
+                    const int jj = 4 * half + j;
+                    uint4 b[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int at = ((nt * p.stage_steps + (s - a0)) * 8 + jj) * 4 + t;
+                        b[nt] = make_uint4(0, 0, 0, 0);
+                        if (nt * 8 + g < p.M) b[nt] = xs[at * mp + g];
+                    }
+                    uint32_t h[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t w = word_of(c[half][q], j);
+                        const uint32_t sc = scale_to_f16(word_of(sf, q) >> (8 * (jj >> 1)));
+                        e2m1x8_to_f16(w, h[q]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(acc[0][nt], h[0][0], h[1][0], h[0][1], h[1][1], b[nt].x, b[nt].y);
+                        mma_f16(acc[1][nt], h[2][0], h[3][0], h[2][1], h[3][1], b[nt].x, b[nt].y);
+                        mma_f16(acc[0][nt], h[0][2], h[1][2], h[0][3], h[1][3], b[nt].z, b[nt].w);
+                        mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
+                    }
                 }
-                uint32_t h[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 c = cur.c[q][jj >> 2];
-                    const uint32_t w = (jj & 3) == 0   ? c.x
-                                       : (jj & 3) == 1 ? c.y
-                                       : (jj & 3) == 2 ? c.z
-                                                       : c.w;
-                    e2m1x8_to_f16(w, h[q]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc[q][jj >> 1]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[0][nt], h[0][0], h[1][0], h[0][1], h[1][1], b[nt].x, b[nt].y);
-                    mma_f16(acc[1][nt], h[2][0], h[3][0], h[2][1], h[3][1], b[nt].x, b[nt].y);
-                    mma_f16(acc[0][nt], h[0][2], h[1][2], h[0][3], h[1][3], b[nt].z, b[nt].w);
-                    mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
+                if (more) {
+                    load_codes(p, s_next, row_next, t, half, c[half]);
+                    if (half == 0) sf_next = load_scales(p, s_next, row_next, t);
                 }
             }
-            cur = next;
+            sf = sf_next;
         }
     }
 
     // ---- sums of the two halves of the warps, then of the cluster's CTAs, in order
-    const float gs = __ldg(p.scale);
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
         if (kw == half) {
@@ -283,10 +324,11 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
                 for (int ta = 0; ta < 2; ++ta)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int row = oct * 8 + g + 64 * ta + 32 * (i >> 1);
+                        const int r = oct * 8 + g + 64 * ta + 32 * (i >> 1);
                         const int col = nt * 8 + 2 * t + (i & 1);
-                        const float v = acc[ta][nt][i] * gs * pow2_biased(e_acc[nt][i & 1] - 14);
-                        part[row][col] = half ? v : part[row][col] + v;
+                        const float v = acc[ta][nt][i] * gs *
+                                        pow2_biased(x_exponent(amax[col]) - 14);
+                        part[r][col] = half ? v : part[r][col] + v;
                     }
         }
         __syncthreads();
@@ -294,26 +336,31 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
     if (pieces > 1) cluster_sync();
     const int share = kTileRows / pieces;
     for (int i = threadIdx.x; i < share * p.M; i += kThreads) {
-        const int m = i / share, row = rank * share + i - m * share;
-        const int n = tile * kTileRows + row;
+        const int m = i / share, r = rank * share + i - m * share;
+        const int n = tile * kTileRows + r;
         if (n >= p.N) continue;
         float v = 0.0f;
         if (pieces == 1) {
-            v = part[row][m];
+            v = part[r][m];
         } else {
-            const uint32_t at = smem_u32(&part[row][m]);
-            for (uint32_t r = 0; r < pieces; ++r) {
+            const uint32_t at = smem_u32(&part[r][m]);
+            for (uint32_t j = 0; j < pieces; ++j) {
                 float y;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];"
                              : "=f"(y)
-                             : "r"(mapa_shared(at, r)));
+                             : "r"(mapa_shared(at, j)));
                 v += y;
             }
         }
         if (p.bias) v += __bfloat162float(p.bias[n]);
         p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(v);
     }
-    if (pieces > 1) cluster_sync();             // the others have read this CTA's sums
+    // the others have read this CTA's sums, before they are written again or the CTA ends
+    if (pieces > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+  }
 }
 
 template <int NT>
@@ -329,10 +376,21 @@ int launch_gemv(GemvParams p, int dev, int sms, cudaStream_t stream)
         }
         ready[dev].store(true, std::memory_order_release);
     }
-    // pieces of K: as many as give every SM two CTAs, while each has a step for both warp halves
-    const int tiles = (p.N + kTileRows - 1) / kTileRows;
+    // Pieces of K, and clusters ("groups") that take the row tiles in turn, two CTAs to an SM:
+    // the split whose busiest CTA has the least to do, counting one step for each tile's sums.
+    p.tiles = (p.N + kTileRows - 1) / kTileRows;
     int pieces = 1;
-    while (pieces < 8 && tiles * pieces < 2 * sms && pieces * 4 <= p.steps) pieces *= 2;
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= 8 && (c == 1 || 2 * c <= p.steps); c *= 2) {
+        const int groups = std::min(p.tiles, std::max(1, 2 * sms / c));
+        const int64_t cost = static_cast<int64_t>((p.tiles + groups - 1) / groups) *
+                             ((p.steps + c - 1) / c + 1);
+        if (cost < best) {
+            best = cost;
+            pieces = c;
+            p.groups = groups;
+        }
+    }
     p.cta_steps = (p.steps + pieces - 1) / pieces;
     const int step_bytes = kStepBytes * (p.M < 8 ? p.M : 8 * NT);
     p.stage_steps = std::min((p.cta_steps + 1) / 2 * 2, kMaxStage / step_bytes / 2 * 2);
@@ -344,7 +402,7 @@ int launch_gemv(GemvParams p, int dev, int sms, cudaStream_t stream)
     attr[1].val.clusterDim.x = pieces;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles) * pieces, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * pieces, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(p.stage_steps) * step_bytes;
     cfg.stream = stream;
@@ -388,7 +446,6 @@ extern "C" int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.steps = static_cast<int32_t>((K + kStepK - 1) / kStepK);
-    p.wide = (reinterpret_cast<uintptr_t>(w_codes) & 31u) == 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (M <= 8) return launch_gemv<1>(p, dev, sms, s);
     if (M <= 16) return launch_gemv<2>(p, dev, sms, s);
