@@ -69,15 +69,15 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
         : "r"(w));
 }
 
-// the E4M3 scale in the low byte, twice in an f16 pair
-__device__ __forceinline__ uint32_t scale_to_f16(uint32_t w)
+// the E4M3 scale in byte i of w, twice in an f16 pair
+__device__ __forceinline__ uint32_t scale_to_f16(uint32_t w, int i)
 {
     uint32_t r;
     asm("{\n\t.reg .b16 a, b;\n\t"
         "mov.b32 {a, b}, %1;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
         : "=r"(r)
-        : "r"(__byte_perm(w, 0, 0x0000)));
+        : "r"(__byte_perm(w, 0, i * 0x11)));
     return r;
 }
 
@@ -110,27 +110,52 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 
-// A lane's loads of a step: half 0 or 1 of its 64 codes of the rows row + 32 q, and the four
-// scales of each.  Outside the weight they are zeros.
-__device__ __forceinline__ void load_codes(const GemvParams& p, int s, int row, int t, int half,
-                                           uint4 (&c)[4])
+// A lane's loads of half a step (128 elements of K): 32 codes of each of its four rows, at t * 32
+// of the half, so that four lanes read 64 bytes of a row side by side; and the 16 scales of those
+// rows and the 64 elements that hold the lane's two blocks.  Rows past N and elements past K are
+// read from the last ones instead: the results of such rows are not stored, and x is zero there.
+struct HalfStep {
+    uint4 c[4];
+    uint4 s;                  // word q: row + 32 q
+};
+
+struct LaneRows {
+    const uint8_t* codes;     // of the lane's first row
+    const uint8_t* sf;
+    uint32_t off[3];          // from there to the other rows' codes
+};
+
+__device__ __forceinline__ uint4 ldg_once(const void* a)
 {
-    const int kt = s * 4 + t;
-    const uint8_t* a = p.codes + static_cast<int64_t>(row) * (p.K / 2) + kt * 32 + 16 * half;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        c[q] = make_uint4(0, 0, 0, 0);
-        if (kt * 64 < p.K && row + 32 * q < p.N)
-            c[q] = __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(16 * q) * p.K));
-    }
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(a));
+    return v;
 }
 
-__device__ __forceinline__ uint4 load_scales(const GemvParams& p, int s, int row, int t)
+__device__ __forceinline__ LaneRows lane_rows(const GemvParams& p, int tile, int row_in_tile)
 {
-    const int kt = s * 4 + t;
-    if (kt * 64 >= p.K) return make_uint4(0, 0, 0, 0);
-    return __ldg(reinterpret_cast<const uint4*>(
-        p.sf + (static_cast<int64_t>(row / kTileRows) * (p.K / 64) + kt) * 512 + (row & 31) * 16));
+    LaneRows r;
+    const int row = min(tile * kTileRows + row_in_tile, p.N - 1);
+    r.codes = p.codes + static_cast<int64_t>(row) * (p.K / 2);
+#pragma unroll
+    for (int q = 1; q < 4; ++q)
+        r.off[q - 1] = static_cast<uint32_t>(min(row + 32 * q, p.N - 1) - row) * (p.K / 2);
+    r.sf = p.sf + static_cast<int64_t>(tile) * (p.K / 64) * 512 + row_in_tile * 16;
+    return r;
+}
+
+__device__ __forceinline__ void load_half(const GemvParams& p, const LaneRows& r, int s, int t,
+                                          int half, HalfStep& d)
+{
+    const uint32_t kt = min(s * 4 + 2 * half + (t >> 1), p.K / 64 - 1);
+    const uint8_t* a = r.codes + (kt * 32 + (t & 1) * 16);
+    d.c[0] = ldg_once(a);
+    d.c[1] = ldg_once(a + r.off[0]);
+    d.c[2] = ldg_once(a + r.off[1]);
+    d.c[3] = ldg_once(a + r.off[2]);
+    d.s = __ldg(reinterpret_cast<const uint4*>(r.sf + kt * 512));
 }
 
 // Biased exponent that a row of x goes by: the row is multiplied by 2^(14 - (e - 127)).
@@ -139,62 +164,71 @@ __device__ __forceinline__ int x_exponent(uint32_t amax_bits)
     return max(15, static_cast<int>(amax_bits >> 23));
 }
 
-// Steps [a0, a1) of x to shared memory in f16, in the order in which the products read them:
-// [x tile][step][eighth of a lane's 64 elements][lane quarter t][row].  amax: bits of the largest
-// |x| of each row so far.  Every thread calls; the stage is readable on return.
-template <int NT>
-__device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, int mp, uint4* xs,
-                                        uint32_t* amax)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
 {
-    constexpr int kBatch = 4;                   // loads of a thread in flight
-    const int lane = threadIdx.x & 31;
-    const int rows = p.M <= 1 ? 1 : 1 << (32 - __clz(p.M - 1));     // a power of two
-    const int m = threadIdx.x & (rows - 1), first = threadIdx.x / rows, stride = kThreads / rows;
-    const int chunks = (a1 - a0) * (kStepK / 8), valid = p.K / 8 - a0 * (kStepK / 8);
-    const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m) * p.K +
-                                                      static_cast<int64_t>(a0) * kStepK);
-    uint4 v[kBatch];
-    const auto load = [&](int i0) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * stride;
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (m < p.M && i < chunks && i < valid) v[j] = __ldg(src + i);
-        }
-    };
-    uint32_t top = 0;
-    for (int i0 = first; i0 < chunks; i0 += kBatch * stride) {
-        load(i0);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const uint32_t a =
-                max_bf16x2(max_bf16x2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
-                           max_bf16x2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu));
-            top = max(top, max(a << 16, a & 0xFFFF0000u));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+
+// Steps [a0, a1) of x to shared memory in f16, rows row_bytes apart; beyond K it is zeros.  Of the
+// 32 16-byte chunks of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped: with
+// that the eight lanes of one shared memory read (four t, two g) are in different banks.  amax:
+// bits of the largest |x| of each row so far.  A warp takes one step of one row at a time and
+// copies all of its own first, so that their latencies overlap; a lane touches no other's.
+// Every thread calls; the stage is readable on return.
+__device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uint4* xs,
+                                        int row_bytes, uint32_t* amax)
+{
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int steps = a1 - a0;
+    uint8_t* base = reinterpret_cast<uint8_t*>(xs) + (lane ^ ((lane >> 3) & 1)) * 16;
+    // units (row m, step s) go to the warps in turn
+    const int m0 = warp / steps, s0 = warp - m0 * steps;
+    const int dm = kWarps / steps, ds = kWarps - dm * steps;
+    for (int m = m0, s = s0; m < p.M;) {
+        const int k = (a0 + s) * kStepK + lane * 8;
+        const bool in = k < p.K;
+        cp_async16(smem_u32(base + m * row_bytes + s * kStepBytes),
+                   p.x + (in ? static_cast<int64_t>(m) * p.K + k : 0), in);
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
         }
     }
-    for (int o = 16; o >= rows; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (m < p.M && lane < rows) atomicMax(&amax[m], top);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int m = m0, s = s0; m < p.M;) {
+        const uint4 v = *reinterpret_cast<const uint4*>(base + m * row_bytes + s * kStepBytes);
+        const uint32_t a = max_bf16x2(max_bf16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                      max_bf16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(a << 16, a & 0xFFFF0000u));
+        if (lane == 0) atomicMax(&amax[m], top);
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
+        }
+    }
     __syncthreads();
-    if (m < p.M) {
-        const int e = x_exponent(amax[m]);
-        const float up = pow2_biased(268 - e);                 // 2^(14 - (e - 127))
-        const bool once = chunks <= kBatch * stride;           // still in registers
-        for (int i0 = first; i0 < chunks; i0 += kBatch * stride) {
-            if (!once) load(i0);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int i = i0 + j * stride;
-                if (i >= chunks) break;
-                uint4 h;
-                h.x = pack_f16(bf16lo_to_f32(v[j].x) * up, bf16hi_to_f32(v[j].x) * up);
-                h.y = pack_f16(bf16lo_to_f32(v[j].y) * up, bf16hi_to_f32(v[j].y) * up);
-                h.z = pack_f16(bf16lo_to_f32(v[j].z) * up, bf16hi_to_f32(v[j].z) * up);
-                h.w = pack_f16(bf16lo_to_f32(v[j].w) * up, bf16hi_to_f32(v[j].w) * up);
-                const int at = (((m >> 3) * p.stage_steps + (i >> 5)) * 8 + (i & 7)) * 4 +
-                               ((i >> 3) & 3);
-                xs[at * mp + (m & 7)] = h;
-            }
+    for (int m = m0, s = s0; m < p.M;) {
+        uint4* at = reinterpret_cast<uint4*>(base + m * row_bytes + s * kStepBytes);
+        const float up = pow2_biased(268 - x_exponent(amax[m]));     // 2^(14 - (e - 127))
+        const uint4 v = *at;
+        uint4 h;
+        h.x = pack_f16(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up);
+        h.y = pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up);
+        h.z = pack_f16(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up);
+        h.w = pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up);
+        *at = h;
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
         }
     }
     __syncthreads();
@@ -204,8 +238,8 @@ __device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, int
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParams p)
 {
-    extern __shared__ uint4 xs[];               // x in f16: [nt][step][8][t][rows of the tile]
-    __shared__ float part[kTileRows][NT * 8];
+    extern __shared__ uint4 xs[];               // x in f16
+    __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
     __shared__ uint32_t amax[NT * 8];           // bits of the largest |x| of this piece so far
     griddep_wait();
     griddep_launch_dependents();
@@ -219,23 +253,28 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
     int tile = blockIdx.x / pieces;
     const int c0 = rank * p.cta_steps, c1 = min(c0 + p.cta_steps, p.steps);
 
-    // in registers: the codes of the step at hand in two halves, each replaced by the next
-    // step's as soon as it is used, and the scales
-    uint4 c[2][4], sf;
+    // in registers: the two halves of the step at hand, each replaced by the next step's as soon
+    // as it is used
+    HalfStep w[2];
+    LaneRows rows = lane_rows(p, tile, oct * 8 + g);
     if (c0 + kw < c1) {
-        const int row = tile * kTileRows + oct * 8 + g;
-        load_codes(p, c0 + kw, row, t, 0, c[0]);
-        sf = load_scales(p, c0 + kw, row, t);
-        load_codes(p, c0 + kw, row, t, 1, c[1]);
+        load_half(p, rows, c0 + kw, t, 0, w[0]);
+        load_half(p, rows, c0 + kw, t, 1, w[1]);
     }
     if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
     __syncthreads();
 
-    const int mp = p.M < 8 ? p.M : 8;           // rows of an x tile in shared memory
+    // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
+    // Rows of a tile past M read the last row; their columns are not stored.
+    const int row_bytes = p.stage_steps * kStepBytes + 32;
+    const uint8_t* xg[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, p.M - 1) * row_bytes + t * 64;
+    const int swap = (t >> 1) * 16;
     const float gs = __ldg(p.scale);
 
   for (; tile < p.tiles; tile += p.groups) {
-    const int row = tile * kTileRows + oct * 8 + g;
     int s = c0 + kw;
     float acc[2][NT][4] = {};
     for (int a0 = c0; a0 < c1; a0 += p.stage_steps) {
@@ -253,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
                 if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
                 __syncthreads();
             }
-            stage_x<NT>(p, a0, a1, mp, xs, amax);
+            stage_x(p, a0, a1, xs, row_bytes, amax);
             if (a0 != c0) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -273,27 +312,25 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
             // the step after the last is the next tile's first
             const bool wrap = s + 2 >= c1;
             const int s_next = wrap ? c0 + kw : s + 2;
-            const int row_next = row + (wrap ? p.groups * kTileRows : 0);
             const bool more = !wrap || tile + p.groups < p.tiles;
-            uint4 sf_next;
+            if (wrap && more) rows = lane_rows(p, tile + p.groups, oct * 8 + g);
+            const int xo = (s - a0) * kStepBytes;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int jj = 4 * half + j;
                     uint4 b[NT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int at = ((nt * p.stage_steps + (s - a0)) * 8 + jj) * 4 + t;
-                        b[nt] = make_uint4(0, 0, 0, 0);
-                        if (nt * 8 + g < p.M) b[nt] = xs[at * mp + g];
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        b[nt] = *reinterpret_cast<const uint4*>(
+                            xg[nt] + xo + half * 256 + ((j * 16) ^ swap));
                     uint32_t h[4][4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t w = word_of(c[half][q], j);
-                        const uint32_t sc = scale_to_f16(word_of(sf, q) >> (8 * (jj >> 1)));
-                        e2m1x8_to_f16(w, h[q]);
+                        // scale byte 2 (t % 2) + j / 2 of the row's word
+                        const uint32_t sc =
+                            scale_to_f16(word_of(w[half].s, q), (t & 1) * 2 + (j >> 1));
+                        e2m1x8_to_f16(word_of(w[half].c[q], j), h[q]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc);
                     }
@@ -305,12 +342,8 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
                         mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
                     }
                 }
-                if (more) {
-                    load_codes(p, s_next, row_next, t, half, c[half]);
-                    if (half == 0) sf_next = load_scales(p, s_next, row_next, t);
-                }
+                if (more) load_half(p, rows, s_next, t, half, w[half]);
             }
-            sf = sf_next;
         }
     }
 
@@ -328,32 +361,35 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParam
                         const int col = nt * 8 + 2 * t + (i & 1);
                         const float v = acc[ta][nt][i] * gs *
                                         pow2_biased(x_exponent(amax[col]) - 14);
-                        part[r][col] = half ? v : part[r][col] + v;
+                        part[col][r] = half ? v : part[col][r] + v;
                     }
         }
         __syncthreads();
     }
     if (pieces > 1) cluster_sync();
+    // a thread keeps its row n: 128 / pieces rows, and every (kThreads / that)-th row of x
     const int share = kTileRows / pieces;
-    for (int i = threadIdx.x; i < share * p.M; i += kThreads) {
-        const int m = i / share, r = rank * share + i - m * share;
-        const int n = tile * kTileRows + r;
-        if (n >= p.N) continue;
-        float v = 0.0f;
+    const int r = rank * share + (threadIdx.x & (share - 1)), n = tile * kTileRows + r;
+    const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f;
+    for (int m = threadIdx.x / share; m < p.M; m += kThreads / share) {
+        if (n >= p.N) break;
+        float v;
         if (pieces == 1) {
-            v = part[r][m];
+            v = part[m][r];
         } else {
-            const uint32_t at = smem_u32(&part[r][m]);
-            for (uint32_t j = 0; j < pieces; ++j) {
-                float y;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                             : "=f"(y)
-                             : "r"(mapa_shared(at, j)));
-                v += y;
+            const uint32_t at = smem_u32(&part[m][r]);
+            float y[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                y[j] = 0.0f;
+                if (j < pieces)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(y[j])
+                                 : "r"(mapa_shared(at, j)));
             }
+            v = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
         }
-        if (p.bias) v += __bfloat162float(p.bias[n]);
-        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(v);
+        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(v + bias);
     }
     // the others have read this CTA's sums, before they are written again or the CTA ends
     if (pieces > 1)
@@ -377,14 +413,17 @@ int launch_gemv(GemvParams p, int dev, int sms, cudaStream_t stream)
         ready[dev].store(true, std::memory_order_release);
     }
     // Pieces of K, and clusters ("groups") that take the row tiles in turn, two CTAs to an SM:
-    // the split whose busiest CTA has the least to do, counting one step for each tile's sums.
+    // the split whose busiest CTA has the least to do.  Counted in instructions of a warp: 200 (and
+    // 32 for each 8 rows of x) for a CTA's step, as much again for the sums of a tile, and 10 for
+    // bringing one row's step of x to shared memory, once.
     p.tiles = (p.N + kTileRows - 1) / kTileRows;
     int pieces = 1;
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8 && (c == 1 || 2 * c <= p.steps); c *= 2) {
         const int groups = std::min(p.tiles, std::max(1, 2 * sms / c));
-        const int64_t cost = static_cast<int64_t>((p.tiles + groups - 1) / groups) *
-                             ((p.steps + c - 1) / c + 1);
+        const int64_t steps = (p.steps + c - 1) / c;
+        const int64_t cost = (p.tiles + groups - 1) / groups * (steps + 1) * (200 + 32 * NT) +
+                             steps * p.M * 10;
         if (cost < best) {
             best = cost;
             pieces = c;
@@ -392,8 +431,8 @@ int launch_gemv(GemvParams p, int dev, int sms, cudaStream_t stream)
         }
     }
     p.cta_steps = (p.steps + pieces - 1) / pieces;
-    const int step_bytes = kStepBytes * (p.M < 8 ? p.M : 8 * NT);
-    p.stage_steps = std::min((p.cta_steps + 1) / 2 * 2, kMaxStage / step_bytes / 2 * 2);
+    p.stage_steps = std::min((p.cta_steps + 1) / 2 * 2,
+                             (kMaxStage / p.M - 32) / kStepBytes / 2 * 2);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -404,7 +443,7 @@ int launch_gemv(GemvParams p, int dev, int sms, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * pieces, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.stage_steps) * step_bytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * (p.stage_steps * kStepBytes + 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
