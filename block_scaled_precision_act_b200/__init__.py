@@ -23,7 +23,7 @@ __all__ = [
     "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_quant", "fp8r_quantize_rows", "fp8r_gemm",
     "nvfp4_linear", "nvfp4_linear_dynamic", "nvfp4_linear_workspace_bytes", "nvfp4_linear_noalloc",
     "nvfp4_linear_noalloc_max_bytes", "fp8r_linear", "fp8r_linear_workspace_bytes",
-    "nvfp4_gemv", "fp8kv_append", "fp8kv_attention", "fp8kv_attention_workspace_bytes",
+    "nvfp4_gemv", "nvfp4_gemv_workspace_bytes", "fp8kv_append", "fp8kv_attention", "fp8kv_attention_workspace_bytes",
     "nvfp4_global_scale", "nvfp4_sf_convert", "nvfp4_sf_bytes", "nvfp4_dequantize",
     "bsp_last_device_status", "bsp_set_wait_limit_ms", "bsp_status_string", "bsp_version",
     "bsp_testing_gemm_stall", "bsp_testing_set_gemm_kernel", "bsp_testing_set_quant_kernel",
@@ -60,8 +60,9 @@ _SIGS = {
     "fp8r_linear_workspace_bytes": ([_c_i64, _c_i64], _c_i64),
     "fp8r_gemm": ([_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
                   _c_int),
-    "nvfp4_gemv": ([_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
-                   _c_int),
+    "nvfp4_gemv": ([_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp,
+                    _c_i64, _c_vp], _c_int),
+    "nvfp4_gemv_workspace_bytes": ([_c_i64, _c_i64, _c_i64], _c_i64),
     "fp8kv_append": ([_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_int,
                       ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp,
                       _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp],
@@ -394,18 +395,32 @@ def fp8r_gemm(a_q, a_row_scale, w_q, w_row_scale, bias=None, out=None, stream=No
     return out
 
 
-def nvfp4_gemv(x: torch.Tensor, w_codes, w_sf, w_scale, bias=None, out=None, stream=None):
-    """Y[M, N] bf16 = x [M, K] times an NVFP4 weight (operands as nvfp4_gemm's), x kept in
-    bf16: the weight-only form for 1 to 32 rows."""
+def nvfp4_gemv_workspace_bytes(M: int, N: int, K: int) -> int:
+    n = lib().nvfp4_gemv_workspace_bytes(M, N, K)
+    if n < 0:
+        raise BSPError("nvfp4_gemv_workspace_bytes", int(n))
+    return int(n)
+
+
+def nvfp4_gemv(x: torch.Tensor, w_codes, w_sf, w_scale, bias=None, out=None, workspace=None,
+               stream=None):
+    """Y[M, N] bf16 = x [M, K] times an NVFP4 weight (operands as nvfp4_gemm's), x not quantized:
+    the weight-only form for 1 to 32 rows.  `workspace` (uint8, at least
+    nvfp4_gemv_workspace_bytes(M, N, K) bytes) is allocated here when not given."""
     M, K = _mat(x, torch.bfloat16, "x")
     N, _ = _mat(w_codes, torch.uint8, "w_codes", K // 2)
     _nvfp4_operands(0, N, K, None, None, w_sf, w_scale, bias)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _buf(out, torch.bfloat16, "out", M * N)
+    if workspace is None:
+        workspace = torch.empty((nvfp4_gemv_workspace_bytes(M, N, K),), dtype=torch.uint8,
+                                device=x.device)
+    _buf(workspace, torch.uint8, "workspace", 0)
     _check("nvfp4_gemv",
            lib().nvfp4_gemv(_ptr(x), _ptr(w_codes), _ptr(w_sf), _ptr(w_scale), _ptr(bias),
-                            _ptr(out), M, N, K, _stream(stream)))
+                            _ptr(out), M, N, K, _ptr(workspace), workspace.numel(),
+                            _stream(stream)))
     return out
 
 

@@ -3,6 +3,7 @@
 
 #include <cstdint>
 #include <utility>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "bsp.h"
@@ -21,6 +22,11 @@ int* device_status_ptr(int device);
 
 // Bounded-wait limit for kernels, in nanoseconds.
 uint64_t wait_limit_ns();
+
+// Tensor map of a 2-D byte tensor [rows][row_bytes] with boxes of box_rows x 128 bytes in the
+// 128-byte swizzle.
+int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+                  uint32_t box_rows);
 
 // nvfp4_gemm (nvf4) / fp8r_gemm launched right after the library's activation quantizer
 // wrote `a` (and `a_sf`): same results, but the weight operand's first stages are fetched

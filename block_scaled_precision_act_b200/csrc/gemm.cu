@@ -1405,6 +1405,13 @@ int gemm_entry(bool nvf4, const uint8_t* a, const uint8_t* sfa, const float* a_s
 
 }  // namespace
 
+int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+                  uint32_t box_rows)
+{
+    return make_map(m, base, row_bytes, rows, box_rows);
+}
+
+
 int gemm_after_quantizer(bool nvf4, const uint8_t* a, const uint8_t* a_sf, const float* a_scale,
                          const uint8_t* w, const uint8_t* w_sf, const float* w_scale,
                          const void* bias_bf16, void* out_bf16, int64_t M, int64_t N, int64_t K,

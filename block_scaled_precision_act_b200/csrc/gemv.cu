@@ -1,23 +1,28 @@
 // gemv.cu -- nvfp4_gemv: y[m][n] = bf16(g * sum_k x[m][k] w[n][k] + bias[n]) for a few rows of
-// bf16 x, w = e2m1(code) * e4m3(scale) in the layout of nvfp4_gemm.  The weight-only form:
-// x is not quantized.
+// bf16 x, w = e2m1(code) * e4m3(scale) in the layout of nvfp4_gemm.  The weight-only form.
 //
-// What bounds it is reading the weight: 9/16 byte per weight.  Decoding 16 weights costs the
-// CUDA cores 8 conversions and 8 products with the scale if the multiply-adds are left to the
-// tensor cores, and several times the budget if they are not, so each weight becomes f16 (e2m1 *
-// e4m3 has at most 6 significant bits and lies in [2^-10, 2688]: exact) and goes through
-// m16n8k16 with fp32 sums, 16 weight rows against 8 rows of x.  x is bf16, whose range f16 lacks:
-// it is scaled by a power of two per row of x and piece of K, so that its largest element is in
-// [2^14, 2^15); f16 then holds elements down to 2^-28 of that exactly and rounds smaller ones by
-// at most 2^-39 of it.
+// What bounds it is reading the weight, 9/16 byte for each.  Decoded by the CUDA cores, a weight
+// costs a conversion, a product with its scale and its share of the products with x: at 16 rows
+// that took 2.7 times as long as the reading.  So no CUDA core touches the weight: it goes from
+// global memory to shared memory and into tcgen05.mma kind::mxf4nvf4 as it is stored, as the M = 128
+// operand, and x is made to fit the other operand instead, as a sum of seven E2M1 rows:
+//     x[m][k] = rho_m * sum_i 2^(q_i) e2m1(c_i[m][k]),    q = 0, -2, -5, -8, -11, -14, -17,
+// rho_m the smallest power of two with |x[m][.]| <= 6 rho_m.  A term takes the nearest code of what
+// the terms before it left:
+//     term 1: |r| <= 6 leaves at most 1 (codes are 2 apart above 4) = 4 * 2^-2;
+//     term 2: |r| <= 4 units leaves at most half a unit (codes are at most 1 apart up to 4),
+//             2^-3 = 4 * 2^-5, and so on: 2^-18 after term 7, while the row's largest is above 3.
+// So x is held to 2^-19.5 of the largest of its row (bf16 has 2^-8 of the element).  The scale
+// vector of that operand is 1 throughout (it is laid down in tensor memory once, where loading one for
+// each stage cost the issuing thread 430 cycles of a budget of 790), and the epilogue adds the seven
+// columns of a row with their powers of two, smallest first.
 //
-// One CTA takes a 128-row tile of the weight (the tile of the scale layout) and a piece of K.  A
-// warp takes the 32 rows r, r + 32, r + 64, r + 96 for 8 values of r, whose scales lie in the same
-// 16-byte words, and every other 256-element step of K: per step a lane reads 32 bytes of codes of
-// each of its four rows and one 16-byte word of scales, all of which it uses.  The products may run
-// over k in any order, so these 64 consecutive codes of a row are the k slots that the lane owns
-// in 16 products.  The next step's loads are in flight while a step is computed.  The pieces of K
-// are a cluster: the CTAs add their sums through distributed shared memory, in order.
+// Two kernels.  nvfp4_gemv_split_kernel writes the seven rows of each x row to the workspace, in the
+// order in which shared memory will hold them.  nvfp4_gemv_kernel, one CTA per SM: the 256-element
+// K stages of all 128-row tiles in a row are cut into equal runs, one for each CTA, so that every SM
+// reads the same number of bytes whatever N and K are; a tile that is cut leaves fp32 parts, and the
+// last CTA to finish one adds them in order.  Its producer fills the ring with weights before the
+// split kernel has ended (that kernel begins only when everything before this call has).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,462 +37,571 @@ namespace bsp {
 namespace {
 
 constexpr int kGemvMaxRows = 32;
-constexpr int kThreads = 256;
+constexpr int kTerms = 7;
 constexpr int kTileRows = 128;
-constexpr int kStepK = 256;
-constexpr int kStepBytes = kStepK * 2;          // of one row of x in f16
-constexpr int kMaxStage = 96 * 1024;            // shared memory for x: two CTAs fit an SM
+constexpr int kStageK = 256;
+constexpr int kABytes = kTileRows * kStageK / 2;
+constexpr int kSfBytes = 4 * 512;                // scales of 128 rows and one stage
+constexpr int kMaxStages = 8;
+constexpr int kMaxCtas = 160;
+constexpr int kThreads = 224;                    // producer, MMA issuer, four epilogue warps, issuer
+constexpr int kRingBytes = 224 * 1024;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kAccCols = 448;                    // of the accumulators; then the scales
+constexpr int kSfaCol = kAccCols, kSfbCol = kSfaCol + 32;
+constexpr int kPoison = 0x7FFFFFFF;              // exponent of a row that is not finite
 
-struct GemvParams {
-    const __nv_bfloat16* x;
-    const uint8_t* codes;
-    const uint8_t* sf;
-    const float* scale;
+__host__ __device__ constexpr int term_exp(int i) { return i == 0 ? 0 : 1 - 3 * i; }
+
+struct GemvArgs {
+    const uint8_t* sfa;
+    const float* w_scale;
     const __nv_bfloat16* bias;
     __nv_bfloat16* out;
+    const uint8_t* xc;           // [stages of K][nb rows][128 bytes], swizzled
+    const int32_t* rho;          // [M] exponent of a row's power of two, or kPoison
+    float* parts;                // [2 * ctas][M][128]
+    int32_t* done;               // [tiles][4] parts that have arrived, zeroed by the split kernel
     int32_t M, N, K;
-    int32_t steps;            // of K in all
-    int32_t cta_steps;        // of one CTA
-    int32_t stage_steps;      // of x in shared memory at a time, even
-    int32_t tiles, groups;    // row tiles, and clusters that share them
+    int32_t mp;                  // rows of x rounded up to 8
+    int32_t nb;                  // 7 mp rounded up to 16: rows of the second operand
+    int32_t num_kt;
+    int32_t stages;              // of the ring
+    int64_t total;               // K stages of all tiles
+    uint64_t wait_ns;
+    int* status;
 };
 
-__device__ __forceinline__ float pow2_biased(int e)     // 2^(e - 127), e in [0, 254]
-{
-    return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
-}
-
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
-{
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-
-// the E4M3 scale in byte i of w, twice in an f16 pair
-__device__ __forceinline__ uint32_t scale_to_f16(uint32_t w, int i)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
-        : "=r"(r)
-        : "r"(__byte_perm(w, 0, i * 0x11)));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t word_of(uint4 v, int i)
-{
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8])
 {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr));
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+// 2^e as a float, e in [-126, 127]
+__device__ __forceinline__ float exp2_int(int e)
 {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// A lane's loads of half a step (128 elements of K): 32 codes of each of its four rows, at t * 32
-// of the half, so that four lanes read 64 bytes of a row side by side; and the 16 scales of those
-// rows and the 64 elements that hold the lane's two blocks.  Rows past N and elements past K are
-// read from the last ones instead: the results of such rows are not stored, and x is zero there.
-struct HalfStep {
-    uint4 c[4];
-    uint4 s;                  // word q: row + 32 q
-};
-
-struct LaneRows {
-    const uint8_t* codes;     // of the lane's first row
-    const uint8_t* sf;
-    uint32_t off[3];          // from there to the other rows' codes
-};
-
-__device__ __forceinline__ uint4 ldg_once(const void* a)
+// ceil(log2(v / 6)) of a positive normal v
+__device__ __forceinline__ int log2_over_6(float v)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(a));
-    return v;
+    const uint32_t b = __float_as_uint(v);
+    return static_cast<int>(b >> 23) - 127 - 2 + ((b & 0x7FFFFFu) > 0x400000u);
 }
 
-__device__ __forceinline__ LaneRows lane_rows(const GemvParams& p, int tile, int row_in_tile)
+// Sixteen codes of r / 2^q (element 2j in the low nibble), and r minus what they stand for.
+__device__ __forceinline__ uint2 take_term(float (&r)[16], int q)
 {
-    LaneRows r;
-    const int row = min(tile * kTileRows + row_in_tile, p.N - 1);
-    r.codes = p.codes + static_cast<int64_t>(row) * (p.K / 2);
+    const float down = exp2_int(-q), up = exp2_int(q);
+    uint2 w;
 #pragma unroll
-    for (int q = 1; q < 4; ++q)
-        r.off[q - 1] = static_cast<uint32_t>(min(row + 32 * q, p.N - 1) - row) * (p.K / 2);
-    r.sf = p.sf + static_cast<int64_t>(tile) * (p.K / 64) * 512 + row_in_tile * 16;
-    return r;
-}
-
-__device__ __forceinline__ void load_half(const GemvParams& p, const LaneRows& r, int s, int t,
-                                          int half, HalfStep& d)
-{
-    const uint32_t kt = min(s * 4 + 2 * half + (t >> 1), p.K / 64 - 1);
-    const uint8_t* a = r.codes + (kt * 32 + (t & 1) * 16);
-    d.c[0] = ldg_once(a);
-    d.c[1] = ldg_once(a + r.off[0]);
-    d.c[2] = ldg_once(a + r.off[1]);
-    d.c[3] = ldg_once(a + r.off[2]);
-    d.s = __ldg(reinterpret_cast<const uint4*>(r.sf + kt * 512));
-}
-
-// Biased exponent that a row of x goes by: the row is multiplied by 2^(14 - (e - 127)).
-__device__ __forceinline__ int x_exponent(uint32_t amax_bits)
-{
-    return max(15, static_cast<int>(amax_bits >> 23));
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
-
-// Steps [a0, a1) of x to shared memory in f16, rows row_bytes apart; beyond K it is zeros.  Of the
-// 32 16-byte chunks of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped: with
-// that the eight lanes of one shared memory read (four t, two g) are in different banks.  amax:
-// bits of the largest |x| of each row so far.  A warp takes one step of one row at a time and
-// copies all of its own first, so that their latencies overlap; a lane touches no other's.
-// Every thread calls; the stage is readable on return.
-__device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uint4* xs,
-                                        int row_bytes, uint32_t* amax)
-{
-    constexpr int kWarps = kThreads / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int steps = a1 - a0;
-    uint8_t* base = reinterpret_cast<uint8_t*>(xs) + (lane ^ ((lane >> 3) & 1)) * 16;
-    // units (row m, step s) go to the warps in turn
-    const int m0 = warp / steps, s0 = warp - m0 * steps;
-    const int dm = kWarps / steps, ds = kWarps - dm * steps;
-    for (int m = m0, s = s0; m < p.M;) {
-        const int k = (a0 + s) * kStepK + lane * 8;
-        const bool in = k < p.K;
-        cp_async16(smem_u32(base + m * row_bytes + s * kStepBytes),
-                   p.x + (in ? static_cast<int64_t>(m) * p.K + k : 0), in);
-        m += dm;
-        s += ds;
-        if (s >= steps) {
-            s -= steps;
-            ++m;
+    for (int half = 0; half < 2; ++half) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = r[8 * half + i] * down;
+        const uint32_t c = cvt_e2m1x8(y);
+        (half ? w.y : w.x) = c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h2;
+            asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+                : "=r"(h2)
+                : "r"(c >> (8 * i) & 0xFFu));
+            const __half2 h = *reinterpret_cast<const __half2*>(&h2);
+            r[8 * half + 2 * i] = fmaf(-up, __low2float(h), r[8 * half + 2 * i]);
+            r[8 * half + 2 * i + 1] = fmaf(-up, __high2float(h), r[8 * half + 2 * i + 1]);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    for (int m = m0, s = s0; m < p.M;) {
-        const uint4 v = *reinterpret_cast<const uint4*>(base + m * row_bytes + s * kStepBytes);
-        const uint32_t a = max_bf16x2(max_bf16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                      max_bf16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(a << 16, a & 0xFFFF0000u));
-        if (lane == 0) atomicMax(&amax[m], top);
-        m += dm;
-        s += ds;
-        if (s >= steps) {
-            s -= steps;
-            ++m;
-        }
-    }
-    __syncthreads();
-    for (int m = m0, s = s0; m < p.M;) {
-        uint4* at = reinterpret_cast<uint4*>(base + m * row_bytes + s * kStepBytes);
-        const float up = pow2_biased(268 - x_exponent(amax[m]));     // 2^(14 - (e - 127))
-        const uint4 v = *at;
-        uint4 h;
-        h.x = pack_f16(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up);
-        h.y = pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up);
-        h.z = pack_f16(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up);
-        h.w = pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up);
-        *at = h;
-        m += dm;
-        s += ds;
-        if (s >= steps) {
-            s -= steps;
-            ++m;
-        }
-    }
-    __syncthreads();
+    return w;
 }
 
-// NT: 8-row tiles of x.
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvParams p)
+// Largest |x| of sixteen bf16 as fp32 bits; an infinity or NaN is the largest of all.
+__device__ __forceinline__ uint32_t max_bits(const uint4 (&v)[2])
 {
-    extern __shared__ uint4 xs[];               // x in f16
-    __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
-    __shared__ uint32_t amax[NT * 8];           // bits of the largest |x| of this piece so far
+    uint32_t m = 0;
+    const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, max(u[i] << 16 & 0x7FFFFFFFu, u[i] & 0x7FFF0000u));
+    return m;
+}
+
+// One CTA per row of x; a thread takes 16-element blocks.  Also zeroes the counters of the tiles.
+__global__ void __launch_bounds__(1024)
+    nvfp4_gemv_split_kernel(const __nv_bfloat16* __restrict__ x, int K, int mp, int nb,
+                            uint8_t* __restrict__ xc, int32_t* __restrict__ rho,
+                            int32_t* __restrict__ done, int counters)
+{
+    __shared__ uint32_t warp_max[32];
     griddep_wait();
     griddep_launch_dependents();
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
-    const int oct = warp & 3, kw = warp >> 2;
-    uint32_t rank, pieces;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(pieces));
-    int tile = blockIdx.x / pieces;
-    const int c0 = rank * p.cta_steps, c1 = min(c0 + p.cta_steps, p.steps);
-
-    // in registers: the two halves of the step at hand, each replaced by the next step's as soon
-    // as it is used
-    HalfStep w[2];
-    LaneRows rows = lane_rows(p, tile, oct * 8 + g);
-    if (c0 + kw < c1) {
-        load_half(p, rows, c0 + kw, t, 0, w[0]);
-        load_half(p, rows, c0 + kw, t, 1, w[1]);
+    const int m = blockIdx.x, blocks = K / 16;
+    const uint4* row = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * K);
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < counters; i += gridDim.x * blockDim.x)
+        done[i] = 0;
+    uint4 v[2] = {};
+    uint32_t top = 0;
+    for (int b = threadIdx.x; b < blocks; b += blockDim.x) {
+        v[0] = row[2 * b];
+        v[1] = row[2 * b + 1];
+        top = max(top, max_bits(v));
     }
-    if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
     __syncthreads();
-
-    // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
-    // Rows of a tile past M read the last row; their columns are not stored.
-    const int row_bytes = p.stage_steps * kStepBytes + 32;
-    const uint8_t* xg[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, p.M - 1) * row_bytes + t * 64;
-    const int swap = (t >> 1) * 16;
-    const float gs = __ldg(p.scale);
-
-  for (; tile < p.tiles; tile += p.groups) {
-    int s = c0 + kw;
-    float acc[2][NT][4] = {};
-    for (int a0 = c0; a0 < c1; a0 += p.stage_steps) {
-        const int a1 = min(a0 + p.stage_steps, c1);
-        // x stays in shared memory from one tile to the next when its piece fits there
-        if (tile == static_cast<int>(blockIdx.x / pieces) || c1 - c0 > p.stage_steps) {
-            int e_old[NT][2];                   // biased exponents that the columns' sums go by
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    e_old[nt][i] = a0 == c0 ? 0 : x_exponent(amax[nt * 8 + 2 * t + i]);
-            __syncthreads();                    // the last stage and its exponents are read
-            if (a0 == c0 && tile != static_cast<int>(blockIdx.x / pieces)) {
-                if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
-                __syncthreads();
-            }
-            stage_x(p, a0, a1, xs, row_bytes, amax);
-            if (a0 != c0) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int d = x_exponent(amax[nt * 8 + 2 * t + i]) - e_old[nt][i];
-                        const float f = d < 127 ? pow2_biased(127 - d) : 0.0f;
-                        acc[0][nt][i] *= f;
-                        acc[0][nt][i + 2] *= f;
-                        acc[1][nt][i] *= f;
-                        acc[1][nt][i + 2] *= f;
-                    }
-            }
+    top = threadIdx.x % 32 < blockDim.x / 32 ? warp_max[threadIdx.x & 31] : 0;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const bool finite = top < 0x7F800000u;
+    const int e = finite ? max(log2_over_6(fmaxf(__uint_as_float(top), 0x1p-120f)), -120) : 0;
+    if (threadIdx.x == 0) rho[m] = finite ? e : kPoison;
+    const float n1 = exp2_int(-e / 2), n2 = exp2_int(-e - -e / 2);
+    const bool held = blocks <= static_cast<int>(blockDim.x);      // v still has the block
+    for (int b = threadIdx.x; b < blocks; b += blockDim.x) {
+        if (!held) {
+            v[0] = row[2 * b];
+            v[1] = row[2 * b + 1];
         }
-
-        for (; s < a1; s += 2) {
-            // the step after the last is the next tile's first
-            const bool wrap = s + 2 >= c1;
-            const int s_next = wrap ? c0 + kw : s + 2;
-            const bool more = !wrap || tile + p.groups < p.tiles;
-            if (wrap && more) rows = lane_rows(p, tile + p.groups, oct * 8 + g);
-            const int xo = (s - a0) * kStepBytes;
+        const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        float r[16];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+        for (int i = 0; i < 8; ++i) {
+            r[2 * i] = bf16lo_to_f32(u[i]) * n1 * n2;
+            r[2 * i + 1] = bf16hi_to_f32(u[i]) * n1 * n2;
+        }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint4 b[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        b[nt] = *reinterpret_cast<const uint4*>(
-                            xg[nt] + xo + half * 256 + ((j * 16) ^ swap));
-                    uint32_t h[4][4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // scale byte 2 (t % 2) + j / 2 of the row's word
-                        const uint32_t sc =
-                            scale_to_f16(word_of(w[half].s, q), (t & 1) * 2 + (j >> 1));
-                        e2m1x8_to_f16(word_of(w[half].c[q], j), h[q]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(acc[0][nt], h[0][0], h[1][0], h[0][1], h[1][1], b[nt].x, b[nt].y);
-                        mma_f16(acc[1][nt], h[2][0], h[3][0], h[2][1], h[3][1], b[nt].x, b[nt].y);
-                        mma_f16(acc[0][nt], h[0][2], h[1][2], h[0][3], h[1][3], b[nt].z, b[nt].w);
-                        mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
-                    }
-                }
-                if (more) load_half(p, rows, s_next, t, half, w[half]);
-            }
+        for (int i = 0; i < kTerms; ++i) {
+            const int j = i * mp + m;
+            const int64_t at = (static_cast<int64_t>(b >> 4) * nb + j) * 128;
+            *reinterpret_cast<uint2*>(xc + at + (((b >> 1 & 7) ^ (j & 7)) << 4) + (b & 1) * 8) =
+                take_term(r, term_exp(i));
         }
     }
-
-    // ---- sums of the two halves of the warps, then of the cluster's CTAs, in order
-#pragma unroll
-    for (int half = 1; half >= 0; --half) {
-        if (kw == half) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int ta = 0; ta < 2; ++ta)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = oct * 8 + g + 64 * ta + 32 * (i >> 1);
-                        const int col = nt * 8 + 2 * t + (i & 1);
-                        const float v = acc[ta][nt][i] * gs *
-                                        pow2_biased(x_exponent(amax[col]) - 14);
-                        part[col][r] = half ? v : part[col][r] + v;
-                    }
-        }
-        __syncthreads();
-    }
-    if (pieces > 1) cluster_sync();
-    // a thread keeps its row n: 128 / pieces rows, and every (kThreads / that)-th row of x
-    const int share = kTileRows / pieces;
-    const int r = rank * share + (threadIdx.x & (share - 1)), n = tile * kTileRows + r;
-    const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f;
-    for (int m = threadIdx.x / share; m < p.M; m += kThreads / share) {
-        if (n >= p.N) break;
-        float v;
-        if (pieces == 1) {
-            v = part[m][r];
-        } else {
-            const uint32_t at = smem_u32(&part[m][r]);
-            float y[8];
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
-                y[j] = 0.0f;
-                if (j < pieces)
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(y[j])
-                                 : "r"(mapa_shared(at, j)));
-            }
-            v = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-        }
-        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(v + bias);
-    }
-    // the others have read this CTA's sums, before they are written again or the CTA ends
-    if (pieces > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-  }
 }
 
-template <int NT>
-int launch_gemv(GemvParams p, int dev, int sms, cudaStream_t stream)
+// First K stage of CTA i's run, and the CTA whose run holds stage s.
+__device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int i)
 {
+    return total * i / ctas;
+}
+
+__device__ __forceinline__ int run_owner(int64_t total, int ctas, int64_t s)
+{
+    return static_cast<int>(((s + 1) * ctas - 1) / total);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap tm_w, const GemvArgs args)
+{
+    griddep_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], ones_ready, fin[2];
+    __shared__ float2 factor[kGemvMaxRows];                      // 2^e g of a row, in two parts
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
+    __shared__ __align__(128) uint32_t ones[128];                // E4M3 1.0
+    volatile int* abort_flag = &abort_word;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stages = args.stages, num_kt = args.num_kt, nb = args.nb;
+    const int b_bytes = nb * 128, stage_bytes = kABytes + b_bytes + kSfBytes;
+    const int ctas = gridDim.x;
+    const int64_t s0 = run_begin(args.total, ctas, blockIdx.x);
+    const int64_t s1 = run_begin(args.total, ctas, blockIdx.x + 1);
+    const int mine = static_cast<int>(s1 - s0);
+    // two issuers' accumulators, twice when they fit
+    const int bufs = 4 * nb <= kAccCols ? 2 : 1, acc_cols = kAccCols / (2 * bufs);
+
+    // a walk over the run's stages: K stage, tile, slot of the ring, and the slot's phase
+    struct Walk {
+        int tile, kt, slot;
+        uint32_t phase;
+    };
+    const int kb_all = args.K / 64;
+    const int tile0 = static_cast<int>(s0 / num_kt);
+    const Walk begin = {tile0, static_cast<int>(s0 - static_cast<int64_t>(tile0) * num_kt),
+                        0, 0};
+    const auto next = [&](Walk& w) {
+        if (++w.kt == num_kt) {
+            w.kt = 0;
+            ++w.tile;
+        }
+        if (++w.slot == stages) {
+            w.slot = 0;
+            w.phase ^= 1;
+        }
+    };
+    const auto weight = [&](const Walk& w) {
+        const int nkb = min(4, kb_all - 4 * w.kt);
+        uint8_t* dst = ring + w.slot * stage_bytes;
+        uint64_t* bar = full + w.slot;
+        mbar_arrive_expect_tx(bar, kABytes + b_bytes + nkb * 512);
+        tma_load_2d(dst, &tm_w, bar, w.kt * (kStageK / 2), w.tile * kTileRows);
+        bulk_load(dst + kABytes + b_bytes,
+                  args.sfa + (static_cast<int64_t>(w.tile) * kb_all + 4 * w.kt) * 512,
+                  nkb * 512, bar);
+    };
+    const auto rows = [&](const Walk& w) {
+        uint8_t* dst = ring + w.slot * stage_bytes;
+        bulk_load(dst + kABytes, args.xc + static_cast<int64_t>(w.kt) * b_bytes, b_bytes,
+                  full + w.slot);
+    };
+    const int early = min(mine, stages);
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull + a, 2);
+            mbar_init(tempty + a, 4);
+        }
+        mbar_init(&ones_ready, 1);
+        mbar_init(fin, 1);
+        mbar_init(fin + 1, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        // The first weights are on their way before the split kernel has ended, and before this CTA is
+        // set up: nothing that this grid depends on writes them.
+        Walk w = begin;
+        for (int i = 0; i < early; ++i, next(w)) weight(w);
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_holder, kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x < 128) ones[threadIdx.x] = 0x38383838u;
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = tmem_holder;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            griddep_wait();                      // x is split
+            Walk w = begin;
+            for (int i = 0; i < early; ++i, next(w)) rows(w);
+            int i = early;
+            for (; i < mine; ++i, next(w)) {
+                if (!mbar_wait(empty + w.slot, w.phase ^ 1u, abort_flag, args.wait_ns, args.status,
+                               101))
+                    break;
+                weight(w);
+                rows(w);
+            }
+            // the last loads must land before shared memory is freed
+            for (int j = max(0, i - stages); j < i; ++j)
+                drain_wait(full + j % stages, j / stages & 1, args.wait_ns, args.status);
+        }
+    } else if (warp == 1 || warp == 6) {
+        // ------------------------------------------------------------ MMA issuers
+        if (lane == 0) {
+            const int own = warp == 6;               // stages i with i % 2 == own
+            const uint32_t idesc = idesc_nvf4(kTileRows, nb);
+            const uint32_t sfa = tbase + kSfaCol + 16 * own, sfb = tbase + kSfbCol;
+            if (own == 0)
+                for (int c = 0; c < 2; ++c)          // scales of up to 256 rows of the second operand
+                    tmem_cp_32x128b_x4(sfb + 4 * c, sdesc_sf_block(smem_u32(ones)));
+            if (own == 0) {
+                tc_commit(&ones_ready);
+            } else if (!mbar_wait(&ones_ready, 0, abort_flag, args.wait_ns, args.status, 105)) {
+                *abort_flag = 1;
+            }
+            tc_fence_after();
+            int seg = -1, kt = static_cast<int>(s0 % num_kt), s = 0;
+            uint32_t phase = 0;
+            bool fresh = true;                       // nothing of this segment is issued yet
+            for (int i = 0; i < mine; ++i) {
+                if (i == 0 || kt == 0) {
+                    if (seg >= 0) tc_commit(tfull + seg % bufs);
+                    ++seg;
+                    fresh = true;
+                    if (!mbar_wait(tempty + seg % bufs, (seg / bufs & 1) ^ 1u, abort_flag,
+                                   args.wait_ns, args.status, 102)) {
+                        seg = -1;
+                        break;
+                    }
+                }
+                if ((i & 1) == own) {
+                    if (!mbar_wait(full + s, phase, abort_flag, args.wait_ns, args.status, 103)) {
+                        seg = -1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(ring + s * stage_bytes);
+                    const uint64_t sf = sdesc_sf_block(a + kABytes + b_bytes);
+                    const uint64_t ad = sdesc_kmajor_sw128(a);
+                    const uint64_t bd = sdesc_kmajor_sw128(a + kABytes);
+                    const uint32_t d = tbase + (2 * (seg % bufs) + own) * acc_cols;
+                    const int nk = args.K / 64 - 4 * kt;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < nk) tmem_cp_32x128b_x4(sfa + 4 * k, sf + 32 * k);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < nk)
+                            mma_nvf4(d, ad + 2 * k, bd + 2 * k, idesc, sfa + 4 * k, sfb,
+                                     fresh && k == 0 ? 0u : 1u);
+                    tc_commit(empty + s);
+                    fresh = false;
+                }
+                if (++kt == num_kt) kt = 0;
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+            if (seg >= 0) tc_commit(tfull + seg % bufs);
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3, row = q * 32 + lane;
+        griddep_wait();                          // the exponents and the counters are written
+        const float g = __ldg(args.w_scale);
+        if (lane < args.M) {                     // each warp writes them all: the same values
+            const int e = __ldcg(args.rho + lane);
+            factor[lane] = e == kPoison ? make_float2(NAN, NAN)
+                                        : make_float2(exp2_int(e / 2) * g, exp2_int(e - e / 2));
+        }
+        __syncwarp();
+        int seg = 0;
+        for (int64_t at = s0; at < s1; ++seg) {
+            const int tile = static_cast<int>(at / num_kt);
+            const int64_t t0 = static_cast<int64_t>(tile) * num_kt, t1 = t0 + num_kt;
+            const bool begins = at == t0, whole = begins && t1 <= s1;
+            const int n = tile * kTileRows + row;
+            const bool in = n < args.N;
+            const float bias = in && args.bias ? __bfloat162float(args.bias[n]) : 0.0f;
+            const int64_t end = min(t1, s1);
+            const bool one = end - at == 1;      // then one of the issuers had nothing to do
+            const int first_own = static_cast<int>(at - s0) & 1;
+            const bool ok = mbar_wait(tfull + seg % bufs, seg / bufs & 1, abort_flag, args.wait_ns,
+                                      args.status, 104);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const uint32_t acc = tbase + (static_cast<uint32_t>(q * 32) << 16) +
+                                 2 * (seg % bufs) * acc_cols;
+            const auto finish = [&](int m, float v) {
+                if (!in || m >= args.M) return;
+                const float2 f = factor[m];
+                args.out[static_cast<int64_t>(m) * args.N + n] =
+                    __float2bfloat16_rn(v * f.x * f.y + bias);
+            };
+            float* part = args.parts +
+                          static_cast<int64_t>(2 * blockIdx.x + begins) * args.M * kTileRows + row;
+            for (int c = 0; c < args.mp; c += 8) {
+                float v[8] = {};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (k == 1 && one) break;
+                    const uint32_t from = acc + (first_own ^ k) * acc_cols + c;
+                    uint32_t r[kTerms][8];
+#pragma unroll
+                    for (int i = 0; i < kTerms; ++i) tmem_ld_x8(from + i * args.mp, r[i]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float y = 0.0f;          // the smallest terms first
+#pragma unroll
+                        for (int i = kTerms - 1; i >= 0; --i)
+                            y = fmaf(__uint_as_float(r[i][j]), 1.0f / (1 << -term_exp(i)), y);
+                        v[j] += y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (whole)
+                        finish(c + j, v[j]);
+                    else if (c + j < args.M)
+                        part[(c + j) * kTileRows] = v[j];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty + seg % bufs);
+            if (!whole) {
+                // each of the four epilogue warps adds its own 32 rows when it is the last of the
+                // CTAs' warps to bring them
+                const int o0 = run_owner(args.total, ctas, t0), o1 = run_owner(args.total, ctas, t1 - 1);
+                __threadfence();
+                __syncwarp();
+                int before = 0;
+                if (lane == 0) before = atomicAdd(args.done + 4 * tile + q, 1);
+                before = __shfl_sync(0xFFFFFFFFu, before, 0);
+                if (before == o1 - o0) {
+                    __threadfence();
+                    const int64_t step = static_cast<int64_t>(2) * args.M * kTileRows;
+                    const float* first = args.parts + o0 * step + step / 2 + row;
+                    const float* rest = args.parts + o0 * step + row;
+                    for (int m = 0; m < args.M; m += 8) {
+                        float v[8];
+                        const int rows = min(8, args.M - m);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = j < rows ? __ldcg(first + (m + j) * kTileRows) : 0.0f;
+                        for (int i0 = 1; i0 <= o1 - o0; i0 += 4) {
+                            float y[4][8];       // four parts' loads in flight
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    y[i][j] = i0 + i <= o1 - o0 && j < rows
+                                                  ? __ldcg(rest + (i0 + i) * step +
+                                                           (m + j) * kTileRows)
+                                                  : 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) v[j] += y[i][j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) finish(m + j, v[j]);
+                    }
+                }
+            }
+            at = end;
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    __syncwarp();
+    if ((warp == 1 || warp == 6) && lane == 0) {
+        tc_commit(fin + (warp == 6));
+        drain_wait(fin + (warp == 6), 0, args.wait_ns, args.status);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Workspace: codes of the split x, parts, exponents, counters.
+struct GemvLayout {
+    int64_t parts, rho, done, bytes;
+    int32_t mp, nb, num_kt, tiles;
+};
+
+GemvLayout gemv_layout(int64_t M, int64_t N, int64_t K)
+{
+    GemvLayout l;
+    l.mp = static_cast<int32_t>((M + 7) / 8 * 8);
+    l.nb = (kTerms * l.mp + 15) / 16 * 16;
+    l.num_kt = static_cast<int32_t>((K + kStageK - 1) / kStageK);
+    l.tiles = static_cast<int32_t>((N + kTileRows - 1) / kTileRows);
+    l.parts = up256(static_cast<int64_t>(l.num_kt) * l.nb * 128);
+    l.rho = l.parts + static_cast<int64_t>(2) * kMaxCtas * M * kTileRows * 4;
+    l.done = up256(l.rho + M * 4);
+    l.bytes = up256(l.done + static_cast<int64_t>(l.tiles) * 16);
+    return l;
+}
+
+int gemv_check(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0) return BSP_ERR_INVALID_ARG;
+    if (M > kGemvMaxRows || K % 64 != 0 || K < 64 || N % 8 != 0 || N > (int64_t{1} << 30) ||
+        K > (int64_t{1} << 24))
+        return BSP_ERR_UNSUPPORTED_SHAPE;
+    return BSP_OK;
+}
+
+}  // namespace
+}  // namespace bsp
+
+extern "C" {
+
+int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    const int st = bsp::gemv_check(M, N, K);
+    return st != BSP_OK ? st : bsp::gemv_layout(M, N, K).bytes;
+}
+
+int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
+               const float* w_scale, const void* bias_bf16, void* out_bf16, int64_t M, int64_t N,
+               int64_t K, void* workspace, int64_t workspace_bytes, bsp_stream_t stream)
+{
+    using namespace bsp;
+    int st = gemv_check(M, N, K);
+    if (st != BSP_OK) return st;
+    if (M == 0 || N == 0) return BSP_OK;
+    if (!x_bf16 || !w_codes || !w_sf || !w_scale || !out_bf16) return BSP_ERR_INVALID_ARG;
+    const GemvLayout l = gemv_layout(M, N, K);
+    if (!workspace || workspace_bytes < l.bytes) return BSP_ERR_INVALID_ARG;
+    if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_sf) || !aligned16(bias_bf16) ||
+        !aligned16(out_bf16) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(w_scale) & 3u))
+        return BSP_ERR_MISALIGNED;
+    int dev = 0, sms = 0;
+    st = check_device(&dev, &sms);
+    if (st != BSP_OK) return st;
     static std::atomic<bool> ready[kMaxDevices];
+    constexpr int kSmem = kRingBytes + 1024;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(nvfp4_gemv_kernel<NT>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kMaxStage) != cudaSuccess) {
+        if (cudaFuncSetAttribute(nvfp4_gemv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmem) != cudaSuccess) {
             cudaGetLastError();
             return BSP_ERR_CUDA;
         }
         ready[dev].store(true, std::memory_order_release);
     }
-    // Pieces of K, and clusters ("groups") that take the row tiles in turn, two CTAs to an SM:
-    // the split whose busiest CTA has the least to do.  Counted in instructions of a warp: 200 (and
-    // 32 for each 8 rows of x) for a CTA's step, as much again for the sums of a tile, and 10 for
-    // bringing one row's step of x to shared memory, once.
-    p.tiles = (p.N + kTileRows - 1) / kTileRows;
-    int pieces = 1;
-    int64_t best = INT64_MAX;
-    for (int c = 1; c <= 8 && (c == 1 || 2 * c <= p.steps); c *= 2) {
-        const int groups = std::min(p.tiles, std::max(1, 2 * sms / c));
-        const int64_t steps = (p.steps + c - 1) / c;
-        const int64_t cost = (p.tiles + groups - 1) / groups * (steps + 1) * (200 + 32 * NT) +
-                             steps * p.M * 10;
-        if (cost < best) {
-            best = cost;
-            pieces = c;
-            p.groups = groups;
-        }
+    CUtensorMap tm;
+    st = make_code_map(&tm, w_codes, static_cast<uint64_t>(K) / 2, static_cast<uint64_t>(N),
+                       kTileRows);
+    if (st != BSP_OK) return st;
+    auto* ws = static_cast<uint8_t*>(workspace);
+    GemvArgs a = {};
+    a.sfa = w_sf;
+    a.w_scale = w_scale;
+    a.bias = static_cast<const __nv_bfloat16*>(bias_bf16);
+    a.out = static_cast<__nv_bfloat16*>(out_bf16);
+    a.xc = ws;
+    a.rho = reinterpret_cast<int32_t*>(ws + l.rho);
+    a.parts = reinterpret_cast<float*>(ws + l.parts);
+    a.done = reinterpret_cast<int32_t*>(ws + l.done);
+    a.M = static_cast<int32_t>(M);
+    a.N = static_cast<int32_t>(N);
+    a.K = static_cast<int32_t>(K);
+    a.mp = l.mp;
+    a.nb = l.nb;
+    a.num_kt = l.num_kt;
+    const int stage_bytes = kABytes + l.nb * 128 + kSfBytes;
+    a.stages = std::min(kMaxStages, kRingBytes / stage_bytes);
+    a.total = static_cast<int64_t>(l.tiles) * l.num_kt;
+    a.wait_ns = wait_limit_ns();
+    a.status = device_status_ptr(dev);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const unsigned threads = static_cast<unsigned>(std::min<int64_t>(1024, (K / 16 + 31) / 32 * 32));
+    // CTAs.  At least sqrt(num_kt M / 20) stages to each: fewer leave more parts of a tile to its
+    // last CTA than they save in stages (about 0.4 us each, against 0.6 us for 32 rows of parts).
+    // Where the tiles are fewer than that many CTAs, a multiple of the tiles gives every CTA one whole
+    // tile or one even part of one; it is taken unless its runs are over 7 stages (3 us, what a
+    // second part in a run costs) longer than equal runs over all SMs.
+    int per = 1;
+    while (per * per * 20 < l.num_kt * M) ++per;
+    int64_t ctas = std::min<int64_t>(std::min(sms, kMaxCtas), (a.total + per - 1) / per);
+    if (l.tiles <= ctas) {
+        const int64_t even = ctas / l.tiles;
+        if ((l.num_kt + even - 1) / even <= (a.total + ctas - 1) / ctas + 7) ctas = even * l.tiles;
     }
-    p.cta_steps = (p.steps + pieces - 1) / pieces;
-    p.stage_steps = std::min((p.cta_steps + 1) / 2 * 2,
-                             (kMaxStage / p.M - 32) / kStepBytes / 2 * 2);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = pieces;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * pieces, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * (p.stage_steps * kStepBytes + 32);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<NT>, p) != cudaSuccess) {
+    if (launch_kernel(nvfp4_gemv_split_kernel, static_cast<unsigned>(M), threads, 0, s, true,
+                      static_cast<const __nv_bfloat16*>(x_bf16), a.K, a.mp, a.nb, ws,
+                      reinterpret_cast<int32_t*>(ws + l.rho),
+                      reinterpret_cast<int32_t*>(ws + l.done), 4 * l.tiles) != cudaSuccess ||
+        launch_kernel(nvfp4_gemv_kernel, static_cast<unsigned>(ctas), kThreads,
+                      static_cast<size_t>(a.stages) * stage_bytes + 1024, s, true, tm,
+                      a) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
     return launch_status();
 }
 
-}  // namespace
-}  // namespace bsp
-
-extern "C" int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
-                          const float* w_scale, const void* bias_bf16, void* out_bf16, int64_t M,
-                          int64_t N, int64_t K, bsp_stream_t stream)
-{
-    using namespace bsp;
-    if (M < 0 || N < 0 || K < 0) return BSP_ERR_INVALID_ARG;
-    if (M > kGemvMaxRows || K % 64 != 0 || K < 64 || N % 8 != 0 || N > (int64_t{1} << 30) ||
-        K > (int64_t{1} << 24))
-        return BSP_ERR_UNSUPPORTED_SHAPE;
-    if (M == 0 || N == 0) return BSP_OK;
-    if (!x_bf16 || !w_codes || !w_sf || !w_scale || !out_bf16) return BSP_ERR_INVALID_ARG;
-    if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_sf) || !aligned16(bias_bf16) ||
-        !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(w_scale) & 3u))
-        return BSP_ERR_MISALIGNED;
-    int dev = 0, sms = 0;
-    int st = check_device(&dev, &sms);
-    if (st != BSP_OK) return st;
-    GemvParams p = {};
-    p.x = static_cast<const __nv_bfloat16*>(x_bf16);
-    p.codes = w_codes;
-    p.sf = w_sf;
-    p.scale = w_scale;
-    p.bias = static_cast<const __nv_bfloat16*>(bias_bf16);
-    p.out = static_cast<__nv_bfloat16*>(out_bf16);
-    p.M = static_cast<int32_t>(M);
-    p.N = static_cast<int32_t>(N);
-    p.K = static_cast<int32_t>(K);
-    p.steps = static_cast<int32_t>((K + kStepK - 1) / kStepK);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (M <= 8) return launch_gemv<1>(p, dev, sms, s);
-    if (M <= 16) return launch_gemv<2>(p, dev, sms, s);
-    if (M <= 24) return launch_gemv<3>(p, dev, sms, s);
-    return launch_gemv<4>(p, dev, sms, s);
-}
+}  // extern "C"

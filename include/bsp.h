@@ -303,19 +303,26 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int layout,
 
 /*
  * nvfp4_gemv -- a few rows of bf16 activations against an NVFP4 weight, the activations NOT
- * quantized: the product of the dequantise-only path ("BFL (fp8r / nvfp4)", closing paragraph
+ * quantized to it: the product of the dequantise-only path ("BFL (fp8r / nvfp4)", closing paragraph
  * of the "Kernels" section) for single tokens, read straight from the 4-bit weight.
  *   x_bf16  [M][K] bf16, 1 <= M <= 32 (M == 0 returns BSP_OK).
  *   w_codes [N][K/2], w_sf (BSP_SF_MMA, rows = N), w_scale (device, 1 fp32), bias_bf16 [N] or
- *           NULL, out_bf16 [M][N]: as nvfp4_gemm.
+ *           NULL, out_bf16 [M][N]: as nvfp4_gemm (block scales have no sign).
  *   Y[m][n] = bf16( w_scale * sum_k x[m][k] * e2m1(w[n][k]) * e4m3(sf[n][k/16]) + bias[n] ),
- *   products exact, sums in fp32.
+ *   sums in fp32.  x reaches the tensor cores held to 2^-19 of the largest element of its row (bf16
+ *   holds an element to 2^-8 of itself).  A row that holds an infinity or a NaN gives NaN.  The rows
+ *   do not affect one another.
+ *   workspace  device buffer of at least nvfp4_gemv_workspace_bytes(M, N, K) bytes, 16-byte
+ *              aligned, any contents; not shared by calls that can run at the same time.
  * Constraints: K % 64 == 0, K >= 64; N % 8 == 0; M <= 32 (BSP_ERR_UNSUPPORTED_SHAPE).  The time
  * is that of reading the weight; above 32 rows nvfp4_linear is the faster form.
  */
 int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
                const float* w_scale, const void* bias_bf16, void* out_bf16, int64_t M, int64_t N,
-               int64_t K, bsp_stream_t stream);
+               int64_t K, void* workspace, int64_t workspace_bytes, bsp_stream_t stream);
+
+/* Workspace bytes nvfp4_gemv needs; negative on bad arguments. */
+int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
  * The block-scaled 8-bit key/value cache.  One cache (one layer) is four device arrays:

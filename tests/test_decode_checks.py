@@ -14,12 +14,17 @@ ON_CPU = "not on a CUDA device"
 
 def test_gemv_host_checks():
     g = bsp.lib().nvfp4_gemv
-    base = dict(x=P, c=P, s=P, g=P, b=None, o=P, M=1, N=64, K=128)
+    base = dict(x=P, c=P, s=P, g=P, b=None, o=P, M=1, N=64, K=128, ws=P, wsb=1 << 30)
 
     def call(**kw):
         a = {**base, **kw}
-        return g(a["x"], a["c"], a["s"], a["g"], a["b"], a["o"], a["M"], a["N"], a["K"], None)
+        return g(a["x"], a["c"], a["s"], a["g"], a["b"], a["o"], a["M"], a["N"], a["K"], a["ws"],
+                 a["wsb"], None)
 
+    need = bsp.nvfp4_gemv_workspace_bytes(1, 64, 128)
+    assert call(ws=None) == INVALID and call(wsb=need - 1) == INVALID and call(ws=P + 8) == MISALIGNED
+    size = bsp.lib().nvfp4_gemv_workspace_bytes
+    assert size(33, 64, 128) == SHAPE and size(-1, 64, 128) == INVALID and size(1, 64, 96) == SHAPE
     for name in "xcsgo":
         assert call(**{name: None}) == INVALID
         assert call(**{name: P + (2 if name == "g" else 8)}) == MISALIGNED
@@ -35,13 +40,14 @@ def test_gemv_binding_checks():
               w_codes=torch.zeros((N, K // 2), dtype=torch.uint8),
               w_sf=torch.zeros((bsp.nvfp4_sf_bytes(N, K),), dtype=torch.uint8),
               w_scale=torch.ones(()), bias=torch.zeros((N,), dtype=torch.bfloat16),
-              out=torch.zeros((M, N), dtype=torch.bfloat16))
+              out=torch.zeros((M, N), dtype=torch.bfloat16),
+              workspace=torch.zeros((bsp.nvfp4_gemv_workspace_bytes(M, N, K),), dtype=torch.uint8))
     with pytest.raises(bsp.BSPError, match=ON_CPU):
         bsp.nvfp4_gemv(**ok)
     for name, bad in [("w_sf", ok["w_sf"][:-1]), ("bias", ok["bias"][:-8]), ("out", ok["out"][:2])]:
         with pytest.raises(bsp.BSPError, match="needs"):
             bsp.nvfp4_gemv(**{**ok, name: bad})
-    for name in ("x", "w_codes", "w_scale", "bias", "out"):
+    for name in ("x", "w_codes", "w_scale", "bias", "out", "workspace"):
         with pytest.raises(TypeError):
             bsp.nvfp4_gemv(**{**ok, name: ok[name].to(torch.float64)})
     with pytest.raises(bsp.BSPError, match="columns"):

@@ -1,9 +1,13 @@
 """nvfp4_gemv on the GPU against the 64-bit product of the decoded weight.
 
-Bound.  Products of a bf16 x (or its f16 form, which holds x to 2^-39 of the largest x) and a
-weight of at most 6 significant bits are exact in fp32; a sum of K of them is a chain of at
-most K / 16 + 32 additions, each off by at most 2^-22 of S = sum |x||w| (a tensor core may cut
-instead of round); the factors and the bias add 3 * 2^-24 of the result, the output 2^-8."""
+Bound.  x enters as seven E2M1 terms, a row's power of two apart.  A term's nearest code leaves at most
+half the codes' distance: 1 unit where |x| <= 6 (distance 2 above 4), which is 4 units of the next
+term, 2^-2; from there half a unit of 2^-2, 2^-5, ... 2^-17, so 2^-18 in the end, and the row's largest
+element is above 3: 2^-19.58 of it.  Products of codes and scales are exact in fp32; a term's sum over K
+is a chain of at most K / 64 + 64 additions (a product instruction takes 64), each off by at most
+2^-22 of sum |term||w|, and a term is at most 4 of its units where 6 units of the first are the most: the
+terms' sizes come to at most |x| + 2^-19.58 top + 2 (1 + 2^-3 + ...) top / 3 <= |x| + top.  The seven sums
+are joined (2^-22 each), the factors and the bias add 2^-21 of the result, the output 2^-8."""
 import math
 
 import numpy as np
@@ -39,11 +43,12 @@ def check(y, x, codes, sf, g, bias=None):
     w, xd = decode(codes, sf, N, K) * g.double().cpu(), x.cpu().double()
     want = xd @ w.t()
     S = xd.abs() @ w.abs().t()
-    small = 2.0 ** -39 * xd.abs().amax(1, keepdim=True) * w.abs().sum(1)
+    top = xd.abs().amax(1, keepdim=True) * w.abs().sum(1)
     if bias is not None:
         want = want + bias.cpu().double()
-    bound = want.abs() * (2.0 ** -8 + 2.0 ** -21) + (K / 16 + 32) * 2.0 ** -22 * S + small
-    bound += 0 if bias is None else bias.cpu().double().abs() * 2.0 ** -23
+    bound = want.abs() * (2.0 ** -8 + 2.0 ** -21) + 2.0 ** -19.58 * top
+    bound += (K / 64 + 72) * 2.0 ** -22 * (S + top)
+    bound += 0 if bias is None else bias.cpu().double().abs() * 2.0 ** -21
     d = (y.cpu().double() - want).abs()
     assert (d <= bound).all(), float((d / bound).max())
 
@@ -67,13 +72,12 @@ def test_sizes(M, N, K):
 
 
 def test_every_code_and_scale():
-    """All 16 codes under every finite E4M3 scale byte, negative ones among them, each block on its
-    own (x is one-hot): the product is exact, so the output is one rounding."""
+    """All 16 codes under every finite scale byte without a sign (the only ones that a block scale
+    has), each block on its own (x is one-hot): the product is exact, so the output is one rounding."""
     N, K = 256, 1024
     i = torch.arange(N * K // 2)
     codes = (i * 7 + i // (K // 2) * 13).to(torch.uint8).view(N, K // 2).cuda()
-    lin = ((torch.arange(N * K // 16) * 5 + 1) % 256).to(torch.uint8)
-    lin[lin & 127 == 127] = 0x20
+    lin = ((torch.arange(N * K // 16) * 5 + 1) % 127).to(torch.uint8)
     sf = bsp.nvfp4_sf_convert(lin.cuda(), N, K, bsp.SF_LINEAR, bsp.SF_MMA)
     g = torch.tensor([0.125], device="cuda")
     w = decode(codes, sf, N, K) * 0.125
