@@ -88,6 +88,11 @@ _SIGS = {
 
 _lib = None
 
+try:                      # C++ short cut for the calls of a decode step (csrc/fastcall.cpp)
+    from . import _fastcall
+except ImportError:       # not built: the same calls, marshalled in Python
+    _fastcall = None
+
 
 class BSPError(RuntimeError):
     """A libbsp call returned a negative bsp_status."""
@@ -407,6 +412,10 @@ def nvfp4_gemv(x: torch.Tensor, w_codes, w_sf, w_scale, bias=None, out=None, wor
     """Y[M, N] bf16 = x [M, K] times an NVFP4 weight (operands as nvfp4_gemm's), x not quantized:
     the weight-only form for 1 to 32 rows.  `workspace` (uint8, at least
     nvfp4_gemv_workspace_bytes(M, N, K) bytes) is allocated here when not given."""
+    if _fastcall is not None and stream is None:
+        y = _fastcall.gemv(x, w_codes, w_sf, w_scale, bias, out, workspace)
+        if y is not None:
+            return y
     M, K = _mat(x, torch.bfloat16, "x")
     N, _ = _mat(w_codes, torch.uint8, "w_codes", K // 2)
     _nvfp4_operands(0, N, K, None, None, w_sf, w_scale, bias)
@@ -479,6 +488,11 @@ def fp8kv_append(k: torch.Tensor, v: torch.Tensor, k_cache, v_cache, k_scale, v_
     paged E4M3 cache (see fp8kv_append in bsp.h).  k, v: bf16 [T, Hkv, D], q: bf16 [T, Hq, D],
     each possibly a slice of one projection's output; inv_freq: fp32 [rot / 2] or None for no
     rotation.  Returns the rotated q (q_out), or None when no q is given."""
+    if _fastcall is not None and stream is None:
+        r = _fastcall.append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv_len,
+                             q, q_out, inv_freq, interleaved, rope_scale)
+        if r is not None:
+            return None if r is True else r
     pages, Hkv, page, D, B, max_pages = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table,
                                                   cu_new, kv_len)
     T, hk, _, ks = _heads(k, "k", None, D)
@@ -521,6 +535,11 @@ def fp8kv_attention(q: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_t
     window 0 means none.  `workspace` (uint8, at least fp8kv_attention_workspace_bytes(T, Hq,
     Hkv, D) bytes) is allocated here when not given.  Returns out (bf16 [T, Hq, D]), or
     (out, lse) with return_lse."""
+    if _fastcall is not None and stream is None:
+        r = _fastcall.attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv_len,
+                                sm_scale, window, out, lse, return_lse, workspace)
+        if r is not None:
+            return r
     pages, Hkv, page, D, B, max_pages = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table,
                                                   cu_new, kv_len)
     T, Hq, _, qs = _heads(q, "q", None, D)

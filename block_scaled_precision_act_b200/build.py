@@ -1,4 +1,5 @@
-"""Build ``libbsp.so`` in-tree with nvcc for sm_100a (B200).
+"""Build ``libbsp.so`` in-tree with nvcc for sm_100a (B200), and ``_fastcall.so``, the binding's
+C++ short cut, with g++ against the installed torch.
 
 No fast-math and no flush-to-zero: the quantizers rely on IEEE division,
 reciprocal and denormals to produce codes bit-identical to their definition.
@@ -16,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 SOURCES = ["api_common.cu", "quant.cu", "gemm.cu", "linear.cu", "linear_noalloc.cu", "gemv.cu",
            "fp8kv_append.cu", "fp8kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -64,7 +66,30 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([NVCC] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    build_fastcall(run, force)
     return LIB
+
+
+def build_fastcall(run, force: bool) -> None:
+    src = os.path.join(CSRC, "fastcall.cpp")
+    if (not force and os.path.exists(FASTCALL)
+            and os.path.getmtime(FASTCALL) >= max(os.path.getmtime(src), _deps())):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = cpp_extension.include_paths(device_type="cuda") + [sysconfig.get_paths()["include"],
+                                                             INCLUDE]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = FASTCALL + f".tmp{os.getpid()}"
+    run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         *[x for d in inc for x in ("-isystem", d)], src, "-o", tmp, "-L", libs, "-lc10",
+         "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L", PKG, "-l:libbsp.so",
+         "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, FASTCALL)
 
 
 if __name__ == "__main__":
