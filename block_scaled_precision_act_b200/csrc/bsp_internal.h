@@ -28,6 +28,11 @@ uint64_t wait_limit_ns();
 int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
                   uint32_t box_rows);
 
+// Tensor map of a paged cache [groups][tokens][D] of bytes, with boxes of box_tokens x 128 bytes in
+// the 128-byte swizzle (bytes past D are zeros).
+int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens, uint64_t groups,
+                  uint32_t box_tokens);
+
 // nvfp4_gemm (nvf4) / fp8r_gemm launched right after the library's activation quantizer
 // wrote `a` (and `a_sf`): same results, but the weight operand's first stages are fetched
 // while that quantizer finishes (the quantizer never writes the weights).

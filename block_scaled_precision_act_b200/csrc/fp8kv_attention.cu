@@ -3,20 +3,29 @@
 //   out[r] = sum_t p_rt v_t / sum_t p_rt,  p_rt = exp(sm_scale q_r . k_t), over the tokens t that
 //   row r sees: t <= pos(r), and t > pos(r) - window when a window is given.
 //
-// Rows: the query heads that share a key head and the new tokens of a sequence, 16 to a tile
-// (row = token * G + head in group).  A step is one 16-token block of the cache, taken by one
-// warp with m16n8k16 f16 products accumulated in fp32; the block's two scales are one number
-// each, so they never touch the elements:
-//   * E4M3 -> f16 is exact.  K goes from global memory into the B fragments without shared
-//     memory: the products may run over d in any order, so a lane takes the 16-byte chunks of its
-//     token row that it loads as the k slots that it owns.  q is scaled by a power of two per row
-//     so that its largest element is in [2^14, 2^15): f16 then holds every bf16 element of the
-//     row down to 2^-28 of the largest exactly, and rounds smaller ones by at most 2^-39 of it.
-//   * V: a lane loads a chunk of each of the four tokens whose k slots it owns; a byte permute
-//     pairs tokens.  The softmax weights (in [0, 1], fp32) are rounded once, to f16 with 11 bits,
-//     after a factor 2^(13 + e_V - e_ref), which keeps them normal down to 2^-27 of the largest;
-//     e_ref follows the V scales when they leave [e_ref - 10, e_ref + 2].
-//   * running maximum and sum in fp32; the output is rescaled only when a maximum moves.
+// What bounds it is reading the cache, 2 D bytes for each token and key head.  Converting the codes
+// for f16 products on the CUDA cores took 500 instructions per 16 tokens and warp, 1.8 times the
+// reading; so the codes go from global memory by TMA to shared memory and into tcgen05.mma
+// kind::f8f6f4 as they are, as the M = 128 operand of both products, and the small operands are
+// made to fit.  A tile is 128 tokens; a block's two scales are one number each and never touch the
+// elements (the key scale multiplies the scores, the value scale the weights).
+//   S[128 tokens][3 R] = K Q^T.  A row of q, scaled by a power of two so that its largest element is in
+//   [128, 256), is the sum of three E4M3 rows of q, 16 q and 256 q's rounding rests: each holds four bits,
+//   so a bf16 element (eight bits) is exact, down to 2^-26 of the row's largest.
+//   O[128 d][4 R] = V^T P^T.  A weight in [0, 2], times 2^(14 + e_V - e_ref), is rounded once, to f16 (11
+//   bits), which is exactly the sum of four E5M2 values: an f16 cut to its upper byte is an E5M2,
+//   three bits of it, and the rest is an f16 again.  e_ref is a common power of two of the values, no
+//   smaller than any block's e_V.
+// One thread holds one token of a tile: its scores of all rows, so a weight's bytes for all rows and
+// terms are one 16- to 128-byte store (the operand's rows are tokens).  The rows' reference
+// maxima move only when a score exceeds one by more than 1 (a factor 2 of the weights), which one
+// vote of the 128 threads finds; only then are maxima exchanged and O is rescaled.  The sums of the
+// weights stay in the threads, in fp32, until a run ends.
+//
+// Warps: 0 loads the tiles (lanes look up pages and issue one box each), 1 issues the first product,
+// 6 the second (into tensor memory of their own, so neither waits for the other's order), 2-5 are
+// the 128 threads.  S and P have two buffers: the first product of tile i + 1 runs while tile i's
+// weights are made.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,6 +44,17 @@ int kv_check_pointers(const KvCache& c);
 
 namespace {
 
+constexpr int kThreads = 224;
+constexpr int kTile = 128;                       // tokens of a tile
+constexpr int kMaxRows = 32;
+constexpr int kMaxCtas = 160;
+constexpr int kMinTiles = 2;                     // tiles a CTA takes at least
+constexpr int kMaxSlots = 12;
+constexpr int kAtom = kTile * 128;               // 128 tokens x 128 bytes
+constexpr int kPShift = 14;
+constexpr int kOCol = 256;                       // tensor memory: S at 0, O from here
+constexpr uint32_t kTmemCols = 512;
+
 struct AttnParams {
     KvCache c;
     const __nv_bfloat16* q;
@@ -44,28 +64,14 @@ struct AttnParams {
     float scale_log2;        // sm_scale * log2(e)
     int32_t window;          // 0: none
     int32_t G;
-    int* status;
+    int32_t rows;            // R: rows of a row tile
+    int32_t slot_rows;       // rows of a part in the workspace
     float* parts;            // [2 * ctas][slot_rows][D + 2]: output, maximum, sum of a part
-    int32_t slot_rows;
+    int32_t box;             // tokens of one load: the largest power of two that divides a page
+    int32_t slots;           // of the ring
+    uint64_t wait_ns;
+    int* status;
 };
-
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kRows = 16;
-constexpr int kTile = kAttnWarps * kKvBlock;     // tokens of one tile: a block for each warp
-constexpr int kMaxCtas = 640;                    // 148 SMs x 4, rounded up
-constexpr int kMinTiles = 2;                     // tiles a CTA takes at least
-constexpr int kPShift = 13;
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -74,43 +80,10 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // log of the sum l of weights exp2(s - m)
 __device__ __forceinline__ float lse_of(float m, float l)
 {
     return m == -INFINITY && l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
-// 0x80 in each byte of w that is an E4M3 NaN
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
-{
-    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
-
-// One pass over 16 tokens of V: o += w * v.  vr[i] are the bytes of this lane's token i (k slots
-// 2t, 2t + 1, 2t + 8, 2t + 9), NT n-tiles in all.
-template <int NT, int VW>
-__device__ __forceinline__ void mma_v(float (&o)[NT][4], const uint32_t (&vr)[4][VW], uint32_t a0,
-                                      uint32_t a1, uint32_t a2, uint32_t a3)
-{
-#pragma unroll
-    for (int w = 0; w < VW; ++w) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint32_t sel = half ? 0x7362u : 0x5140u;
-            uint32_t b0[2], b1[2];
-            e4m3x4_to_f16(__byte_perm(vr[0][w], vr[1][w], sel), b0[0], b0[1]);
-            e4m3x4_to_f16(__byte_perm(vr[2][w], vr[3][w], sel), b1[0], b1[1]);
-            mma_f16(o[4 * w + 2 * half], a0, a1, a2, a3, b0[0], b1[0]);
-            mma_f16(o[4 * w + 2 * half + 1], a0, a1, a2, a3, b0[1], b1[1]);
-        }
-    }
 }
 
 // ---- how the work is split.  An item is one row tile of one key head of a sequence; sequence b
@@ -130,7 +103,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
     s.first = r.first;
     s.n = r.n;
     s.len = kv_length(p.c, b);
-    s.row_tiles = (s.n * p.G + kRows - 1) / kRows;
+    s.row_tiles = (s.n * p.G + p.rows - 1) / p.rows;
     const int32_t lo = p.window ? max(0, s.len - s.n - p.window + 1) : 0;
     s.tile0 = lo / kTile;
     s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
@@ -143,21 +116,15 @@ __device__ __forceinline__ int64_t seq_tiles(const AttnParams& p, int b)
     return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * s.tiles;
 }
 
-// Where tile `at` of the whole row lies.  total is the row's length.
-struct Place {
-    int b;
-    int64_t before;              // tiles of the sequences before b
-};
-
 struct SplitShared {
-    int64_t warp_sum[kAttnWarps];
-    int64_t before;
+    int64_t warp_sum[8];
+    int64_t before;              // tiles of the sequences before b
     int b;
 };
 
 __device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_t& chunk)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int64_t inc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -169,8 +136,7 @@ __device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_
     __syncthreads();
     chunk = 0;
     int64_t pre = 0;
-#pragma unroll
-    for (int i = 0; i < kAttnWarps; ++i) {
+    for (int i = 0; i < warps; ++i) {
         if (i < warp) pre += sh.warp_sum[i];
         chunk += sh.warp_sum[i];
     }
@@ -178,13 +144,13 @@ __device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_
 }
 
 // Total number of tiles, and (through `pick`, which maps the total to a tile) the sequence that
-// holds that tile.  Called by every thread; Place is valid where pick's tile is below the total.
+// holds that tile, in sh.  Called by every thread.
 template <typename Pick>
-__device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& sh, Pick pick,
-                                             Place& place)
+__device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& sh, Pick pick)
 {
+    const int threads = blockDim.x;
     int64_t total = 0, w = 0, excl = 0, chunk = 0;
-    for (int base = 0; base < p.c.B; base += kAttnThreads) {
+    for (int base = 0; base < p.c.B; base += threads) {
         const int i = base + threadIdx.x;
         w = i < p.c.B ? seq_tiles(p, i) : 0;
         excl = chunk_scan(w, sh, chunk);
@@ -196,14 +162,14 @@ __device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& s
         sh.before = 0;
     }
     __syncthreads();
-    if (p.c.B <= kAttnThreads) {                 // one chunk: it is still in registers
+    if (p.c.B <= threads) {                      // one chunk: it is still in registers
         if (at >= excl && at < excl + w) {
             sh.b = threadIdx.x;
             sh.before = excl;
         }
     } else {
         int64_t carry = 0;
-        for (int base = 0; base < p.c.B; base += kAttnThreads) {
+        for (int base = 0; base < p.c.B; base += threads) {
             const int i = base + threadIdx.x;
             w = i < p.c.B ? seq_tiles(p, i) : 0;
             excl = chunk_scan(w, sh, chunk) + carry;
@@ -215,8 +181,6 @@ __device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& s
         }
     }
     __syncthreads();
-    place.b = sh.b;
-    place.before = sh.before;
     return total;
 }
 
@@ -226,390 +190,738 @@ __device__ __forceinline__ int64_t run_length(int64_t total, int ctas)
     return per < kMinTiles ? kMinTiles : per;
 }
 
-// DP: head dimension rounded up to 64, 128 or 256.
-template <int DP>
-struct Dims {
-    static constexpr int kQWords = DP / 16 * 32 * 4;           // q fragments, 32-bit words
-    static constexpr int kNT = DP / 8;                          // 8-column tiles of the output
-    static constexpr int kVW = DP / 32;                         // words of one token's V chunk(s)
-    static constexpr size_t kSmem = kQWords * 4 + kAttnWarps * kRows * (DP + 4) * 4;
+// A walk over the items (or parts of items) of a run; every role of the CTA makes its own.
+struct Segment {
+    SeqWork sw;
+    int b, h, row_base, nrows;
+    int tile_begin, tile_end;    // token tiles of the sequence
+    bool begins, whole;
 };
 
-template <int DP>
-__global__ void __launch_bounds__(kAttnThreads) fp8kv_attention_kernel(const AttnParams p)
-{
-    using S = Dims<DP>;
-    extern __shared__ uint4 smem[];
-    uint32_t* qs = reinterpret_cast<uint32_t*>(smem);           // [DP/16][32 lanes][4]
-    float* os = reinterpret_cast<float*>(qs + S::kQWords);      // [warps][16][DP + 4]
-    __shared__ float row_fac[kRows];
-    __shared__ float stat_m[kAttnWarps][kRows], stat_l[kAttnWarps][kRows];
-    __shared__ int stat_e[kAttnWarps];
+struct SegmentWalk {
+    int64_t at, end, before;
+    int b;
 
+    __device__ __forceinline__ bool next(const AttnParams& p, Segment& s)
+    {
+        if (at >= end) return false;
+        s.sw = seq_work(p, b);
+        int64_t mine = static_cast<int64_t>(s.sw.row_tiles) * p.c.Hkv * s.sw.tiles;
+        while (at >= before + mine && b + 1 < p.c.B) {
+            before += mine;
+            s.sw = seq_work(p, ++b);
+            mine = static_cast<int64_t>(s.sw.row_tiles) * p.c.Hkv * s.sw.tiles;
+        }
+        const int64_t item = (at - before) / s.sw.tiles;
+        const int seg0 = static_cast<int>((at - before) - item * s.sw.tiles);
+        const int seg1 = static_cast<int>(min(static_cast<int64_t>(s.sw.tiles), seg0 + (end - at)));
+        at += seg1 - seg0;
+        s.b = b;
+        s.begins = seg0 == 0;
+        s.whole = seg0 == 0 && seg1 == s.sw.tiles;
+        s.h = static_cast<int>(item / s.sw.row_tiles);
+        s.row_base = static_cast<int>(item - static_cast<int64_t>(s.h) * s.sw.row_tiles) * p.rows;
+        s.nrows = min(p.rows, s.sw.n * p.G - s.row_base);
+        s.tile_begin = s.sw.tile0 + seg0;
+        s.tile_end = s.sw.tile0 + seg1;
+        return true;
+    }
+};
+
+// ---- PTX
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float (&r)[8])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float (&r)[8])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Barriers of the 128 token threads.
+__device__ __forceinline__ void token_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ bool token_any(bool b)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, 1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(b))
+        : "memory");
+    return r != 0;
+}
+
+// Descriptor of an operand whose rows (the K dimension) hold `row_bytes` = 32, 64 or 128 bytes
+// of the M or N dimension, swizzled over as many bytes; groups of eight rows follow one another.
+__device__ __forceinline__ uint64_t sdesc_mn_major(uint32_t saddr, int row_bytes)
+{
+    const uint64_t layout = row_bytes == 32 ? 6 : row_bytes == 64 ? 4 : 2;
+    uint64_t d = (saddr >> 4) & 0x3FFFu;
+    d |= static_cast<uint64_t>(1) << 16;                          // one atom wide: not used
+    d |= static_cast<uint64_t>(row_bytes * 8 >> 4) << 32;         // next eight rows
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= layout << 61;
+    return d;
+}
+
+// E4M3 x E5M2 -> F32, both operands with their M / N dimension contiguous.
+__host__ __device__ constexpr uint32_t idesc_pv(uint32_t M, uint32_t N)
+{
+    return (1u << 4) | (0u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((N >> 3) << 17) |
+           ((M >> 4) << 24);
+}
+
+// 0x80 in each byte of w that is an E4M3 NaN
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
+{
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Order-preserving map of a float that is not NaN to an int
+__device__ __forceinline__ int ordered(float f)
+{
+    const int i = __float_as_int(f);
+    return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+
+__device__ __forceinline__ float from_ordered(int i)
+{
+    return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
+}
+
+// R: rows of a row tile; ATOMS: 128-byte pieces of a head.
+template <int R, int ATOMS>
+struct Cfg {
+    static constexpr int kNS = (3 * R + 15) / 16 * 16;            // columns of S
+    static constexpr int kNO = 4 * R;                             // columns of O
+    static constexpr int kSlot = ATOMS * kAtom;
+    static constexpr int kQ = ATOMS * kNS * 128;
+    static constexpr int kP = kTile * kNO;                        // one of two buffers
+    static constexpr int kSlots = std::min(kMaxSlots, (222 * 1024 - kQ - 2 * kP) / kSlot);
+    static constexpr int kSmem = 1024 + kSlots * kSlot + kQ + 2 * kP;
+    static_assert(kSlots >= 4, "two tiles in the ring");
+    static_assert(2 * kNS <= kOCol && kOCol + ATOMS * kNO <= static_cast<int>(kTmemCols), "TMEM");
+};
+
+template <int R>
+struct TokenShared {
+    float row_fac[R];                            // scores: sm_scale log2(e) 2^(row's power)
+    int row_pos[R];
+    int wmax[4][R];
+    int we[4];
+    float wsum[4][R];
+    uint32_t nan[R][8];                          // NaN elements of V that a row sees, by d
+};
+
+template <int R, int ATOMS>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const AttnParams p)
+{
+    using C = Cfg<R, ATOMS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* qs = ring + C::kSlots * C::kSlot;                    // [ATOMS][kNS][128]
+    uint8_t* ps = qs + C::kQ;                                     // [2][128 tokens][kNO]
+    __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+    __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full, fin[2];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
     __shared__ SplitShared split;
+    __shared__ TokenShared<R> sh;
+    volatile int* abort_flag = &abort_word;
 
     const KvCache& c = p.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(s_free + i, 4);
+            mbar_init(p_full + i, 4);
+            mbar_init(p_done + i, 1);
+            mbar_init(fin + i, 1);
+        }
+        mbar_init(&q_full, 4);
+        abort_word = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_holder, kTmemCols);
+        tmem_relinquish();
+    }
     griddep_wait();
     griddep_launch_dependents();
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
-    Place place;
     const int ctas = gridDim.x;
     const int64_t total = find_tile(
-        p, split, [&](int64_t n) { return blockIdx.x * run_length(n, ctas); }, place);
-    const int64_t per = run_length(total, ctas);
-    int64_t at = blockIdx.x * per;
-    const int64_t end = min(at + per, total);
-    int b = place.b;
-    int64_t before = place.before;
-
-  while (at < end) {
-    SeqWork sw = seq_work(p, b);
-    int64_t mine = static_cast<int64_t>(sw.row_tiles) * c.Hkv * sw.tiles;
-    while (at >= before + mine && b + 1 < c.B) {
-        before += mine;
-        sw = seq_work(p, ++b);
-        mine = static_cast<int64_t>(sw.row_tiles) * c.Hkv * sw.tiles;
-    }
-    const int64_t item = (at - before) / sw.tiles;
-    const int seg0 = static_cast<int>((at - before) - item * sw.tiles);
-    const int seg1 = static_cast<int>(min(static_cast<int64_t>(sw.tiles), seg0 + (end - at)));
-    at += seg1 - seg0;
-    const bool whole = seg0 == 0 && seg1 == sw.tiles;
-    const int h = static_cast<int>(item / sw.row_tiles);
-    const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * kRows;
-    const int nrows = min(kRows, sw.n * p.G - row_base);
-    const int32_t len = sw.len;
-    const int32_t start = len - sw.n;                            // position of the first new token
-    __syncthreads();                                             // the shared buffers are free
-
-    // ---- q: f16 fragments in shared memory
-    for (int i = 0; i < kRows / kAttnWarps; ++i) {
-        const int r = warp * (kRows / kAttnWarps) + i;
-        const int rr = row_base + r, tok = rr / p.G, head = rr - tok * p.G;
-        const bool ok = r < nrows;
-        const __nv_bfloat16* src = p.q + (sw.first + tok) * p.q_stride +
-                                   static_cast<int64_t>(h * p.G + head) * c.D;
-        uint32_t w[DP / 64];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
-            const int d = 2 * (lane + 32 * j);
-            w[j] = ok && d < c.D ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
-            amax = max(amax, max(w[j] << 16 & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-        }
-        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        int e = static_cast<int>(amax >> 23);                    // biased exponent of the largest
-        e = e < 15 ? 15 : e;
-        const float up = kv_pow2(254 - e + 14 > 254 ? 254 : 254 - e + 14);   // 2^(14 - (e - 127))
-        if (lane == 0) row_fac[r] = p.scale_log2 * kv_pow2(e - 14);
-#pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
-            const int d = 2 * (lane + 32 * j);
-            const int chunk = d >> 4, cg = chunk >> 2, ct = chunk & 3;
-            const int jj = (d & 15) >> 2, hi = (d >> 1) & 1;
-            qs[((cg * 4 + jj) * 32 + (r & 7) * 4 + ct) * 4 + (r >> 3) + 2 * hi] =
-                pack_f16(bf16lo_to_f32(w[j]) * up, bf16hi_to_f32(w[j]) * up);
-        }
-    }
+        p, split, [&](int64_t n) { return blockIdx.x * run_length(n, ctas); });
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = tmem_holder;
+    const int64_t per = run_length(total, ctas);
+    SegmentWalk walk;
+    walk.at = blockIdx.x * per;
+    walk.end = min(walk.at + per, total);
+    walk.before = split.before;
+    walk.b = split.b;
+    Segment seg;
 
-    const float fac0 = row_fac[g], fac1 = row_fac[g + 8];
-    const int pos0 = start + (row_base + min(g, nrows - 1)) / p.G;
-    const int pos1 = start + (row_base + min(g + 8, nrows - 1)) / p.G;
-    const int pos_lo = start + row_base / p.G, pos_hi = start + (row_base + nrows - 1) / p.G;
-    const int first_tok = p.window ? max(0, pos_lo - p.window + 1) : 0;
-    const int blk_begin = max(first_tok / kKvBlock, (sw.tile0 + seg0) * kAttnWarps);
-    const int blk_end = min((pos_hi + kKvBlock) / kKvBlock, (sw.tile0 + seg1) * kAttnWarps);
-
-    float o[S::kNT][4];
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        const int boxes = kTile / p.box, page = c.page_blocks * kKvBlock;
+        const uint32_t box_bytes = p.box * 128;
+        int slot = 0, used = 0;
+        uint32_t phase = 1;                      // of an empty slot's barrier, for the first round
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+            const int len = seg.sw.len;
+            const int lo = p.window ? max(0, len - seg.sw.n - p.window + 1) : 0;
+            const int32_t* row = c.table + static_cast<int64_t>(seg.b) * c.max_pages;
+            // lane i takes box i of a tile; -1: nothing to load
+            const auto page_of = [&](int tile) {
+                const int tok = tile * kTile + lane * p.box;
+                return lane < boxes && tile < seg.tile_end && tok < len && tok + p.box > lo
+                           ? __ldg(row + tok / page)
+                           : -1;
+            };
+            int32_t next_page = page_of(seg.tile_begin);
+            for (int tile = seg.tile_begin; ok && tile < seg.tile_end; ++tile) {
+                const int32_t id = next_page;
+                next_page = page_of(tile + 1);
+                const int tok = tile * kTile + lane * p.box;
+                const bool mine = id >= 0 && id < c.pages;
+                if (!mine && id != -1) kv_report_bad_batch(p.status);
+                if (id == -1 && lane < boxes && tok < len && tok + p.box > lo)
+                    kv_report_bad_batch(p.status);
+                const uint32_t bytes =
+                    __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes * ATOMS;
+                const int32_t y = tok % page, z = mine ? id * c.Hkv + seg.h : 0;
 #pragma unroll
-    for (int i = 0; i < S::kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    int e_ref = -1, e_top = 0;
-
-    for (int blk = blk_begin + warp; blk < blk_end; blk += kAttnWarps) {
-        const int pi = blk / c.page_blocks, in_page = blk - pi * c.page_blocks;
-        const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + pi);
-        const bool page_ok = page >= 0 && page < c.pages;
-        if (!page_ok) {
-            if (lane == 0) kv_report_bad_batch(p.status);
-            continue;
-        }
-        const int64_t group = (static_cast<int64_t>(page) * c.Hkv + h) * c.page_blocks + in_page;
-        const uint8_t* kp = c.k + group * kKvBlock * c.D;
-        const uint8_t* vp = c.v + group * kKvBlock * c.D;
-        uint4 kr[2][DP / 64];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int cg = 0; cg < DP / 64; ++cg) {
-                const int d = (cg * 4 + t) * 16;
-                kr[nt][cg] = d < c.D ? __ldg(reinterpret_cast<const uint4*>(
-                                           kp + (nt * 8 + g) * c.D + d))
-                                     : make_uint4(0, 0, 0, 0);
-            }
-        uint32_t vr[4][S::kVW];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* row = vp + (2 * t + (i & 1) + (i >> 1) * 8) * c.D;
-            if constexpr (DP == 64) {
-                const uint2 x = 8 * g < c.D ? __ldg(reinterpret_cast<const uint2*>(row + 8 * g))
-                                            : make_uint2(0, 0);
-                vr[i][0] = x.x;
-                vr[i][1] = x.y;
-            } else {
-#pragma unroll
-                for (int hh = 0; hh < DP / 128; ++hh) {
-                    const int d = 128 * hh + 16 * g;
-                    const uint4 x = d < c.D ? __ldg(reinterpret_cast<const uint4*>(row + d))
-                                            : make_uint4(0, 0, 0, 0);
-                    vr[i][4 * hh] = x.x;
-                    vr[i][4 * hh + 1] = x.y;
-                    vr[i][4 * hh + 2] = x.z;
-                    vr[i][4 * hh + 3] = x.w;
-                }
-            }
-        }
-        const int ek = min(static_cast<int>(__ldg(c.k_scale + group)), kKvMaxExp);
-        const int ev = min(static_cast<int>(__ldg(c.v_scale + group)), kKvMaxExp);
-
-        // ---- scores
-        float s[2][4] = {};
-#pragma unroll
-        for (int cg = 0; cg < DP / 64; ++cg) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 a = reinterpret_cast<const uint4*>(qs)[(cg * 4 + j) * 32 + lane];
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint32_t w = j == 0   ? kr[nt][cg].x
-                                       : j == 1 ? kr[nt][cg].y
-                                       : j == 2 ? kr[nt][cg].z
-                                                : kr[nt][cg].w;
-                    uint32_t b0, b1;
-                    e4m3x4_to_f16(w, b0, b1);
-                    mma_f16(s[nt], a.x, a.y, a.z, a.w, b0, b1);
-                }
-            }
-        }
-        const float kf = kv_pow2(ek);
-        const float f0 = fac0 * kf, f1 = fac1 * kf;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            s[nt][0] *= f0;
-            s[nt][1] *= f0;
-            s[nt][2] *= f1;
-            s[nt][3] *= f1;
-        }
-        const int tok0 = blk * kKvBlock;
-        const bool edge = tok0 + kKvBlock - 1 > pos_lo || (p.window && tok0 <= pos_hi - p.window);
-        uint32_t seen = 0xFFu;                    // bit 4 * nt + i: s[nt][i] is in the mask
-        if (edge) {
-            seen = 0;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = tok0 + nt * 8 + 2 * t + (i & 1);
-                    const int pos = i < 2 ? pos0 : pos1;
-                    const bool in = tok <= pos && (p.window == 0 || tok > pos - p.window);
-                    if (in) seen |= 1u << (4 * nt + i);
-                    if (!in) s[nt][i] = -INFINITY;
-                }
-        }
-
-        // ---- running maximum and sum
-        float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-#pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, x));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xFFFFFFFFu, n1, x));
-        }
-        n0 = fmaxf(n0, m0);
-        n1 = fmaxf(n1, m1);
-        int e_new = e_ref;
-        e_top = max(e_top, ev);
-        if (e_ref < 0 || ev > e_ref + 2 || ev < e_ref - 10) e_new = max(ev, e_top - 40);
-        if (__any_sync(0xFFFFFFFFu, n0 != m0 || n1 != m1) || e_new != e_ref) {
-            const float de = e_ref < 0 ? 0.0f : static_cast<float>(e_ref - e_new);
-            const float c0 = m0 == -INFINITY ? 0.0f : ex2(m0 - n0);
-            const float c1 = m1 == -INFINITY ? 0.0f : ex2(m1 - n1);
-            l0 *= c0;
-            l1 *= c1;
-            const float x0 = c0 * ex2(de), x1 = c1 * ex2(de);
-#pragma unroll
-            for (int i = 0; i < S::kNT; ++i) {
-                o[i][0] *= x0;
-                o[i][1] *= x0;
-                o[i][2] *= x1;
-                o[i][3] *= x1;
-            }
-            m0 = n0;
-            m1 = n1;
-            e_ref = e_new;
-        }
-        const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            s[nt][0] = ex2(s[nt][0] - z0);
-            s[nt][1] = ex2(s[nt][1] - z0);
-            s[nt][2] = ex2(s[nt][2] - z1);
-            s[nt][3] = ex2(s[nt][3] - z1);
-            l0 += s[nt][0] + s[nt][1];
-            l1 += s[nt][2] + s[nt][3];
-        }
-        const int we = 127 + kPShift + ev - e_ref;
-        const float wf = we > 0 ? kv_pow2(we) : 0.0f;
-        const uint32_t a0 = pack_f16(s[0][0] * wf, s[0][1] * wf);
-        const uint32_t a1 = pack_f16(s[0][2] * wf, s[0][3] * wf);
-        const uint32_t a2 = pack_f16(s[1][0] * wf, s[1][1] * wf);
-        const uint32_t a3 = pack_f16(s[1][2] * wf, s[1][3] * wf);
-
-        // ---- values.  A masked token's weight is 0, but 0 * NaN is not: where the mask cuts the
-        // block, bytes of tokens that no row sees are cleared, and NaNs of tokens that only some
-        // rows see are counted with 0 / 1 weights and put into just those rows.
-        if (edge) {
-            uint32_t nan = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = tok0 + 2 * t + (i & 1) + (i >> 1) * 8;
-                const bool any = tok <= pos_hi && (p.window == 0 || tok > pos_lo - p.window);
-#pragma unroll
-                for (int w = 0; w < S::kVW; ++w) {
-                    vr[i][w] = any ? vr[i][w] : 0u;
-                    nan |= nan_bytes(vr[i][w]);
-                }
-            }
-            if (__any_sync(0xFFFFFFFFu, nan != 0)) {
-                const uint32_t one = 0x3C00u;                    // 1.0 in f16
-                const auto bits = [&](int i) {
-                    return ((seen >> i) & 1u) * one | ((seen >> (i + 1)) & 1u) * (one << 16);
-                };
-                const uint32_t i0 = bits(0), i1 = bits(2), i2 = bits(4), i3 = bits(6);
-                uint32_t mark[4][S::kVW];                        // 2.0 in E4M3 where V is NaN
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int w = 0; w < S::kVW; ++w) {
-                        const uint32_t n = nan_bytes(vr[i][w]);
-                        mark[i][w] = n >> 1;
-                        vr[i][w] &= ~((n >> 7) * 0xFFu);
+                for (int kv = 0; kv < 2; ++kv) {
+                    bool got = true;
+                    if (lane == 0) {
+                        got = mbar_wait(empty + slot, phase, abort_flag, p.wait_ns, p.status, 111);
+                        if (got) mbar_arrive_expect_tx(full + slot, bytes);
                     }
-                float count[S::kNT][4] = {};
-                mma_v<S::kNT, S::kVW>(count, mark, i0, i1, i2, i3);
+                    ok = __shfl_sync(0xFFFFFFFFu, got, 0);
+                    if (!ok) break;
+                    if (mine)
+                        for (int a = 0; a < ATOMS; ++a)
+                            tma_load_3d(ring + slot * C::kSlot + a * kAtom + lane * box_bytes,
+                                        kv ? &tm_v : &tm_k, full + slot, a * 128, y, z);
+                    ++used;
+                    if (++slot == C::kSlots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+        // the last loads must land before shared memory is freed
+        __syncwarp();
+        if (lane == 0)
+            for (int i = max(0, used - C::kSlots); i < used; ++i)
+                drain_wait(full + i % C::kSlots, i / C::kSlots & 1, p.wait_ns, p.status);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ S = K Q^T
+        if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3(kTile, C::kNS);
+            const int ksteps = (c.D + 31) / 32;
+            int slot = 0, i = 0, nseg = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            while (ok && walk.next(p, seg)) {
+                ok = mbar_wait(&q_full, nseg & 1, abort_flag, p.wait_ns, p.status, 112);
+                ++nseg;
+                for (int tile = seg.tile_begin; ok && tile < seg.tile_end; ++tile, ++i) {
+                    ok = mbar_wait(s_free + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
+                                   p.status, 113) &&
+                         mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 114);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint64_t a = sdesc_kmajor_sw128(smem_u32(ring + slot * C::kSlot));
+                    uint64_t b = sdesc_kmajor_sw128(smem_u32(qs));
+#pragma unroll 1
+                    for (int k = 0; k < ksteps; ++k) {
+                        mma_f8f6f4(tbase + (i & 1) * C::kNS, a, b, idesc, k);
+                        // 32 bytes a step, four steps to a 128-byte atom; units of 16 bytes
+                        a += (k & 3) == 3 ? kAtom / 16 - 6 : 2;
+                        b += (k & 3) == 3 ? C::kNS * 8 - 6 : 2;
+                    }
+                    tc_commit(empty + slot);
+                    tc_commit(s_full + (i & 1));
+                    slot += 2;
+                    if (slot >= C::kSlots) {
+                        slot -= C::kSlots;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------------------ O += V^T P^T
+        if (lane == 0) {
+            const uint32_t idesc = idesc_pv(kTile, C::kNO);
+            int slot = 1, i = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            while (ok && walk.next(p, seg)) {
+                for (int tile = seg.tile_begin; ok && tile < seg.tile_end; ++tile, ++i) {
+                    ok = mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 115) &&
+                         mbar_wait(p_full + (i & 1), i >> 1 & 1, abort_flag, p.wait_ns, p.status,
+                                   116);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(ring + slot * C::kSlot);
+                    const uint64_t b = sdesc_mn_major(smem_u32(ps + (i & 1) * C::kP), C::kNO);
 #pragma unroll
-                for (int i = 0; i < S::kNT; ++i)
+                    for (int at = 0; at < ATOMS; ++at) {
+                        const uint64_t ad = sdesc_mn_major(a + at * kAtom, 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)      // 32 tokens each
+                            mma_f8f6f4(tbase + kOCol + at * C::kNO, ad + k * (32 * 128 / 16),
+                                       b + k * (32 * C::kNO / 16), idesc,
+                                       tile > seg.tile_begin || k > 0);
+                    }
+                    tc_commit(empty + slot);
+                    tc_commit(p_done + (i & 1));
+                    slot += 2;
+                    if (slot >= C::kSlots) {
+                        slot -= C::kSlots;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ the token threads
+        const int q = warp & 3, t = q * 32 + lane;               // TMEM lane, and token of a tile
+        const uint32_t tlane = tbase + (static_cast<uint32_t>(q * 32) << 16);
+        int i = 0, slot = 1;
+        uint32_t phase = 0;                                       // of this tile's V slot
+        bool ok = true;
+        while (walk.next(p, seg)) {
+            const int len = seg.sw.len, nrows = seg.nrows;
+            const int start = len - seg.sw.n;                     // position of the first new token
+            const int pos_lo = start + seg.row_base / p.G;
+            const int pos_hi = start + (seg.row_base + nrows - 1) / p.G;
+            const int lo = p.window ? max(0, pos_lo - p.window + 1) : 0;
+            const int32_t* table = c.table + static_cast<int64_t>(seg.b) * c.max_pages;
+
+            // scales: the page of tile i + 2 and the scales of tile i + 1 are on their way during tile i
+            const auto page_of = [&](int tile) {
+                const int tok = tile * kTile + t;
+                return tile < seg.tile_end && tok < len && tok >= lo
+                           ? __ldg(table + tok / kKvBlock / c.page_blocks)
+                           : -1;
+            };
+            const auto scales_of = [&](int tile, int32_t id) {    // key scale | value scale << 8, -1: none
+                if (id < 0 || id >= c.pages) return -1;
+                const int blk = (tile * kTile + t) / kKvBlock;
+                const int64_t at =
+                    (static_cast<int64_t>(id) * c.Hkv + seg.h) * c.page_blocks + blk % c.page_blocks;
+                return __ldg(c.k_scale + at) | __ldg(c.v_scale + at) << 8;
+            };
+            const int32_t page0 = page_of(seg.tile_begin);
+            int32_t page1 = page_of(seg.tile_begin + 1);
+            int scale0 = scales_of(seg.tile_begin, page0);
+
+            // ---- q: three E4M3 rows each
+            for (int r = q; r < R; r += 4) {
+                const int rr = seg.row_base + r, tok = rr / p.G, head = rr - tok * p.G;
+                const bool in = r < nrows;
+                const __nv_bfloat16* src = p.q + (seg.sw.first + tok) * p.q_stride +
+                                           static_cast<int64_t>(seg.h * p.G + head) * c.D;
+                uint32_t w[2 * ATOMS];
+                uint32_t amax = 0;
+#pragma unroll
+                for (int j = 0; j < 2 * ATOMS; ++j) {
+                    const int d = 2 * (lane + 32 * j);
+                    w[j] = in && d < c.D ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
+                    amax = max(amax, max(w[j] << 16 & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+                }
+                amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+                const int e = max(static_cast<int>(amax >> 23), 8);   // biased exponent of the largest
+                const float up = kv_pow2(min(254, 261 - e));          // 2^(7 - (e - 127))
+                if (lane == 0) {
+                    sh.row_fac[r] = amax < 0x7F800000u ? p.scale_log2 * kv_pow2(e - 7) : NAN;
+                    sh.row_pos[r] = start + (seg.row_base + min(r, nrows - 1)) / p.G;
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * ATOMS; ++j) {
+                    const int d = 2 * (lane + 32 * j);
+                    float x0 = bf16lo_to_f32(w[j]) * up, x1 = bf16hi_to_f32(w[j]) * up;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t code = cvt_e4m3x2(x0, x1);
+                        const int n = k * R + r, byte = d & 127;
+                        *reinterpret_cast<uint16_t*>(qs + (d >> 7) * C::kNS * 128 + n * 128 +
+                                                     (((byte >> 4) ^ (n & 7)) << 4) + (byte & 15)) =
+                            static_cast<uint16_t>(code);
+                        uint32_t h, unused;
+                        e4m3x4_to_f16(code, h, unused);
+                        float y0, y1;
+                        f16x2_to_f32(h, y0, y1);
+                        x0 = (x0 - y0) * 16.0f;
+                        x1 = (x1 - y1) * 16.0f;
+                    }
+                }
+            }
+            for (int k = t; k < R * 8; k += 128) sh.nan[k >> 3][k & 7] = 0;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+            token_sync();
+
+            float m[R], l[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                m[r] = -INFINITY;
+                l[r] = 0.0f;
+            }
+            int e_ref = -1, e_top = 0;
+            bool any_nan = false;
+
+            for (int tile = seg.tile_begin; tile < seg.tile_end; ++tile, ++i) {
+                const int scale = scale0;
+                scale0 = scales_of(tile + 1, page1);
+                page1 = page_of(tile + 2);
+                const int tok = tile * kTile + t;
+                // a token that no row sees (or whose page is bad) has scale -1
+                const bool seen = scale >= 0 && tok <= pos_hi;
+                const int ev = seen ? min(scale >> 8, kKvMaxExp) : -1;
+                const float kf = kv_pow2(seen ? min(scale & 255, kKvMaxExp) : 127);
+                const bool edge = tile * kTile + kTile - 1 > pos_lo ||
+                                  (p.window && tile * kTile <= pos_hi - p.window);
+
+                ok = mbar_wait(s_full + (i & 1), i >> 1 & 1, abort_flag, p.wait_ns, p.status, 117) &&
+                     ok;
+                if (token_any(!ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                __syncwarp();
+                float s[R];
+                bool exceed = ev > e_ref || (ev > 0 && ev < e_ref - 10);
+#pragma unroll
+                for (int r0 = 0; r0 < R; r0 += 8) {
+                    float a[3][8];
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        tmem_ld_x8(tlane + (i & 1) * C::kNS + k * R + r0, a[k]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        s[r0 + j] = fmaf(fmaf(a[2][j], 0.0625f, a[1][j]), 0.0625f, a[0][j]) *
+                                    sh.row_fac[r0 + j] * kf;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free + (i & 1));
+                if (!seen) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) s[r] = -INFINITY;
+                } else if (edge) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int pos = sh.row_pos[r];
+                        if (tok > pos || (p.window && tok <= pos - p.window)) s[r] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) exceed = exceed || s[r] > m[r] + 1.0f;
+
+                if (token_any(exceed)) {
+                    // ---- new reference maxima and exponent; O follows
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int v = __reduce_max_sync(
+                            0xFFFFFFFFu, ordered(s[r] == s[r] ? s[r] : -INFINITY));
+                        if (lane == 0) sh.wmax[q][r] = v;
+                    }
+                    const int we = __reduce_max_sync(0xFFFFFFFFu, ev);
+                    if (lane == 0) sh.we[q] = we;
+                    token_sync();
+                    const int e_tile = max(max(sh.we[0], sh.we[1]), max(sh.we[2], sh.we[3]));
+                    int e_new = e_ref;
+                    e_top = max(e_top, e_tile);
+                    if (e_ref < 0 || e_tile > e_ref || (e_tile >= 0 && e_tile < e_ref - 10))
+                        e_new = max(max(e_tile, e_top - 40), 0);
+                    const float ef = e_ref < 0 ? 0.0f : ex2(static_cast<float>(e_ref - e_new));
+                    e_ref = e_new;
+                    float f[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float v = from_ordered(max(max(sh.wmax[0][r], sh.wmax[1][r]),
+                                                         max(sh.wmax[2][r], sh.wmax[3][r])));
+                        const float n = fmaxf(m[r], v);
+                        f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - n);
+                        l[r] *= f[r];
+                        f[r] *= ef;
+                        m[r] = n;
+                    }
+                    if (tile > seg.tile_begin) {
+                        ok = mbar_wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag,
+                                       p.wait_ns, p.status, 118) &&
+                             ok;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < ATOMS * 4; ++k)
+#pragma unroll
+                            for (int r0 = 0; r0 < R; r0 += 8) {
+                                float o[8];
+                                __syncwarp();
+                                tmem_ld_x8(tlane + kOCol + k * R + r0, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] *= f[r0 + j];
+                                tmem_st_x8(tlane + kOCol + k * R + r0, o);
+                            }
+                        tmem_st_wait();
+                    }
+                }
+
+                // ---- weights, their sums, and their four E5M2 terms
+                ok = mbar_wait(p_done + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns, p.status,
+                               119) &&
+                     ok;
+                const int we = 127 + kPShift + ev - e_ref;
+                const float wf = seen && we > 0 ? kv_pow2(we) : 0.0f;
+                uint8_t* pt = ps + (i & 1) * C::kP + t * C::kNO;
+#pragma unroll
+                for (int r0 = 0; r0 < R; r0 += 16) {
+                    constexpr int kW = R < 16 ? R : 16;
+                    uint32_t h[kW / 2];
+#pragma unroll
+                    for (int j = 0; j < kW; j += 2) {
+                        const int r = r0 + j;
+                        const float z0 = m[r] == -INFINITY ? 0.0f : m[r];
+                        const float z1 = m[r + 1] == -INFINITY ? 0.0f : m[r + 1];
+                        const float p0 = ex2(s[r] - z0), p1 = ex2(s[r + 1] - z1);
+                        l[r] += p0;
+                        l[r + 1] += p1;
+                        h[j / 2] = pack_f16(p0 * wf, p1 * wf);
+                    }
+                    uint32_t bytes[4][kW / 4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                        for (int j = 0; j < kW / 4; ++j)
+                            bytes[k][j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
+#pragma unroll
+                        for (int j = 0; j < kW / 2; ++j)
+                            h[j] = sub_f16x2(h[j], h[j] & 0xFF00FF00u);
+                    }
+                    // 16-byte chunks of the token's row, swizzled over its 32, 64 or 128 bytes
+                    if constexpr (R == 8) {
+                        const int x = (t >> 2) & 1;
+                        *reinterpret_cast<uint4*>(pt + 16 * x) =
+                            make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
+                        *reinterpret_cast<uint4*>(pt + 16 * (x ^ 1)) =
+                            make_uint4(bytes[2][0], bytes[2][1], bytes[3][0], bytes[3][1]);
+                    } else {
+                        const int x = R == 16 ? (t >> 1) & 3 : t & 7;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(pt + 16 * ((k * (R / 16) + r0 / 16) ^ x)) =
+                                make_uint4(bytes[k][0], bytes[k][1], bytes[k][2], bytes[k][3]);
+                    }
+                }
+
+                // ---- A masked token's weight is 0, but 0 * NaN is not: the values of a token that no
+                // row sees are cleared, and NaNs of one that only some rows see are taken out and
+                // noted for just those rows.
+                if (!seen || edge) {
+                    ok = mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 120) && ok;
+                    uint8_t* v = ring + slot * C::kSlot + t * 128;
+#pragma unroll 1
+                    for (int a = 0; a < ATOMS; ++a)
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
+                            uint4* at = reinterpret_cast<uint4*>(v + a * kAtom + 16 * (k ^ (t & 7)));
+                            if (!seen) {
+                                *at = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            uint4 x = *at;
+                            const uint32_t n[4] = {nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z),
+                                                   nan_bytes(x.w)};
+                            if ((n[0] | n[1] | n[2] | n[3]) == 0) continue;
+                            uint32_t bits = 0;                    // of the 16 elements
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) bits |= (n[j >> 2] >> (8 * (j & 3) + 7) & 1u) << j;
+                            for (int r = 0; r < R; ++r) {
+                                const int pos = sh.row_pos[r];
+                                if (tok <= pos && (p.window == 0 || tok > pos - p.window))
+                                    atomicOr(&sh.nan[r][a * 4 + (k >> 1)], bits << (16 * (k & 1)));
+                            }
+                            x.x &= ~((n[0] >> 7) * 0xFFu);
+                            x.y &= ~((n[1] >> 7) * 0xFFu);
+                            x.z &= ~((n[2] >> 7) * 0xFFu);
+                            x.w &= ~((n[3] >> 7) * 0xFFu);
+                            *at = x;
+                            any_nan = true;
+                        }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + (i & 1));
+                slot += 2;
+                if (slot >= C::kSlots) {
+                    slot -= C::kSlots;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) break;
+
+            // ---- end of the segment: sums over the tokens, then this thread's d of every row
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], x);
+                if (lane == 0) sh.wsum[q][r] = l[r];
+            }
+            ok = mbar_wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag, p.wait_ns, p.status,
+                           121) &&
+                 ok;
+            const bool nans = token_any(any_nan);                 // also: the sums are written
+            tc_fence_after();
+            const float back = 1.0f / (1 << kPShift), unit = kv_pow2(max(e_ref, 0));
+#pragma unroll
+            for (int r0 = 0; r0 < R; r0 += 8) {
+                if (r0 >= nrows) break;
+#pragma unroll
+                for (int a = 0; a < ATOMS; ++a) {
+                    float o[4][8];
+                    __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (count[i][k] > 0.0f) o[i][k] = NAN;
+                        tmem_ld_x8(tlane + kOCol + a * C::kNO + k * R + r0, o[k]);
+                    tmem_ld_wait();
+                    const int d = a * 128 + t;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = r0 + j;
+                        if (r >= nrows) break;
+                        const float sum =
+                            sh.wsum[0][r] + sh.wsum[1][r] + sh.wsum[2][r] + sh.wsum[3][r];
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        float x = ((o[3][j] + o[2][j]) + (o[1][j] + o[0][j])) * (inv * back) * unit;
+                        if (nans && (sh.nan[r][d >> 5] >> (d & 31) & 1u)) x = NAN;
+                        const int rr = seg.row_base + r, tok = rr / p.G;
+                        const int64_t row = static_cast<int64_t>(seg.sw.first + tok) * c.Hq +
+                                            seg.h * p.G + rr - tok * p.G;
+                        if (seg.whole) {
+                            if (d < c.D) p.out[row * c.D + d] = __float2bfloat16_rn(x);
+                            if (p.lse && d == 0) p.lse[row] = lse_of(m[r], sum);
+                        } else {
+                            float* part = p.parts +
+                                          (static_cast<int64_t>(2 * blockIdx.x + seg.begins) *
+                                               p.slot_rows +
+                                           r) * (c.D + 2);
+                            if (d < c.D) part[d] = x;
+                            if (d == 0) {
+                                part[c.D] = m[r];
+                                part[c.D + 1] = sum;
+                            }
+                        }
+                    }
+                }
             }
+            tc_fence_before();
+            token_sync();                        // O, the sums and q's rows are free
         }
-        mma_v<S::kNT, S::kVW>(o, vr, a0, a1, a2, a3);
     }
 
-    // ---- join the warps: common maximum, then the weighted sum of their outputs
-#pragma unroll
-    for (int x = 1; x < 4; x <<= 1) {
-        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, x);
-        l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, x);
+    // ---------------------------------------------------------------- teardown
+    __syncwarp();
+    if ((warp == 1 || warp == 6) && lane == 0) {
+        tc_commit(fin + (warp == 6));
+        drain_wait(fin + (warp == 6), 0, p.wait_ns, p.status);
     }
-    if (t == 0) {
-        stat_m[warp][g] = m0;
-        stat_m[warp][g + 8] = m1;
-        stat_l[warp][g] = l0;
-        stat_l[warp][g + 8] = l1;
-    }
-    if (lane == 0) stat_e[warp] = e_ref < 0 ? 0 : e_ref;
-    {
-        float* ow = os + warp * kRows * (DP + 4);
-#pragma unroll
-        for (int i = 0; i < S::kNT; ++i) {
-            // column of B fragment n: DP 64: 8 n + i ; else 128 (i / 16) + 16 n + i % 16
-            const int d0 = DP == 64 ? 16 * t + i : (i >> 4) * 128 + 32 * t + (i & 15);
-            const int d1 = d0 + (DP == 64 ? 8 : 16);
-            ow[g * (DP + 4) + d0] = o[i][0];
-            ow[g * (DP + 4) + d1] = o[i][1];
-            ow[(g + 8) * (DP + 4) + d0] = o[i][2];
-            ow[(g + 8) * (DP + 4) + d1] = o[i][3];
-        }
-    }
+    tc_fence_before();
     __syncthreads();
-    for (int r = warp; r < nrows; r += kAttnWarps) {
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, stat_m[w][r]);
-        const float z = m == -INFINITY ? 0.0f : m;
-        float f[kAttnWarps];
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
-            f[w] = ex2(stat_m[w][r] - z);
-            l += stat_l[w][r] * f[w];
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int rr = row_base + r, tok = rr / p.G, head = h * p.G + rr - tok * p.G;
-        const int64_t row = static_cast<int64_t>(sw.first + tok) * c.Hq + head;
-        float* part = p.parts + (static_cast<int64_t>(2 * blockIdx.x + (seg0 == 0)) * p.slot_rows +
-                                 r) * (c.D + 2);
-        for (int d = 2 * lane; d < c.D; d += 64) {
-            float x = 0.0f, y = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                const float* ow = os + (w * kRows + r) * (DP + 4) + d;
-                const float f1 = f[w] * inv * (1.0f / (1 << kPShift)), f2 = kv_pow2(stat_e[w]);
-                x += ow[0] * f1 * f2;
-                y += ow[1] * f1 * f2;
-            }
-            if (whole)
-                *reinterpret_cast<__nv_bfloat162*>(p.out + row * c.D + d) =
-                    __floats2bfloat162_rn(x, y);
-            else
-                *reinterpret_cast<float2*>(part + d) = make_float2(x, y);
-        }
-        if (lane == 0) {
-            if (!whole) {
-                part[c.D] = m;
-                part[c.D + 1] = l;
-            } else if (p.lse) {
-                p.lse[row] = lse_of(m, l);
-            }
-        }
-    }
-  }
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, kTmemCols);
 }
 
 // Adds the parts of the item that CTA blockIdx.x of the attention kernel began and did not end
 // (if it did): part i weighs l_i 2^(m_i - m), in the order of the tokens.  One warp takes one row.
-__global__ void __launch_bounds__(kAttnThreads)
-    fp8kv_join_kernel(const AttnParams p)
+constexpr int kJoinThreads = 128;
+
+__global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnParams p)
 {
     __shared__ SplitShared split;
     const KvCache& c = p.c;
     const int ctas = gridDim.x;
-    Place place;
     int64_t last = 0;
-    const int64_t total = find_tile(
-        p, split,
-        [&](int64_t n) {
-            last = min((blockIdx.x + int64_t{1}) * run_length(n, ctas), n) - 1;
-            return last;
-        },
-        place);
+    const int64_t total = find_tile(p, split, [&](int64_t n) {
+        last = min((blockIdx.x + int64_t{1}) * run_length(n, ctas), n) - 1;
+        return last;
+    });
     const int64_t per = run_length(total, ctas);
     const int64_t begin = blockIdx.x * per;
     griddep_wait();
     if (begin >= total) return;
-    const SeqWork sw = seq_work(p, place.b);
-    const int64_t item = (last - place.before) / sw.tiles;
-    const int64_t s0 = place.before + item * sw.tiles, s1 = s0 + sw.tiles;   // the item's tiles
+    const SeqWork sw = seq_work(p, split.b);
+    const int64_t item = (last - split.before) / sw.tiles;
+    const int64_t s0 = split.before + item * sw.tiles, s1 = s0 + sw.tiles;   // the item's tiles
     if (s0 < begin || s1 <= last + 1) return;
     const int parts = static_cast<int>((s1 - 1) / per - blockIdx.x) + 1;
     const int h = static_cast<int>(item / sw.row_tiles);
-    const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * kRows;
-    const int r = blockIdx.y * kAttnWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= min(kRows, sw.n * p.G - row_base)) return;
+    const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * p.rows;
+    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= min(p.rows, sw.n * p.G - row_base)) return;
     const int64_t step = static_cast<int64_t>(2) * p.slot_rows * (c.D + 2);
     // part 0 is the second slot of this CTA, part i > 0 the first slot of CTA blockIdx.x + i
     const float* first = p.parts + (static_cast<int64_t>(2 * blockIdx.x + 1) * p.slot_rows + r) *
@@ -622,17 +934,31 @@ __global__ void __launch_bounds__(kAttnThreads)
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const float z = m == -INFINITY ? 0.0f : m;
     float l = 0.0f, x[8] = {};
-    for (int i = 0; i < parts; ++i) {
-        const float* part = i ? rest + i * step : first;
-        const float w = part[c.D + 1] * ex2(part[c.D] - z);
-        l += w;
+    constexpr int kSide = 4;                     // parts whose loads are in flight together
+    for (int i0 = 0; i0 < parts; i0 += kSide) {
+        float w[kSide];
+        float2 v[kSide][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int d = 2 * lane + 64 * j;
-            if (d >= c.D) break;
-            const float2 v = *reinterpret_cast<const float2*>(part + d);
-            x[2 * j] = fmaf(w, v.x, x[2 * j]);
-            x[2 * j + 1] = fmaf(w, v.y, x[2 * j + 1]);
+        for (int k = 0; k < kSide; ++k) {
+            const int i = i0 + k;
+            const float* part = i ? rest + i * step : first;
+            w[k] = 0.0f;
+            if (i < parts) w[k] = part[c.D + 1] * ex2(part[c.D] - z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = 2 * lane + 64 * j;
+                v[k][j] = make_float2(0.0f, 0.0f);
+                if (i < parts && d < c.D) v[k][j] = *reinterpret_cast<const float2*>(part + d);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kSide; ++k) {
+            l += w[k];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = fmaf(w[k], v[k][j].x, x[2 * j]);
+                x[2 * j + 1] = fmaf(w[k], v[k][j].y, x[2 * j + 1]);
+            }
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -648,46 +974,35 @@ __global__ void __launch_bounds__(kAttnThreads)
     if (p.lse && lane == 0) p.lse[row] = lse_of(m, l);
 }
 
-template <int DP>
-int launch_attention(const AttnParams& p, int sms, cudaStream_t s)
+template <int R, int ATOMS>
+int launch_attention(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int dev,
+                     int sms, cudaStream_t s)
 {
-    // kernel attribute and CTAs per SM, once per device; 0 = not asked yet
-    static std::atomic<int> occupancy[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return BSP_ERR_CUDA;
-    }
-    int occ = occupancy[dev].load(std::memory_order_acquire);
-    if (occ == 0) {
-        if (cudaFuncSetAttribute(fp8kv_attention_kernel<DP>,
+    using C = Cfg<R, ATOMS>;
+    static std::atomic<bool> ready[kMaxDevices];
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(fp8kv_attention_kernel<R, ATOMS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(Dims<DP>::kSmem)) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fp8kv_attention_kernel<DP>,
-                                                          kAttnThreads,
-                                                          Dims<DP>::kSmem) != cudaSuccess ||
-            occ < 1) {
+                                 C::kSmem) != cudaSuccess) {
             cudaGetLastError();
             return BSP_ERR_CUDA;
         }
-        occupancy[dev].store(occ, std::memory_order_release);
+        ready[dev].store(true, std::memory_order_release);
     }
-    const unsigned ctas = static_cast<unsigned>(std::min(sms * occ, kMaxCtas));
-    if (launch_kernel(fp8kv_attention_kernel<DP>, ctas, kAttnThreads, Dims<DP>::kSmem, s, true,
-                      p) != cudaSuccess) {
-        cudaGetLastError();
-        return BSP_ERR_CUDA;
-    }
+    const unsigned ctas = static_cast<unsigned>(std::min(sms, kMaxCtas));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(ctas, kRows / kAttnWarps, 1);
-    cfg.blockDim = dim3(kAttnThreads, 1, 1);
+    cfg.gridDim = dim3(ctas, (std::min(p.rows, p.slot_rows) + kJoinThreads / 32 - 1) /
+                                 (kJoinThreads / 32), 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fp8kv_join_kernel, p) != cudaSuccess) {
+    if (launch_kernel(fp8kv_attention_kernel<R, ATOMS>, ctas, kThreads, C::kSmem, s, true, k, v,
+                      p) != cudaSuccess ||
+        cudaLaunchKernelEx(&cfg, fp8kv_join_kernel, p) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
@@ -703,7 +1018,7 @@ int64_t fp8kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int6
 {
     if (T < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return BSP_ERR_INVALID_ARG;
     if (D % 16 != 0 || D > 256) return BSP_ERR_UNSUPPORTED_SHAPE;
-    const int64_t rows = std::min<int64_t>(bsp::kRows, T * (Hq / Hkv));
+    const int64_t rows = std::min<int64_t>(bsp::kMaxRows, T * (Hq / Hkv));
     return 2 * bsp::kMaxCtas * rows * (D + 2) * static_cast<int64_t>(sizeof(float));
 }
 
@@ -724,7 +1039,7 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     if (T == 0 || B == 0) return BSP_OK;
     if (!q_bf16 || !out_bf16 || q_stride < Hq * D || pages == 0 || max_pages == 0)
         return BSP_ERR_INVALID_ARG;
-    if (q_stride % 8 != 0) return BSP_ERR_UNSUPPORTED_SHAPE;
+    if (q_stride % 8 != 0 || pages * Hkv >= (int64_t{1} << 31)) return BSP_ERR_UNSUPPORTED_SHAPE;
     const int64_t need = fp8kv_attention_workspace_bytes(T, Hq, Hkv, D);
     if (!workspace || workspace_bytes < need) return BSP_ERR_INVALID_ARG;
     st = kv_check_pointers(p.c);
@@ -742,13 +1057,28 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.window = window > (int64_t{1} << 30) ? 0 : static_cast<int32_t>(window);
     p.G = static_cast<int32_t>(Hq / Hkv);
-    p.status = device_status_ptr(dev);
     p.parts = static_cast<float*>(workspace);
-    p.slot_rows = static_cast<int32_t>(std::min<int64_t>(kRows, T * p.G));
+    p.slot_rows = static_cast<int32_t>(std::min<int64_t>(kMaxRows, T * p.G));
+    p.box = 16;
+    while (p.box < kTile && page_size % (2 * p.box) == 0) p.box *= 2;
+    p.wait_ns = wait_limit_ns();
+    p.status = device_status_ptr(dev);
+    CUtensorMap tk, tv;
+    st = make_page_map(&tk, k_cache, D, page_size, pages * Hkv, p.box);
+    if (st != BSP_OK) return st;
+    st = make_page_map(&tv, v_cache, D, page_size, pages * Hkv, p.box);
+    if (st != BSP_OK) return st;
+    // rows of a row tile: enough for the average sequence's, at most 32
+    const int64_t rows = p.G * ((T + B - 1) / B);
+    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (D <= 64) return launch_attention<64>(p, sms, s);
-    if (D <= 128) return launch_attention<128>(p, sms, s);
-    return launch_attention<256>(p, sms, s);
+    if (D <= 128)
+        return p.rows == 8    ? launch_attention<8, 1>(p, tk, tv, dev, sms, s)
+               : p.rows == 16 ? launch_attention<16, 1>(p, tk, tv, dev, sms, s)
+                              : launch_attention<32, 1>(p, tk, tv, dev, sms, s);
+    return p.rows == 8    ? launch_attention<8, 2>(p, tk, tv, dev, sms, s)
+           : p.rows == 16 ? launch_attention<16, 2>(p, tk, tv, dev, sms, s)
+                          : launch_attention<32, 2>(p, tk, tv, dev, sms, s);
 }
 
 }  // extern "C"

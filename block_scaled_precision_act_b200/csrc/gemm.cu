@@ -1411,6 +1411,21 @@ int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t
     return make_map(m, base, row_bytes, rows, box_rows);
 }
 
+int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens, uint64_t groups,
+                  uint32_t box_tokens)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return BSP_ERR_CUDA;
+    cuuint64_t dims[3] = {D, tokens, groups};
+    cuuint64_t strides[2] = {D, D * tokens};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(kBKB), box_tokens, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_CUDA;
+}
+
 
 int gemm_after_quantizer(bool nvf4, const uint8_t* a, const uint8_t* a_sf, const float* a_scale,
                          const uint8_t* w, const uint8_t* w_sf, const float* w_scale,
