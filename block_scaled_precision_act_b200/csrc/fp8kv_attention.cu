@@ -12,20 +12,22 @@
 //   S[128 tokens][3 R] = K Q^T.  A row of q, scaled by a power of two so that its largest element is in
 //   [128, 256), is the sum of three E4M3 rows of q, 16 q and 256 q's rounding rests: each holds four bits,
 //   so a bf16 element (eight bits) is exact, down to 2^-26 of the row's largest.
-//   O[128 d][4 R] = V^T P^T.  A weight in [0, 2], times 2^(14 + e_V - e_ref), is rounded once, to f16 (11
-//   bits), which is exactly the sum of four E5M2 values: an f16 cut to its upper byte is an E5M2,
-//   three bits of it, and the rest is an f16 again.  e_ref is a common power of two of the values, no
-//   smaller than any block's e_V.
+//   O[128 d][4 R] = V^T P^T.  A weight in [0, 2^7], times 2^(8 + e_V - e_ref), is rounded once, to f16 (11
+//   bits down to weights of 2^-22, an absolute 2^-33 below), which is exactly the sum of four E5M2
+//   values: an f16 cut to its upper byte is an E5M2, three bits of it, and the rest is an f16 again.
+//   e_ref is a common power of two of the values, no smaller than any block's e_V.
 // One thread holds one token of a tile: its scores of all rows, so a weight's bytes for all rows and
 // terms are one 16- to 128-byte store (the operand's rows are tokens).  The rows' reference
-// maxima move only when a score exceeds one by more than 1 (a factor 2 of the weights), which one
+// maxima move only when a score exceeds one by more than 7 (a factor 2^7 of the weights), which one
 // vote of the 128 threads finds; only then are maxima exchanged and O is rescaled.  The sums of the
 // weights stay in the threads, in fp32, until a run ends.
 //
 // Warps: 0 loads the tiles (lanes look up pages and issue one box each), 1 issues the first product,
 // 6 the second (into tensor memory of their own, so neither waits for the other's order), 2-5 are
 // the 128 threads.  S and P have two buffers: the first product of tile i + 1 runs while tile i's
-// weights are made.
+// weights are made.  The token threads' work is a chain of latencies (one warp to a scheduler), so
+// two CTAs share an SM where tensor memory has room for both (R <= 16): one's waits, and its
+// beginnings and ends of items, hide behind the other's tiles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,13 +49,12 @@ namespace {
 constexpr int kThreads = 224;
 constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kMaxRows = 32;
-constexpr int kMaxCtas = 160;
+constexpr int kMaxCtas = 320;
 constexpr int kMinTiles = 2;                     // tiles a CTA takes at least
 constexpr int kMaxSlots = 12;
 constexpr int kAtom = kTile * 128;               // 128 tokens x 128 bytes
-constexpr int kPShift = 14;
-constexpr int kOCol = 256;                       // tensor memory: S at 0, O from here
-constexpr uint32_t kTmemCols = 512;
+constexpr int kPShift = 8;
+constexpr float kMaxGrowth = 7.0f;               // 2^(8 + 7) is below the largest f16
 
 struct AttnParams {
     KvCache c;
@@ -212,14 +213,17 @@ struct SegmentWalk {
             s.sw = seq_work(p, ++b);
             mine = static_cast<int64_t>(s.sw.row_tiles) * p.c.Hkv * s.sw.tiles;
         }
-        const int64_t item = (at - before) / s.sw.tiles;
-        const int seg0 = static_cast<int>((at - before) - item * s.sw.tiles);
+        const int64_t off = at - before;
+        const int64_t item = off < (int64_t{1} << 31)
+                                 ? static_cast<uint32_t>(off) / static_cast<uint32_t>(s.sw.tiles)
+                                 : off / s.sw.tiles;
+        const int seg0 = static_cast<int>(off - item * s.sw.tiles);
         const int seg1 = static_cast<int>(min(static_cast<int64_t>(s.sw.tiles), seg0 + (end - at)));
         at += seg1 - seg0;
         s.b = b;
         s.begins = seg0 == 0;
         s.whole = seg0 == 0 && seg1 == s.sw.tiles;
-        s.h = static_cast<int>(item / s.sw.row_tiles);
+        s.h = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(s.sw.row_tiles));
         s.row_base = static_cast<int>(item - static_cast<int64_t>(s.h) * s.sw.row_tiles) * p.rows;
         s.nrows = min(p.rows, s.sw.n * p.G - s.row_base);
         s.tile_begin = s.sw.tile0 + seg0;
@@ -335,13 +339,17 @@ template <int R, int ATOMS>
 struct Cfg {
     static constexpr int kNS = (3 * R + 15) / 16 * 16;            // columns of S
     static constexpr int kNO = 4 * R;                             // columns of O
+    static constexpr int kOCol = 2 * kNS;                         // tensor memory: S at 0, then O
+    static constexpr int kCols = kOCol + ATOMS * kNO;
+    static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static constexpr int kCtas = kTmemCols <= 256 ? 2 : 1;        // of an SM
     static constexpr int kSlot = ATOMS * kAtom;
     static constexpr int kQ = ATOMS * kNS * 128;
     static constexpr int kP = kTile * kNO;                        // one of two buffers
-    static constexpr int kSlots = std::min(kMaxSlots, (222 * 1024 - kQ - 2 * kP) / kSlot);
+    static constexpr int kRoom = (kCtas == 2 ? 110 : 222) * 1024;
+    static constexpr int kSlots = std::min(kMaxSlots, (kRoom - kQ - 2 * kP) / kSlot);
     static constexpr int kSmem = 1024 + kSlots * kSlot + kQ + 2 * kP;
-    static_assert(kSlots >= 4, "two tiles in the ring");
-    static_assert(2 * kNS <= kOCol && kOCol + ATOMS * kNO <= static_cast<int>(kTmemCols), "TMEM");
+    static_assert(kSlots >= 2 && kCols <= 512, "shared and tensor memory");
 };
 
 template <int R>
@@ -351,11 +359,13 @@ struct TokenShared {
     int wmax[4][R];
     int we[4];
     float wsum[4][R];
+    float m[R], inv[R];                          // of a segment's end
+    void* to[R];                                 // where the row's output or part goes
     uint32_t nan[R][8];                          // NaN elements of V that a row sees, by d
 };
 
 template <int R, int ATOMS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     fp8kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const AttnParams p)
 {
@@ -394,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_v);
     }
     if (warp == 1) {
-        tmem_alloc(&tmem_holder, kTmemCols);
+        tmem_alloc(&tmem_holder, C::kTmemCols);
         tmem_relinquish();
     }
     griddep_wait();
@@ -482,8 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait(&q_full, nseg & 1, abort_flag, p.wait_ns, p.status, 112);
                 ++nseg;
                 for (int tile = seg.tile_begin; ok && tile < seg.tile_end; ++tile, ++i) {
+                    // S(i) also says that P's buffer is free, so that the token threads need not ask
                     ok = mbar_wait(s_free + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
                                    p.status, 113) &&
+                         mbar_wait(p_done + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
+                                   p.status, 119) &&
                          mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 114);
                     if (!ok) break;
                     tc_fence_after();
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t ad = sdesc_mn_major(a + at * kAtom, 128);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)      // 32 tokens each
-                            mma_f8f6f4(tbase + kOCol + at * C::kNO, ad + k * (32 * 128 / 16),
+                            mma_f8f6f4(tbase + C::kOCol + at * C::kNO, ad + k * (32 * 128 / 16),
                                        b + k * (32 * C::kNO / 16), idesc,
                                        tile > seg.tile_begin || k > 0);
                     }
@@ -548,6 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int i = 0, slot = 1;
         uint32_t phase = 0;                                       // of this tile's V slot
         bool ok = true;
+        // a thread's 16-token block one tile on: pages and blocks to add
+        const int step_pages = kTile / kKvBlock / c.page_blocks;
+        const int step_blocks = kTile / kKvBlock - step_pages * c.page_blocks;
         while (walk.next(p, seg)) {
             const int len = seg.sw.len, nrows = seg.nrows;
             const int start = len - seg.sw.n;                     // position of the first new token
@@ -557,24 +573,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t* table = c.table + static_cast<int64_t>(seg.b) * c.max_pages;
 
             // scales: the page of tile i + 2 and the scales of tile i + 1 are on their way during tile i
+            struct Scales {                                       // as loaded: combining them would wait
+                uint8_t k, v;
+                bool in;
+            };
+            int at_page, at_block;                                // of the tile whose page is asked for
+            {
+                const uint32_t blk = (seg.tile_begin * kTile + t) / kKvBlock;
+                at_page = blk / static_cast<uint32_t>(c.page_blocks);
+                at_block = blk - at_page * c.page_blocks;
+            }
             const auto page_of = [&](int tile) {
                 const int tok = tile * kTile + t;
-                return tile < seg.tile_end && tok < len && tok >= lo
-                           ? __ldg(table + tok / kKvBlock / c.page_blocks)
-                           : -1;
+                return tile < seg.tile_end && tok < len && tok >= lo ? __ldg(table + at_page) : -1;
             };
-            const auto scales_of = [&](int tile, int32_t id) {    // key scale | value scale << 8, -1: none
-                if (id < 0 || id >= c.pages) return -1;
-                const int blk = (tile * kTile + t) / kKvBlock;
-                const int64_t at =
-                    (static_cast<int64_t>(id) * c.Hkv + seg.h) * c.page_blocks + blk % c.page_blocks;
-                return __ldg(c.k_scale + at) | __ldg(c.v_scale + at) << 8;
+            const auto forward = [&] {
+                at_page += step_pages;
+                at_block += step_blocks;
+                if (at_block >= c.page_blocks) {
+                    at_block -= c.page_blocks;
+                    ++at_page;
+                }
+            };
+            const auto scales_of = [&](int32_t id, int block) {
+                Scales x = {127, 0, id >= 0 && id < c.pages};
+                if (x.in) {
+                    const int64_t at =
+                        (static_cast<int64_t>(id) * c.Hkv + seg.h) * c.page_blocks + block;
+                    x.k = __ldg(c.k_scale + at);
+                    x.v = __ldg(c.v_scale + at);
+                }
+                return x;
             };
             const int32_t page0 = page_of(seg.tile_begin);
+            const int block0 = at_block;
+            forward();
             int32_t page1 = page_of(seg.tile_begin + 1);
-            int scale0 = scales_of(seg.tile_begin, page0);
+            int block1 = at_block;
 
             // ---- q: three E4M3 rows each
+#pragma unroll 1
             for (int r = q; r < R; r += 4) {
                 const int rr = seg.row_base + r, tok = rr / p.G, head = rr - tok * p.G;
                 const bool in = r < nrows;
@@ -621,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&q_full);
             token_sync();
 
+            Scales scale0 = scales_of(page0, block0);
             float m[R], l[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -631,23 +670,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool any_nan = false;
 
             for (int tile = seg.tile_begin; tile < seg.tile_end; ++tile, ++i) {
-                const int scale = scale0;
-                scale0 = scales_of(tile + 1, page1);
+                const Scales scale = scale0;
+                scale0 = scales_of(page1, block1);
+                forward();
                 page1 = page_of(tile + 2);
+                block1 = at_block;
                 const int tok = tile * kTile + t;
-                // a token that no row sees (or whose page is bad) has scale -1
-                const bool seen = scale >= 0 && tok <= pos_hi;
-                const int ev = seen ? min(scale >> 8, kKvMaxExp) : -1;
-                const float kf = kv_pow2(seen ? min(scale & 255, kKvMaxExp) : 127);
+                const bool seen = scale.in && tok <= pos_hi;      // by some row, and the page is good
+                const int ev = seen ? min(static_cast<int>(scale.v), kKvMaxExp) : -1;
+                const float kf = kv_pow2(seen ? min(static_cast<int>(scale.k), kKvMaxExp) : 127);
                 const bool edge = tile * kTile + kTile - 1 > pos_lo ||
                                   (p.window && tile * kTile <= pos_hi - p.window);
 
                 ok = mbar_wait(s_full + (i & 1), i >> 1 & 1, abort_flag, p.wait_ns, p.status, 117) &&
                      ok;
-                if (token_any(!ok)) {
-                    ok = false;
-                    break;
-                }
                 tc_fence_after();
                 __syncwarp();
                 float s[R];
@@ -678,9 +714,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < R; ++r) exceed = exceed || s[r] > m[r] + 1.0f;
+                for (int r = 0; r < R; ++r) exceed = exceed || s[r] > m[r] + kMaxGrowth;
 
-                if (token_any(exceed)) {
+                if (token_any(exceed || !ok)) {
+                    if (token_any(!ok)) {                         // a wait ran out
+                        ok = false;
+                        break;
+                    }
                     // ---- new reference maxima and exponent; O follows
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
@@ -720,20 +760,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int r0 = 0; r0 < R; r0 += 8) {
                                 float o[8];
                                 __syncwarp();
-                                tmem_ld_x8(tlane + kOCol + k * R + r0, o);
+                                tmem_ld_x8(tlane + C::kOCol + k * R + r0, o);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) o[j] *= f[r0 + j];
-                                tmem_st_x8(tlane + kOCol + k * R + r0, o);
+                                tmem_st_x8(tlane + C::kOCol + k * R + r0, o);
                             }
                         tmem_st_wait();
                     }
                 }
 
                 // ---- weights, their sums, and their four E5M2 terms
-                ok = mbar_wait(p_done + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns, p.status,
-                               119) &&
-                     ok;
                 const int we = 127 + kPShift + ev - e_ref;
                 const float wf = seen && we > 0 ? kv_pow2(we) : 0.0f;
                 uint8_t* pt = ps + (i & 1) * C::kP + t * C::kNO;
@@ -824,57 +861,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
 
-            // ---- end of the segment: sums over the tokens, then this thread's d of every row
+            // ---- end of the segment: sums over the tokens, then this thread's d of every row.  This code
+            // runs once for many tiles: kept short, it does not wait for its own instructions.
+            {
+                // R sums over 32 lanes: lanes exchange halves of the rows, so that R / 2 + R / 4 + ..
+                // shuffles leave each lane one row
+                int row = 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+                for (int n = R / 2, x = 16; x > 0; x >>= 1) {
+                    if (n > 0) {
+                        const bool up = lane & x;
 #pragma unroll
-                for (int x = 16; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], x);
-                if (lane == 0) sh.wsum[q][r] = l[r];
+                        for (int r = 0; r < n; ++r) {
+                            const float give = up ? l[r] : l[r + n];
+                            l[r] = (up ? l[r + n] : l[r]) + __shfl_xor_sync(0xFFFFFFFFu, give, x);
+                        }
+                        row += up ? n : 0;
+                        n /= 2;
+                    } else {
+                        l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], x);
+                    }
+                }
+                sh.wsum[q][row] = l[0];                           // lanes of one row write the same
             }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (t == r) sh.m[r] = m[r];
             ok = mbar_wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag, p.wait_ns, p.status,
                            121) &&
                  ok;
             const bool nans = token_any(any_nan);                 // also: the sums are written
             tc_fence_after();
-            const float back = 1.0f / (1 << kPShift), unit = kv_pow2(max(e_ref, 0));
-#pragma unroll
-            for (int r0 = 0; r0 < R; r0 += 8) {
-                if (r0 >= nrows) break;
-#pragma unroll
-                for (int a = 0; a < ATOMS; ++a) {
+            if (t < nrows) {
+                const float sum = sh.wsum[0][t] + sh.wsum[1][t] + sh.wsum[2][t] + sh.wsum[3][t];
+                const int rr = seg.row_base + t, tok = rr / p.G;
+                const int64_t row = static_cast<int64_t>(seg.sw.first + tok) * c.Hq + seg.h * p.G + rr -
+                                    tok * p.G;
+                sh.inv[t] = sum == 0.0f ? 0.0f : 1.0f / sum * (1.0f / (1 << kPShift));
+                float* part = p.parts + (static_cast<int64_t>(2 * blockIdx.x + seg.begins) *
+                                             p.slot_rows +
+                                         t) * (c.D + 2);
+                sh.to[t] = seg.whole ? static_cast<void*>(p.out + row * c.D) : part;
+                if (!seg.whole) {
+                    part[c.D] = sh.m[t];
+                    part[c.D + 1] = sum;
+                } else if (p.lse) {
+                    p.lse[row] = lse_of(sh.m[t], sum);
+                }
+            }
+            token_sync();
+            const float unit = kv_pow2(max(e_ref, 0));
+#pragma unroll 1
+            for (int a = 0; a < ATOMS; ++a) {
+                const int d = a * 128 + t;
+#pragma unroll 1
+                for (int r0 = 0; r0 < nrows; r0 += 8) {
                     float o[4][8];
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tmem_ld_x8(tlane + kOCol + a * C::kNO + k * R + r0, o[k]);
+                        tmem_ld_x8(tlane + C::kOCol + a * C::kNO + k * R + r0, o[k]);
                     tmem_ld_wait();
-                    const int d = a * 128 + t;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int r = r0 + j;
-                        if (r >= nrows) break;
-                        const float sum =
-                            sh.wsum[0][r] + sh.wsum[1][r] + sh.wsum[2][r] + sh.wsum[3][r];
-                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                        float x = ((o[3][j] + o[2][j]) + (o[1][j] + o[0][j])) * (inv * back) * unit;
+                        if (r >= nrows || d >= c.D) break;
+                        float x = ((o[3][j] + o[2][j]) + (o[1][j] + o[0][j])) * sh.inv[r] * unit;
                         if (nans && (sh.nan[r][d >> 5] >> (d & 31) & 1u)) x = NAN;
-                        const int rr = seg.row_base + r, tok = rr / p.G;
-                        const int64_t row = static_cast<int64_t>(seg.sw.first + tok) * c.Hq +
-                                            seg.h * p.G + rr - tok * p.G;
-                        if (seg.whole) {
-                            if (d < c.D) p.out[row * c.D + d] = __float2bfloat16_rn(x);
-                            if (p.lse && d == 0) p.lse[row] = lse_of(m[r], sum);
-                        } else {
-                            float* part = p.parts +
-                                          (static_cast<int64_t>(2 * blockIdx.x + seg.begins) *
-                                               p.slot_rows +
-                                           r) * (c.D + 2);
-                            if (d < c.D) part[d] = x;
-                            if (d == 0) {
-                                part[c.D] = m[r];
-                                part[c.D + 1] = sum;
-                            }
-                        }
+                        if (seg.whole)
+                            static_cast<__nv_bfloat16*>(sh.to[r])[d] = __float2bfloat16_rn(x);
+                        else
+                            static_cast<float*>(sh.to[r])[d] = x;
                     }
                 }
             }
@@ -892,16 +949,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+    if (warp == 1) tmem_dealloc(tbase, C::kTmemCols);
 }
 
 // Adds the parts of the item that CTA blockIdx.x of the attention kernel began and did not end
-// (if it did): part i weighs l_i 2^(m_i - m), in the order of the tokens.  One warp takes one row.
-constexpr int kJoinThreads = 128;
+// (if it did): part i weighs l_i 2^(m_i - m).  One block takes one row; its four warps take the parts
+// in turn, so that a row of many parts is a few rounds of loads.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
 __global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnParams p)
 {
     __shared__ SplitShared split;
+    __shared__ float warp_m[kJoinWarps], warp_l[kJoinWarps], warp_x[kJoinWarps][256];
     const KvCache& c = p.c;
     const int ctas = gridDim.x;
     int64_t last = 0;
@@ -920,7 +979,7 @@ __global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnPara
     const int parts = static_cast<int>((s1 - 1) / per - blockIdx.x) + 1;
     const int h = static_cast<int>(item / sw.row_tiles);
     const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * p.rows;
-    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (r >= min(p.rows, sw.n * p.G - row_base)) return;
     const int64_t step = static_cast<int64_t>(2) * p.slot_rows * (c.D + 2);
     // part 0 is the second slot of this CTA, part i > 0 the first slot of CTA blockIdx.x + i
@@ -928,22 +987,18 @@ __global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnPara
                                        (c.D + 2);
     const float* rest = p.parts + (static_cast<int64_t>(2 * blockIdx.x) * p.slot_rows + r) *
                                       (c.D + 2);
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, (i ? rest + i * step : first)[c.D]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float z = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, x[8] = {};
+    // warp w takes parts w, w + 4, ..: a running maximum, as in the attention itself
+    float m = -INFINITY, l = 0.0f, x[8] = {};
     constexpr int kSide = 4;                     // parts whose loads are in flight together
-    for (int i0 = 0; i0 < parts; i0 += kSide) {
-        float w[kSide];
+    for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kSide) {
+        float pm[kSide], pl[kSide];
         float2 v[kSide][4];
 #pragma unroll
         for (int k = 0; k < kSide; ++k) {
-            const int i = i0 + k;
+            const int i = i0 + kJoinWarps * k;
             const float* part = i ? rest + i * step : first;
-            w[k] = 0.0f;
-            if (i < parts) w[k] = part[c.D + 1] * ex2(part[c.D] - z);
+            pm[k] = i < parts ? part[c.D] : -INFINITY;
+            pl[k] = i < parts ? part[c.D + 1] : 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int d = 2 * lane + 64 * j;
@@ -953,25 +1008,46 @@ __global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnPara
         }
 #pragma unroll
         for (int k = 0; k < kSide; ++k) {
-            l += w[k];
+            const float top = fmaxf(m, pm[k]), z = top == -INFINITY ? 0.0f : top;
+            const float old = ex2(m - z), w = pl[k] * ex2(pm[k] - z);
+            m = top;
+            l = fmaf(l, old, w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[2 * j] = fmaf(w[k], v[k][j].x, x[2 * j]);
-                x[2 * j + 1] = fmaf(w[k], v[k][j].y, x[2 * j + 1]);
+                x[2 * j] = fmaf(x[2 * j], old, w * v[k][j].x);
+                x[2 * j + 1] = fmaf(x[2 * j + 1], old, w * v[k][j].y);
             }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int rr = row_base + r, tok = rr / p.G, head = h * p.G + rr - tok * p.G;
-    const int64_t row = static_cast<int64_t>(sw.first + tok) * c.Hq + head;
+    if (lane == 0) {
+        warp_m[warp] = m;
+        warp_l[warp] = l;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int d = 2 * lane + 64 * j;
-        if (d >= c.D) break;
-        *reinterpret_cast<__nv_bfloat162*>(p.out + row * c.D + d) =
-            __floats2bfloat162_rn(x[2 * j] * inv, x[2 * j + 1] * inv);
+        warp_x[warp][2 * lane + 64 * j] = x[2 * j];
+        warp_x[warp][2 * lane + 64 * j + 1] = x[2 * j + 1];
     }
-    if (p.lse && lane == 0) p.lse[row] = lse_of(m, l);
+    __syncthreads();
+    float top = -INFINITY, sum = 0.0f, f[kJoinWarps];
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, warp_m[w]);
+    const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = ex2(warp_m[w] - z);
+        sum = fmaf(warp_l[w], f[w], sum);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int rr = row_base + r, tok = rr / p.G, head = h * p.G + rr - tok * p.G;
+    const int64_t row = static_cast<int64_t>(sw.first + tok) * c.Hq + head;
+    for (int d = threadIdx.x; d < c.D; d += kJoinThreads) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) y = fmaf(f[w], warp_x[w][d], y);
+        p.out[row * c.D + d] = __float2bfloat16_rn(y * inv);
+    }
+    if (p.lse && threadIdx.x == 0) p.lse[row] = lse_of(top, sum);
 }
 
 template <int R, int ATOMS>
@@ -989,13 +1065,12 @@ int launch_attention(const AttnParams& p, const CUtensorMap& k, const CUtensorMa
         }
         ready[dev].store(true, std::memory_order_release);
     }
-    const unsigned ctas = static_cast<unsigned>(std::min(sms, kMaxCtas));
+    const unsigned ctas = static_cast<unsigned>(std::min(sms * C::kCtas, kMaxCtas));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(ctas, (std::min(p.rows, p.slot_rows) + kJoinThreads / 32 - 1) /
-                                 (kJoinThreads / 32), 1);
+    cfg.gridDim = dim3(ctas, std::min(p.rows, p.slot_rows), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
