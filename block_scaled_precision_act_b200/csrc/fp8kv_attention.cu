@@ -22,12 +22,12 @@
 // vote of the 128 threads finds; only then are maxima exchanged and O is rescaled.  The sums of the
 // weights stay in the threads, in fp32, until a run ends.
 //
-// Warps: 0 loads the tiles (lanes look up pages and issue one box each), 1 issues the first product,
-// 6 the second (into tensor memory of their own, so neither waits for the other's order), 2-5 are
+// Warps: 0 walks over the items and loads the tiles (lanes look up pages and issue one box each), 1
+// issues both products (that of tile i + 1's scores before that of tile i's values), 2-5 are
 // the 128 threads.  S and P have two buffers: the first product of tile i + 1 runs while tile i's
 // weights are made.  The token threads' work is a chain of latencies (one warp to a scheduler), so
-// two CTAs share an SM where tensor memory has room for both (R <= 16): one's waits, and its
-// beginnings and ends of items, hide behind the other's tiles.
+// several CTAs share an SM where tensor and shared memory have room (R <= 16): one's waits, and its
+// beginnings and ends of items, hide behind the others' tiles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,10 +46,11 @@ int kv_check_pointers(const KvCache& c);
 
 namespace {
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 192;                    // loads, issuer, 128 token threads
 constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kMaxRows = 32;
-constexpr int kMaxCtas = 320;
+constexpr int kMaxCtas = 480;
+constexpr int kQueue = 4;                        // segments that the loads are ahead by
 constexpr int kMinTiles = 2;                     // tiles a CTA takes at least
 constexpr int kMaxSlots = 12;
 constexpr int kAtom = kTile * 128;               // 128 tokens x 128 bytes
@@ -84,7 +85,7 @@ __device__ __forceinline__ float ex2(float x)
 // log of the sum l of weights exp2(s - m)
 __device__ __forceinline__ float lse_of(float m, float l)
 {
-    return m == -INFINITY && l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // ---- how the work is split.  An item is one row tile of one key head of a sequence; sequence b
@@ -191,10 +192,10 @@ __device__ __forceinline__ int64_t run_length(int64_t total, int ctas)
     return per < kMinTiles ? kMinTiles : per;
 }
 
-// A walk over the items (or parts of items) of a run; every role of the CTA makes its own.
+// An item, or a part of one, in a run.
 struct Segment {
     SeqWork sw;
-    int b, h, row_base, nrows;
+    int b, h, row_base, nrows;   // nrows < 0: the run has ended
     int tile_begin, tile_end;    // token tiles of the sequence
     bool begins, whole;
 };
@@ -342,11 +343,11 @@ struct Cfg {
     static constexpr int kOCol = 2 * kNS;                         // tensor memory: S at 0, then O
     static constexpr int kCols = kOCol + ATOMS * kNO;
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static constexpr int kCtas = kTmemCols <= 256 ? 2 : 1;        // of an SM
+    static constexpr int kCtas = kTmemCols <= 128 && ATOMS == 1 ? 3 : kTmemCols <= 256 ? 2 : 1;  // of an SM
     static constexpr int kSlot = ATOMS * kAtom;
     static constexpr int kQ = ATOMS * kNS * 128;
     static constexpr int kP = kTile * kNO;                        // one of two buffers
-    static constexpr int kRoom = (kCtas == 2 ? 110 : 222) * 1024;
+    static constexpr int kRoom = (kCtas == 3 ? 73 : kCtas == 2 ? 110 : 220) * 1024;
     static constexpr int kSlots = std::min(kMaxSlots, (kRoom - kQ - 2 * kP) / kSlot);
     static constexpr int kSmem = 1024 + kSlots * kSlot + kQ + 2 * kP;
     static_assert(kSlots >= 2 && kCols <= 512, "shared and tensor memory");
@@ -376,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     uint8_t* qs = ring + C::kSlots * C::kSlot;                    // [ATOMS][kNS][128]
     uint8_t* ps = qs + C::kQ;                                     // [2][128 tokens][kNO]
     __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
-    __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full, fin[2];
+    __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full, fin;
+    __shared__ uint64_t seg_full[kQueue], seg_free[kQueue];
+    __shared__ Segment queue[kQueue];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_word;
     __shared__ SplitShared split;
@@ -395,8 +398,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             mbar_init(s_free + i, 4);
             mbar_init(p_full + i, 4);
             mbar_init(p_done + i, 1);
-            mbar_init(fin + i, 1);
         }
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(seg_full + i, 1);
+            mbar_init(seg_free + i, 5);
+        }
+        mbar_init(&fin, 1);
         mbar_init(&q_full, 4);
         abort_word = 0;
         fence_mbar_init();
@@ -417,12 +424,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     tc_fence_after();
     const uint32_t tbase = tmem_holder;
     const int64_t per = run_length(total, ctas);
-    SegmentWalk walk;
-    walk.at = blockIdx.x * per;
-    walk.end = min(walk.at + per, total);
-    walk.before = split.before;
-    walk.b = split.b;
-    Segment seg;
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -431,7 +432,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         int slot = 0, used = 0;
         uint32_t phase = 1;                      // of an empty slot's barrier, for the first round
         bool ok = true;
-        while (ok && walk.next(p, seg)) {
+        SegmentWalk walk;
+        walk.at = blockIdx.x * per;
+        walk.end = min(walk.at + per, total);
+        walk.before = split.before;
+        walk.b = split.b;
+        Segment seg;
+        for (int nseg = 0; ok; ++nseg) {
+            const bool more = walk.next(p, seg);
+            const int e = nseg % kQueue;
+            bool room = true;
+            if (lane == 0) {
+                room = mbar_wait(seg_free + e, (nseg / kQueue & 1) ^ 1u, abort_flag, p.wait_ns,
+                                 p.status, 110);
+                if (room) {
+                    if (!more) seg.nrows = -1;
+                    queue[e] = seg;
+                    mbar_arrive(seg_full + e);
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, room, 0);
+            if (!ok || !more) break;
             const int len = seg.sw.len;
             const int lo = p.window ? max(0, len - seg.sw.n - p.window + 1) : 0;
             const int32_t* row = c.table + static_cast<int64_t>(seg.b) * c.max_pages;
@@ -481,77 +502,70 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             for (int i = max(0, used - C::kSlots); i < used; ++i)
                 drain_wait(full + i % C::kSlots, i / C::kSlots & 1, p.wait_ns, p.status);
     } else if (warp == 1) {
-        // ------------------------------------------------------------ S = K Q^T
+        // ------------------------------------------------------------ S = K Q^T, O += V^T P^T
         if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3(kTile, C::kNS);
+            const uint32_t idesc_s = idesc_e4m3(kTile, C::kNS), idesc_o = idesc_pv(kTile, C::kNO);
             const int ksteps = (c.D + 31) / 32;
-            int slot = 0, i = 0, nseg = 0;
-            uint32_t phase = 0;
+            int kslot = 0, vslot = 1, i = 0;
+            uint32_t kphase = 0, vphase = 0;
+            const auto forward = [&](int& slot, uint32_t& phase) {
+                slot += 2;
+                if (slot >= C::kSlots) {
+                    slot -= C::kSlots;
+                    phase ^= 1;
+                }
+            };
+            // O += V^T P^T of tile j of the run
+            const auto values = [&](int j, bool fresh) {
+                if (!mbar_wait(full + vslot, vphase, abort_flag, p.wait_ns, p.status, 115) ||
+                    !mbar_wait(p_full + (j & 1), j >> 1 & 1, abort_flag, p.wait_ns, p.status, 116))
+                    return false;
+                tc_fence_after();
+                const uint32_t a = smem_u32(ring + vslot * C::kSlot);
+                const uint64_t b = sdesc_mn_major(smem_u32(ps + (j & 1) * C::kP), C::kNO);
+#pragma unroll
+                for (int at = 0; at < ATOMS; ++at) {
+                    const uint64_t ad = sdesc_mn_major(a + at * kAtom, 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)          // 32 tokens each
+                        mma_f8f6f4(tbase + C::kOCol + at * C::kNO, ad + k * (32 * 128 / 16),
+                                   b + k * (32 * C::kNO / 16), idesc_o, !fresh || k > 0);
+                }
+                tc_commit(empty + vslot);
+                tc_commit(p_done + (j & 1));
+                forward(vslot, vphase);
+                return true;
+            };
             bool ok = true;
-            while (ok && walk.next(p, seg)) {
+            for (int nseg = 0; ok; ++nseg) {
+                const int e = nseg % kQueue;
+                ok = mbar_wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 122);
+                if (!ok || queue[e].nrows < 0) break;
+                const int begin = queue[e].tile_begin, end = queue[e].tile_end;
+                mbar_arrive(seg_free + e);
                 ok = mbar_wait(&q_full, nseg & 1, abort_flag, p.wait_ns, p.status, 112);
-                ++nseg;
-                for (int tile = seg.tile_begin; ok && tile < seg.tile_end; ++tile, ++i) {
-                    // S(i) also says that P's buffer is free, so that the token threads need not ask
+                for (int tile = begin; ok && tile < end; ++tile, ++i) {
                     ok = mbar_wait(s_free + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
                                    p.status, 113) &&
-                         mbar_wait(p_done + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
-                                   p.status, 119) &&
-                         mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 114);
+                         mbar_wait(full + kslot, kphase, abort_flag, p.wait_ns, p.status, 114);
                     if (!ok) break;
                     tc_fence_after();
-                    uint64_t a = sdesc_kmajor_sw128(smem_u32(ring + slot * C::kSlot));
+                    uint64_t a = sdesc_kmajor_sw128(smem_u32(ring + kslot * C::kSlot));
                     uint64_t b = sdesc_kmajor_sw128(smem_u32(qs));
 #pragma unroll 1
                     for (int k = 0; k < ksteps; ++k) {
-                        mma_f8f6f4(tbase + (i & 1) * C::kNS, a, b, idesc, k);
+                        mma_f8f6f4(tbase + (i & 1) * C::kNS, a, b, idesc_s, k);
                         // 32 bytes a step, four steps to a 128-byte atom; units of 16 bytes
                         a += (k & 3) == 3 ? kAtom / 16 - 6 : 2;
                         b += (k & 3) == 3 ? C::kNS * 8 - 6 : 2;
                     }
-                    tc_commit(empty + slot);
+                    tc_commit(empty + kslot);
+                    // also says that tile i - 2's second product is done, so P's buffer is free
                     tc_commit(s_full + (i & 1));
-                    slot += 2;
-                    if (slot >= C::kSlots) {
-                        slot -= C::kSlots;
-                        phase ^= 1;
-                    }
+                    forward(kslot, kphase);
+                    if (tile > begin) ok = values(i - 1, tile == begin + 1);
                 }
-            }
-        }
-    } else if (warp == 6) {
-        // ------------------------------------------------------------ O += V^T P^T
-        if (lane == 0) {
-            const uint32_t idesc = idesc_pv(kTile, C::kNO);
-            int slot = 1, i = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            while (ok && walk.next(p, seg)) {
-                for (int tile = seg.tile_begin; ok && tile < seg.tile_end; ++tile, ++i) {
-                    ok = mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 115) &&
-                         mbar_wait(p_full + (i & 1), i >> 1 & 1, abort_flag, p.wait_ns, p.status,
-                                   116);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t a = smem_u32(ring + slot * C::kSlot);
-                    const uint64_t b = sdesc_mn_major(smem_u32(ps + (i & 1) * C::kP), C::kNO);
-#pragma unroll
-                    for (int at = 0; at < ATOMS; ++at) {
-                        const uint64_t ad = sdesc_mn_major(a + at * kAtom, 128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)      // 32 tokens each
-                            mma_f8f6f4(tbase + C::kOCol + at * C::kNO, ad + k * (32 * 128 / 16),
-                                       b + k * (32 * C::kNO / 16), idesc,
-                                       tile > seg.tile_begin || k > 0);
-                    }
-                    tc_commit(empty + slot);
-                    tc_commit(p_done + (i & 1));
-                    slot += 2;
-                    if (slot >= C::kSlots) {
-                        slot -= C::kSlots;
-                        phase ^= 1;
-                    }
-                }
+                ok = ok && values(i - 1, end == begin + 1);
             }
         }
     } else {
@@ -564,7 +578,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         // a thread's 16-token block one tile on: pages and blocks to add
         const int step_pages = kTile / kKvBlock / c.page_blocks;
         const int step_blocks = kTile / kKvBlock - step_pages * c.page_blocks;
-        while (walk.next(p, seg)) {
+        for (int nseg = 0;; ++nseg) {
+            const int e = nseg % kQueue;
+            ok = mbar_wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 123) && ok;
+            if (token_any(!ok)) break;
+            const Segment seg = queue[e];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_free + e);
+            if (seg.nrows < 0) break;
             const int len = seg.sw.len, nrows = seg.nrows;
             const int start = len - seg.sw.n;                     // position of the first new token
             const int pos_lo = start + seg.row_base / p.G;
@@ -612,44 +633,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             int block1 = at_block;
 
             // ---- q: three E4M3 rows each
+            constexpr int kSide = 2;                              // rows of a warp whose loads are in flight
 #pragma unroll 1
-            for (int r = q; r < R; r += 4) {
-                const int rr = seg.row_base + r, tok = rr / p.G, head = rr - tok * p.G;
-                const bool in = r < nrows;
-                const __nv_bfloat16* src = p.q + (seg.sw.first + tok) * p.q_stride +
-                                           static_cast<int64_t>(seg.h * p.G + head) * c.D;
-                uint32_t w[2 * ATOMS];
-                uint32_t amax = 0;
+            for (int r0 = q; r0 < R; r0 += 4 * kSide) {
+                uint32_t w[kSide][2 * ATOMS];
 #pragma unroll
-                for (int j = 0; j < 2 * ATOMS; ++j) {
-                    const int d = 2 * (lane + 32 * j);
-                    w[j] = in && d < c.D ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
-                    amax = max(amax, max(w[j] << 16 & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-                }
-                amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-                const int e = max(static_cast<int>(amax >> 23), 8);   // biased exponent of the largest
-                const float up = kv_pow2(min(254, 261 - e));          // 2^(7 - (e - 127))
-                if (lane == 0) {
-                    sh.row_fac[r] = amax < 0x7F800000u ? p.scale_log2 * kv_pow2(e - 7) : NAN;
-                    sh.row_pos[r] = start + (seg.row_base + min(r, nrows - 1)) / p.G;
+                for (int u = 0; u < kSide; ++u) {
+                    const int r = r0 + 4 * u, rr = seg.row_base + r, tok = rr / p.G;
+                    const __nv_bfloat16* src = p.q + (seg.sw.first + tok) * p.q_stride +
+                                               static_cast<int64_t>(seg.h * p.G + rr - tok * p.G) * c.D;
+#pragma unroll
+                    for (int j = 0; j < 2 * ATOMS; ++j) {
+                        const int d = 2 * (lane + 32 * j);
+                        w[u][j] = r < nrows && d < c.D ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
+                    }
+                    if (lane == 0)
+                        sh.row_pos[r] = start + (seg.row_base + min(r, nrows - 1)) / p.G;
                 }
 #pragma unroll
-                for (int j = 0; j < 2 * ATOMS; ++j) {
-                    const int d = 2 * (lane + 32 * j);
-                    float x0 = bf16lo_to_f32(w[j]) * up, x1 = bf16hi_to_f32(w[j]) * up;
+                for (int u = 0; u < kSide; ++u) {
+                    const int r = r0 + 4 * u;
+                    uint32_t amax = 0;
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint32_t code = cvt_e4m3x2(x0, x1);
-                        const int n = k * R + r, byte = d & 127;
-                        *reinterpret_cast<uint16_t*>(qs + (d >> 7) * C::kNS * 128 + n * 128 +
-                                                     (((byte >> 4) ^ (n & 7)) << 4) + (byte & 15)) =
-                            static_cast<uint16_t>(code);
-                        uint32_t h, unused;
-                        e4m3x4_to_f16(code, h, unused);
-                        float y0, y1;
-                        f16x2_to_f32(h, y0, y1);
-                        x0 = (x0 - y0) * 16.0f;
-                        x1 = (x1 - y1) * 16.0f;
+                    for (int j = 0; j < 2 * ATOMS; ++j)
+                        amax = max(amax, max(w[u][j] << 16 & 0x7FFFFFFFu, w[u][j] & 0x7FFF0000u));
+                    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+                    const int ex = max(static_cast<int>(amax >> 23), 8);  // biased exponent of the largest
+                    const float up = kv_pow2(min(254, 261 - ex));         // 2^(7 - (ex - 127))
+                    if (lane == 0)
+                        sh.row_fac[r] = amax < 0x7F800000u ? p.scale_log2 * kv_pow2(ex - 7) : NAN;
+#pragma unroll
+                    for (int j = 0; j < 2 * ATOMS; ++j) {
+                        const int d = 2 * (lane + 32 * j), byte = d & 127;
+                        float x0 = bf16lo_to_f32(w[u][j]) * up, x1 = bf16hi_to_f32(w[u][j]) * up;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const uint32_t code = cvt_e4m3x2(x0, x1);
+                            const int n = k * R + r;
+                            *reinterpret_cast<uint16_t*>(qs + (d >> 7) * C::kNS * 128 + n * 128 +
+                                                         (((byte >> 4) ^ (n & 7)) << 4) + (byte & 15)) =
+                                static_cast<uint16_t>(code);
+                            uint32_t h, unused;
+                            e4m3x4_to_f16(code, h, unused);
+                            float y0, y1;
+                            f16x2_to_f32(h, y0, y1);
+                            x0 = (x0 - y0) * 16.0f;
+                            x1 = (x1 - y1) * 16.0f;
+                        }
                     }
                 }
             }
@@ -663,9 +693,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             float m[R], l[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                m[r] = -INFINITY;
+                m[r] = 0.0f;
                 l[r] = 0.0f;
             }
+            uint32_t unset = 0xFFFFFFFFu >> (32 - R);             // rows whose reference is not set yet
             int e_ref = -1, e_top = 0;
             bool any_nan = false;
 
@@ -686,19 +717,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                      ok;
                 tc_fence_after();
                 __syncwarp();
-                float s[R];
-                bool exceed = ev > e_ref || (ev > 0 && ev < e_ref - 10);
+                float s[R];                                       // scores less the row's reference
 #pragma unroll
                 for (int r0 = 0; r0 < R; r0 += 8) {
-                    float a[3][8];
+                    float x[3][8];
 #pragma unroll
                     for (int k = 0; k < 3; ++k)
-                        tmem_ld_x8(tlane + (i & 1) * C::kNS + k * R + r0, a[k]);
+                        tmem_ld_x8(tlane + (i & 1) * C::kNS + k * R + r0, x[k]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        s[r0 + j] = fmaf(fmaf(a[2][j], 0.0625f, a[1][j]), 0.0625f, a[0][j]) *
-                                    sh.row_fac[r0 + j] * kf;
+                        s[r0 + j] = fmaf(fmaf(fmaf(x[2][j], 0.0625f, x[1][j]), 0.0625f, x[0][j]),
+                                         sh.row_fac[r0 + j] * kf, -m[r0 + j]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -713,8 +743,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                         if (tok > pos || (p.window && tok <= pos - p.window)) s[r] = -INFINITY;
                     }
                 }
+                float most = s[0];                                // NaN is no reason to move a reference
 #pragma unroll
-                for (int r = 0; r < R; ++r) exceed = exceed || s[r] > m[r] + kMaxGrowth;
+                for (int r = 1; r < R; ++r) most = fmaxf(most, s[r]);
+                const bool exceed = most > (unset ? -INFINITY : kMaxGrowth) || ev > e_ref ||
+                                    (ev > 0 && ev < e_ref - 10);
 
                 if (token_any(exceed || !ok)) {
                     if (token_any(!ok)) {                         // a wait ran out
@@ -741,10 +774,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     float f[R];
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        const float v = from_ordered(max(max(sh.wmax[0][r], sh.wmax[1][r]),
-                                                         max(sh.wmax[2][r], sh.wmax[3][r])));
-                        const float n = fmaxf(m[r], v);
-                        f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - n);
+                        // how far the reference moves: once to the first maximum, then only up
+                        float v = from_ordered(max(max(sh.wmax[0][r], sh.wmax[1][r]),
+                                                   max(sh.wmax[2][r], sh.wmax[3][r])));
+                        const bool first = unset >> r & 1u, some = v > -INFINITY;
+                        v = first ? (some ? v : 0.0f) : fmaxf(v, 0.0f);
+                        if (some) unset &= ~(1u << r);
+                        const float n = m[r] + v;
+                        f[r] = first ? 0.0f : ex2(m[r] - n);
+                        s[r] += m[r] - n;
                         l[r] *= f[r];
                         f[r] *= ef;
                         m[r] = n;
@@ -754,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                                        p.wait_ns, p.status, 118) &&
                              ok;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < ATOMS * 4; ++k)
 #pragma unroll
                             for (int r0 = 0; r0 < R; r0 += 8) {
@@ -781,9 +819,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
 #pragma unroll
                     for (int j = 0; j < kW; j += 2) {
                         const int r = r0 + j;
-                        const float z0 = m[r] == -INFINITY ? 0.0f : m[r];
-                        const float z1 = m[r + 1] == -INFINITY ? 0.0f : m[r + 1];
-                        const float p0 = ex2(s[r] - z0), p1 = ex2(s[r + 1] - z1);
+                        const float p0 = ex2(s[r]), p1 = ex2(s[r + 1]);
                         l[r] += p0;
                         l[r + 1] += p1;
                         h[j / 2] = pack_f16(p0 * wf, p1 * wf);
@@ -903,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                                          t) * (c.D + 2);
                 sh.to[t] = seg.whole ? static_cast<void*>(p.out + row * c.D) : part;
                 if (!seg.whole) {
-                    part[c.D] = sh.m[t];
+                    part[c.D] = sum == 0.0f ? -INFINITY : sh.m[t];
                     part[c.D + 1] = sum;
                 } else if (p.lse) {
                     p.lse[row] = lse_of(sh.m[t], sum);
@@ -942,9 +978,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
 
     // ---------------------------------------------------------------- teardown
     __syncwarp();
-    if ((warp == 1 || warp == 6) && lane == 0) {
-        tc_commit(fin + (warp == 6));
-        drain_wait(fin + (warp == 6), 0, p.wait_ns, p.status);
+    if (warp == 1 && lane == 0) {
+        tc_commit(&fin);
+        drain_wait(&fin, 0, p.wait_ns, p.status);
     }
     tc_fence_before();
     __syncthreads();
