@@ -51,11 +51,14 @@ constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kMaxRows = 32;
 constexpr int kMaxCtas = 480;
 constexpr int kQueue = 4;                        // segments that the loads are ahead by
-constexpr int kMinTiles = 2;                     // tiles a CTA takes at least
+constexpr int kItemCost = 3;                     // of an item, in tiles
+constexpr int kMinRun = kItemCost + 2;           // weight that a CTA takes at least
 constexpr int kMaxSlots = 12;
 constexpr int kAtom = kTile * 128;               // 128 tokens x 128 bytes
 constexpr int kPShift = 8;
 constexpr float kMaxGrowth = 7.0f;               // 2^(8 + 7) is below the largest f16
+
+struct Cut;
 
 struct AttnParams {
     KvCache c;
@@ -69,6 +72,7 @@ struct AttnParams {
     int32_t rows;            // R: rows of a row tile
     int32_t slot_rows;       // rows of a part in the workspace
     float* parts;            // [2 * ctas][slot_rows][D + 2]: output, maximum, sum of a part
+    Cut* cuts;               // [ctas]
     int32_t box;             // tokens of one load: the largest power of two that divides a page
     int32_t slots;           // of the ring
     uint64_t wait_ns;
@@ -89,10 +93,11 @@ __device__ __forceinline__ float lse_of(float m, float l)
 }
 
 // ---- how the work is split.  An item is one row tile of one key head of a sequence; sequence b
-// has items(b) = row tiles * Hkv of tiles(b) token tiles each.  All tiles of all items in a row
-// are cut into equal runs, one for each CTA, whatever the lengths are: a run may end one item,
-// hold whole ones and begin another.  Only the first and the last item of a run can be cut, so a
-// CTA leaves at most two parts; fp8kv_join_kernel adds the parts of a cut item in order.
+// has items(b) = row tiles * Hkv of tiles(b) token tiles each.  An item weighs its tiles and kItemCost
+// for its beginning and end.  All items in a row are cut into runs of equal weight, one for each CTA,
+// whatever the lengths are: a run may end one item, hold whole ones and begin another.  Only the first
+// and the last item of a run can be cut, so a CTA leaves at most two parts; the CTA that begins an
+// item and does not end it notes that, and fp8kv_join_kernel adds the item's parts in order.
 struct SeqWork {
     int32_t first, n, len;       // rows, new tokens, length
     int32_t row_tiles, tile0, tiles;
@@ -112,15 +117,14 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
     return s;
 }
 
-__device__ __forceinline__ int64_t seq_tiles(const AttnParams& p, int b)
+__device__ __forceinline__ int64_t seq_weight(const AttnParams& p, const SeqWork& s)
 {
-    const SeqWork s = seq_work(p, b);
-    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * s.tiles;
+    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * (s.tiles + kItemCost);
 }
 
 struct SplitShared {
     int64_t warp_sum[8];
-    int64_t before;              // tiles of the sequences before b
+    int64_t before;              // weight of the sequences before b
     int b;
 };
 
@@ -142,11 +146,11 @@ __device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_
         if (i < warp) pre += sh.warp_sum[i];
         chunk += sh.warp_sum[i];
     }
-    return pre + inc - w;        // tiles before this thread's sequence, in this chunk
+    return pre + inc - w;        // weight before this thread's sequence, in this chunk
 }
 
-// Total number of tiles, and (through `pick`, which maps the total to a tile) the sequence that
-// holds that tile, in sh.  Called by every thread.
+// Total weight, and (through `pick`, which maps the total to a place in the row) the sequence that
+// holds that place, in sh.  Called by every thread.
 template <typename Pick>
 __device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& sh, Pick pick)
 {
@@ -154,7 +158,7 @@ __device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& s
     int64_t total = 0, w = 0, excl = 0, chunk = 0;
     for (int base = 0; base < p.c.B; base += threads) {
         const int i = base + threadIdx.x;
-        w = i < p.c.B ? seq_tiles(p, i) : 0;
+        w = i < p.c.B ? seq_weight(p, seq_work(p, i)) : 0;
         excl = chunk_scan(w, sh, chunk);
         total += chunk;
     }
@@ -173,7 +177,7 @@ __device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& s
         int64_t carry = 0;
         for (int base = 0; base < p.c.B; base += threads) {
             const int i = base + threadIdx.x;
-            w = i < p.c.B ? seq_tiles(p, i) : 0;
+            w = i < p.c.B ? seq_weight(p, seq_work(p, i)) : 0;
             excl = chunk_scan(w, sh, chunk) + carry;
             if (at >= excl && at < excl + w) {
                 sh.b = i;
@@ -189,7 +193,7 @@ __device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& s
 __device__ __forceinline__ int64_t run_length(int64_t total, int ctas)
 {
     const int64_t per = (total + ctas - 1) / ctas;
-    return per < kMinTiles ? kMinTiles : per;
+    return per < kMinRun ? kMinRun : per;
 }
 
 // An item, or a part of one, in a run.
@@ -197,6 +201,7 @@ struct Segment {
     SeqWork sw;
     int b, h, row_base, nrows;   // nrows < 0: the run has ended
     int tile_begin, tile_end;    // token tiles of the sequence
+    int parts;                   // of the item from this one on, when it begins and does not end here
     bool begins, whole;
 };
 
@@ -204,33 +209,46 @@ struct SegmentWalk {
     int64_t at, end, before;
     int b;
 
-    __device__ __forceinline__ bool next(const AttnParams& p, Segment& s)
+    __device__ __forceinline__ bool next(const AttnParams& p, int64_t per, Segment& s)
     {
-        if (at >= end) return false;
-        s.sw = seq_work(p, b);
-        int64_t mine = static_cast<int64_t>(s.sw.row_tiles) * p.c.Hkv * s.sw.tiles;
-        while (at >= before + mine && b + 1 < p.c.B) {
-            before += mine;
-            s.sw = seq_work(p, ++b);
-            mine = static_cast<int64_t>(s.sw.row_tiles) * p.c.Hkv * s.sw.tiles;
+        while (at < end) {
+            s.sw = seq_work(p, b);
+            int64_t mine = seq_weight(p, s.sw);
+            while (at >= before + mine && b + 1 < p.c.B) {
+                before += mine;
+                s.sw = seq_work(p, ++b);
+                mine = seq_weight(p, s.sw);
+            }
+            const int weight = s.sw.tiles + kItemCost;
+            const int64_t off = at - before;
+            const int64_t item = off < (int64_t{1} << 31)
+                                     ? static_cast<uint32_t>(off) / static_cast<uint32_t>(weight)
+                                     : off / weight;
+            const int from = static_cast<int>(off - item * weight);
+            const int to = static_cast<int>(min(static_cast<int64_t>(weight), from + (end - at)));
+            at += to - from;
+            // the item's first kItemCost units hold no tile
+            const int seg0 = max(0, from - kItemCost), seg1 = max(0, to - kItemCost);
+            if (seg0 == seg1) continue;
+            s.b = b;
+            s.begins = seg0 == 0;
+            s.whole = seg0 == 0 && seg1 == s.sw.tiles;
+            // the run that holds the item's last unit, counted from this one, whose last unit is at - 1
+            s.parts = static_cast<int>((before + (item + 1) * weight - 1) / per - (at - 1) / per) + 1;
+            s.h = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(s.sw.row_tiles));
+            s.row_base = static_cast<int>(item - static_cast<int64_t>(s.h) * s.sw.row_tiles) * p.rows;
+            s.nrows = min(p.rows, s.sw.n * p.G - s.row_base);
+            s.tile_begin = s.sw.tile0 + seg0;
+            s.tile_end = s.sw.tile0 + seg1;
+            return true;
         }
-        const int64_t off = at - before;
-        const int64_t item = off < (int64_t{1} << 31)
-                                 ? static_cast<uint32_t>(off) / static_cast<uint32_t>(s.sw.tiles)
-                                 : off / s.sw.tiles;
-        const int seg0 = static_cast<int>(off - item * s.sw.tiles);
-        const int seg1 = static_cast<int>(min(static_cast<int64_t>(s.sw.tiles), seg0 + (end - at)));
-        at += seg1 - seg0;
-        s.b = b;
-        s.begins = seg0 == 0;
-        s.whole = seg0 == 0 && seg1 == s.sw.tiles;
-        s.h = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(s.sw.row_tiles));
-        s.row_base = static_cast<int>(item - static_cast<int64_t>(s.h) * s.sw.row_tiles) * p.rows;
-        s.nrows = min(p.rows, s.sw.n * p.G - s.row_base);
-        s.tile_begin = s.sw.tile0 + seg0;
-        s.tile_end = s.sw.tile0 + seg1;
-        return true;
+        return false;
     }
+};
+
+// What the join has to know of an item that CTA i began and did not end; parts = 0: there is none.
+struct Cut {
+    int32_t parts, nrows, row_base, h, first, pad[3];
 };
 
 // ---- PTX
@@ -439,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         walk.b = split.b;
         Segment seg;
         for (int nseg = 0; ok; ++nseg) {
-            const bool more = walk.next(p, seg);
+            const bool more = walk.next(p, per, seg);
             const int e = nseg % kQueue;
             bool room = true;
             if (lane == 0) {
@@ -578,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         // a thread's 16-token block one tile on: pages and blocks to add
         const int step_pages = kTile / kKvBlock / c.page_blocks;
         const int step_blocks = kTile / kKvBlock - step_pages * c.page_blocks;
+        Cut cut = {};
         for (int nseg = 0;; ++nseg) {
             const int e = nseg % kQueue;
             ok = mbar_wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 123) && ok;
@@ -586,6 +605,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             __syncwarp();
             if (lane == 0) mbar_arrive(seg_free + e);
             if (seg.nrows < 0) break;
+            if (seg.begins && !seg.whole) {
+                cut.parts = seg.parts;
+                cut.nrows = seg.nrows;
+                cut.row_base = seg.row_base;
+                cut.h = seg.h;
+                cut.first = seg.sw.first;
+            }
             const int len = seg.sw.len, nrows = seg.nrows;
             const int start = len - seg.sw.n;                     // position of the first new token
             const int pos_lo = start + seg.row_base / p.G;
@@ -974,6 +1000,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             tc_fence_before();
             token_sync();                        // O, the sums and q's rows are free
         }
+        if (t == 0) p.cuts[blockIdx.x] = cut;
     }
 
     // ---------------------------------------------------------------- teardown
@@ -995,28 +1022,12 @@ constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
 __global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnParams p)
 {
-    __shared__ SplitShared split;
     __shared__ float warp_m[kJoinWarps], warp_l[kJoinWarps], warp_x[kJoinWarps][256];
     const KvCache& c = p.c;
-    const int ctas = gridDim.x;
-    int64_t last = 0;
-    const int64_t total = find_tile(p, split, [&](int64_t n) {
-        last = min((blockIdx.x + int64_t{1}) * run_length(n, ctas), n) - 1;
-        return last;
-    });
-    const int64_t per = run_length(total, ctas);
-    const int64_t begin = blockIdx.x * per;
     griddep_wait();
-    if (begin >= total) return;
-    const SeqWork sw = seq_work(p, split.b);
-    const int64_t item = (last - split.before) / sw.tiles;
-    const int64_t s0 = split.before + item * sw.tiles, s1 = s0 + sw.tiles;   // the item's tiles
-    if (s0 < begin || s1 <= last + 1) return;
-    const int parts = static_cast<int>((s1 - 1) / per - blockIdx.x) + 1;
-    const int h = static_cast<int>(item / sw.row_tiles);
-    const int row_base = static_cast<int>(item - static_cast<int64_t>(h) * sw.row_tiles) * p.rows;
-    const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (r >= min(p.rows, sw.n * p.G - row_base)) return;
+    const Cut cut = p.cuts[blockIdx.x];
+    const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parts = cut.parts;
+    if (parts == 0 || r >= cut.nrows) return;
     const int64_t step = static_cast<int64_t>(2) * p.slot_rows * (c.D + 2);
     // part 0 is the second slot of this CTA, part i > 0 the first slot of CTA blockIdx.x + i
     const float* first = p.parts + (static_cast<int64_t>(2 * blockIdx.x + 1) * p.slot_rows + r) *
@@ -1075,8 +1086,8 @@ __global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnPara
         sum = fmaf(warp_l[w], f[w], sum);
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = row_base + r, tok = rr / p.G, head = h * p.G + rr - tok * p.G;
-    const int64_t row = static_cast<int64_t>(sw.first + tok) * c.Hq + head;
+    const int rr = cut.row_base + r, tok = rr / p.G, head = cut.h * p.G + rr - tok * p.G;
+    const int64_t row = static_cast<int64_t>(cut.first + tok) * c.Hq + head;
     for (int d = threadIdx.x; d < c.D; d += kJoinThreads) {
         float y = 0.0f;
 #pragma unroll
@@ -1130,7 +1141,8 @@ int64_t fp8kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int6
     if (T < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return BSP_ERR_INVALID_ARG;
     if (D % 16 != 0 || D > 256) return BSP_ERR_UNSUPPORTED_SHAPE;
     const int64_t rows = std::min<int64_t>(bsp::kMaxRows, T * (Hq / Hkv));
-    return 2 * bsp::kMaxCtas * rows * (D + 2) * static_cast<int64_t>(sizeof(float));
+    return bsp::kMaxCtas * (static_cast<int64_t>(sizeof(bsp::Cut)) +
+                            2 * rows * (D + 2) * static_cast<int64_t>(sizeof(float)));
 }
 
 int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache,
@@ -1168,7 +1180,8 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     p.window = window > (int64_t{1} << 30) ? 0 : static_cast<int32_t>(window);
     p.G = static_cast<int32_t>(Hq / Hkv);
-    p.parts = static_cast<float*>(workspace);
+    p.cuts = static_cast<Cut*>(workspace);
+    p.parts = reinterpret_cast<float*>(p.cuts + kMaxCtas);
     p.slot_rows = static_cast<int32_t>(std::min<int64_t>(kMaxRows, T * p.G));
     p.box = 16;
     while (p.box < kTile && page_size % (2 * p.box) == 0) p.box *= 2;
