@@ -657,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             forward();
             int32_t page1 = page_of(seg.tile_begin + 1);
             int block1 = at_block;
+            Scales scale0;
 
             // ---- q: three E4M3 rows each
             constexpr int kSide = 2;                              // rows of a warp whose loads are in flight
@@ -676,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     if (lane == 0)
                         sh.row_pos[r] = start + (seg.row_base + min(r, nrows - 1)) / p.G;
                 }
+                if (r0 == q) scale0 = scales_of(page0, block0);  // its page has come meanwhile
 #pragma unroll
                 for (int u = 0; u < kSide; ++u) {
                     const int r = r0 + 4 * u;
@@ -715,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             if (lane == 0) mbar_arrive(&q_full);
             token_sync();
 
-            Scales scale0 = scales_of(page0, block0);
             float m[R], l[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
