@@ -98,6 +98,8 @@ __device__ __forceinline__ float lse_of(float m, float l)
 // whatever the lengths are: a run may end one item, hold whole ones and begin another.  Only the first
 // and the last item of a run can be cut, so a CTA leaves at most two parts; the CTA that begins an
 // item and does not end it notes that, and fp8kv_join_kernel adds the item's parts in order.
+// Where there is little work, so that runs of kMinRun do and every item can have its own, the items are
+// aligned to the runs: then no CTA goes through the end of one item and the beginning of another.
 struct SeqWork {
     int32_t first, n, len;       // rows, new tokens, length
     int32_t row_tiles, tile0, tiles;
@@ -117,9 +119,16 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
     return s;
 }
 
-__device__ __forceinline__ int64_t seq_weight(const AttnParams& p, const SeqWork& s)
+// Weight of an item of the sequence, and of all of them
+__device__ __forceinline__ int32_t item_weight(const SeqWork& s, bool aligned)
 {
-    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * (s.tiles + kItemCost);
+    const int32_t w = s.tiles + kItemCost;
+    return aligned ? (w + kMinRun - 1) / kMinRun * kMinRun : w;
+}
+
+__device__ __forceinline__ int64_t seq_weight(const AttnParams& p, const SeqWork& s, bool aligned)
+{
+    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * item_weight(s, aligned);
 }
 
 struct SplitShared {
@@ -149,51 +158,53 @@ __device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_
     return pre + inc - w;        // weight before this thread's sequence, in this chunk
 }
 
-// Total weight, and (through `pick`, which maps the total to a place in the row) the sequence that
-// holds that place, in sh.  Called by every thread.
-template <typename Pick>
-__device__ __forceinline__ int64_t find_tile(const AttnParams& p, SplitShared& sh, Pick pick)
+// How the row is cut, and in sh the sequence that holds the beginning of CTA blockIdx.x's run (if the
+// row is that long).  Called by every thread.
+struct Split {
+    int64_t total, per;
+    bool aligned;
+};
+
+__device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
 {
-    const int threads = blockDim.x;
-    int64_t total = 0, w = 0, excl = 0, chunk = 0;
-    for (int base = 0; base < p.c.B; base += threads) {
-        const int i = base + threadIdx.x;
-        w = i < p.c.B ? seq_weight(p, seq_work(p, i)) : 0;
-        excl = chunk_scan(w, sh, chunk);
-        total += chunk;
+    const int threads = blockDim.x, ctas = gridDim.x;
+    Split s = {0, 0, true};
+    int64_t w = 0, excl = 0, chunk = 0;
+    for (int pass = 0; pass < 2; ++pass) {       // are the items short and few? if not, cut them anywhere
+        s.total = 0;
+        for (int base = 0; base < p.c.B; base += threads) {
+            const int i = base + threadIdx.x;
+            w = i < p.c.B ? seq_weight(p, seq_work(p, i), s.aligned) : 0;
+            excl = chunk_scan(w, sh, chunk);
+            s.total += chunk;
+        }
+        s.per = kMinRun;
+        if (s.total <= static_cast<int64_t>(ctas) * kMinRun) break;
+        s.per = (s.total + ctas - 1) / ctas;
+        if (!s.aligned) break;
+        s.aligned = false;
     }
-    const int64_t at = pick(total);
+    const int64_t at = blockIdx.x * s.per;
     if (threadIdx.x == 0) {
         sh.b = 0;
         sh.before = 0;
     }
     __syncthreads();
-    if (p.c.B <= threads) {                      // one chunk: it is still in registers
-        if (at >= excl && at < excl + w) {
-            sh.b = threadIdx.x;
-            sh.before = excl;
-        }
-    } else {
-        int64_t carry = 0;
-        for (int base = 0; base < p.c.B; base += threads) {
-            const int i = base + threadIdx.x;
-            w = i < p.c.B ? seq_weight(p, seq_work(p, i)) : 0;
+    int64_t carry = 0;
+    for (int base = 0; base < p.c.B; base += threads) {
+        const int i = base + threadIdx.x;
+        if (p.c.B > threads) {                   // otherwise it is still in registers
+            w = i < p.c.B ? seq_weight(p, seq_work(p, i), s.aligned) : 0;
             excl = chunk_scan(w, sh, chunk) + carry;
-            if (at >= excl && at < excl + w) {
-                sh.b = i;
-                sh.before = excl;
-            }
             carry += chunk;
+        }
+        if (at >= excl && at < excl + w) {
+            sh.b = i;
+            sh.before = excl;
         }
     }
     __syncthreads();
-    return total;
-}
-
-__device__ __forceinline__ int64_t run_length(int64_t total, int ctas)
-{
-    const int64_t per = (total + ctas - 1) / ctas;
-    return per < kMinRun ? kMinRun : per;
+    return s;
 }
 
 // An item, or a part of one, in a run.
@@ -209,17 +220,17 @@ struct SegmentWalk {
     int64_t at, end, before;
     int b;
 
-    __device__ __forceinline__ bool next(const AttnParams& p, int64_t per, Segment& s)
+    __device__ __forceinline__ bool next(const AttnParams& p, const Split& split, Segment& s)
     {
         while (at < end) {
             s.sw = seq_work(p, b);
-            int64_t mine = seq_weight(p, s.sw);
+            int64_t mine = seq_weight(p, s.sw, split.aligned);
             while (at >= before + mine && b + 1 < p.c.B) {
                 before += mine;
                 s.sw = seq_work(p, ++b);
-                mine = seq_weight(p, s.sw);
+                mine = seq_weight(p, s.sw, split.aligned);
             }
-            const int weight = s.sw.tiles + kItemCost;
+            const int weight = item_weight(s.sw, split.aligned);
             const int64_t off = at - before;
             const int64_t item = off < (int64_t{1} << 31)
                                      ? static_cast<uint32_t>(off) / static_cast<uint32_t>(weight)
@@ -227,14 +238,16 @@ struct SegmentWalk {
             const int from = static_cast<int>(off - item * weight);
             const int to = static_cast<int>(min(static_cast<int64_t>(weight), from + (end - at)));
             at += to - from;
-            // the item's first kItemCost units hold no tile
-            const int seg0 = max(0, from - kItemCost), seg1 = max(0, to - kItemCost);
-            if (seg0 == seg1) continue;
+            // the item's first kItemCost units hold no tile, and none follows its tiles
+            const int seg0 = max(0, from - kItemCost);
+            const int seg1 = min(s.sw.tiles, max(0, to - kItemCost));
+            if (seg0 >= seg1) continue;
             s.b = b;
             s.begins = seg0 == 0;
             s.whole = seg0 == 0 && seg1 == s.sw.tiles;
-            // the run that holds the item's last unit, counted from this one, whose last unit is at - 1
-            s.parts = static_cast<int>((before + (item + 1) * weight - 1) / per - (at - 1) / per) + 1;
+            // the run that holds the item's last tile, counted from this one, whose last unit is at - 1
+            s.parts = static_cast<int>((before + item * weight + kItemCost + s.sw.tiles - 1) / split.per -
+                                       (at - 1) / split.per) + 1;
             s.h = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(s.sw.row_tiles));
             s.row_base = static_cast<int>(item - static_cast<int64_t>(s.h) * s.sw.row_tiles) * p.rows;
             s.nrows = min(p.rows, s.sw.n * p.G - s.row_base);
@@ -434,15 +447,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const int ctas = gridDim.x;
-    const int64_t total = find_tile(
-        p, split, [&](int64_t n) { return blockIdx.x * run_length(n, ctas); });
+    const Split cut_up = find_run(p, split);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = tmem_holder;
-    const int64_t per = run_length(total, ctas);
-
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         const int boxes = kTile / p.box, page = c.page_blocks * kKvBlock;
@@ -451,13 +460,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         uint32_t phase = 1;                      // of an empty slot's barrier, for the first round
         bool ok = true;
         SegmentWalk walk;
-        walk.at = blockIdx.x * per;
-        walk.end = min(walk.at + per, total);
+        walk.at = blockIdx.x * cut_up.per;
+        walk.end = min(walk.at + cut_up.per, cut_up.total);
         walk.before = split.before;
         walk.b = split.b;
         Segment seg;
         for (int nseg = 0; ok; ++nseg) {
-            const bool more = walk.next(p, per, seg);
+            const bool more = walk.next(p, cut_up, seg);
             const int e = nseg % kQueue;
             bool room = true;
             if (lane == 0) {
