@@ -158,31 +158,66 @@ __device__ __forceinline__ int64_t chunk_scan(int64_t w, SplitShared& sh, int64_
     return pre + inc - w;        // weight before this thread's sequence, in this chunk
 }
 
-// How the row is cut, and in sh the sequence that holds the beginning of CTA blockIdx.x's run (if the
-// row is that long).  Called by every thread.
+// How the row is cut, and the sequence that holds the beginning of CTA blockIdx.x's run (if the row is
+// that long).
 struct Split {
     int64_t total, per;
     bool aligned;
+    int64_t before;              // weight of the sequences before b
+    int b;
 };
 
+__device__ __forceinline__ bool cut_by(Split& s, int64_t total, bool aligned)
+{
+    const int ctas = gridDim.x;
+    const bool few = total <= static_cast<int64_t>(ctas) * kMinRun;
+    s.total = total;
+    s.aligned = aligned;
+    s.per = few ? kMinRun : (total + ctas - 1) / ctas;
+    return few || !aligned;
+}
+
+// Up to 32 sequences: one warp finds it, without a barrier.
+__device__ __forceinline__ Split find_run_warp(const AttnParams& p)
+{
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < p.c.B;
+    SeqWork sw = {};
+    if (in) sw = seq_work(p, lane);
+    Split s;
+    for (int aligned = 1; aligned >= 0; --aligned) {
+        const int64_t w = in ? seq_weight(p, sw, aligned) : 0;
+        int64_t inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (!cut_by(s, __shfl_sync(0xFFFFFFFFu, inc, 31), aligned)) continue;
+        const int64_t at = blockIdx.x * s.per;
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, at >= inc - w && at < inc);
+        s.b = here ? __ffs(here) - 1 : 0;
+        s.before = __shfl_sync(0xFFFFFFFFu, inc - w, s.b);
+        break;
+    }
+    return s;
+}
+
+// Any number of them: called by every thread.
 __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
 {
-    const int threads = blockDim.x, ctas = gridDim.x;
-    Split s = {0, 0, true};
+    const int threads = blockDim.x;
+    Split s;
     int64_t w = 0, excl = 0, chunk = 0;
-    for (int pass = 0; pass < 2; ++pass) {       // are the items short and few? if not, cut them anywhere
-        s.total = 0;
+    for (int aligned = 1; aligned >= 0; --aligned) {   // are the items short and few? if not, cut them anywhere
+        int64_t total = 0;
         for (int base = 0; base < p.c.B; base += threads) {
             const int i = base + threadIdx.x;
-            w = i < p.c.B ? seq_weight(p, seq_work(p, i), s.aligned) : 0;
+            w = i < p.c.B ? seq_weight(p, seq_work(p, i), aligned) : 0;
             excl = chunk_scan(w, sh, chunk);
-            s.total += chunk;
+            total += chunk;
         }
-        s.per = kMinRun;
-        if (s.total <= static_cast<int64_t>(ctas) * kMinRun) break;
-        s.per = (s.total + ctas - 1) / ctas;
-        if (!s.aligned) break;
-        s.aligned = false;
+        if (cut_by(s, total, aligned)) break;
     }
     const int64_t at = blockIdx.x * s.per;
     if (threadIdx.x == 0) {
@@ -204,6 +239,8 @@ __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
         }
     }
     __syncthreads();
+    s.b = sh.b;
+    s.before = sh.before;
     return s;
 }
 
@@ -447,7 +484,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const Split cut_up = find_run(p, split);
+    Split cut_up;                                // only the loads ask for it
+    if (p.c.B > 32)
+        cut_up = find_run(p, split);
+    else if (warp == 0)
+        cut_up = find_run_warp(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -462,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         SegmentWalk walk;
         walk.at = blockIdx.x * cut_up.per;
         walk.end = min(walk.at + cut_up.per, cut_up.total);
-        walk.before = split.before;
-        walk.b = split.b;
+        walk.before = cut_up.before;
+        walk.b = cut_up.b;
         Segment seg;
         for (int nseg = 0; ok; ++nseg) {
             const bool more = walk.next(p, cut_up, seg);
@@ -1025,86 +1066,90 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     if (warp == 1) tmem_dealloc(tbase, C::kTmemCols);
 }
 
-// Adds the parts of the item that CTA blockIdx.x of the attention kernel began and did not end
-// (if it did): part i weighs l_i 2^(m_i - m).  One block takes one row; its four warps take the parts
-// in turn, so that a row of many parts is a few rounds of loads.
+// Adds the parts of the items that some of the attention kernel's CTAs (`group` of them for each block)
+// began and did not end: part i weighs l_i 2^(m_i - m).  `share` warps of the four
+// take a row: one where there are many items of few parts, four where a few items have many.
 constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
-__global__ void __launch_bounds__(kJoinThreads) fp8kv_join_kernel(const AttnParams p)
+template <int ATOMS>
+__global__ void __launch_bounds__(kJoinThreads)
+    fp8kv_join_kernel(const AttnParams p, int ctas, int group, int share)
 {
-    __shared__ float warp_m[kJoinWarps], warp_l[kJoinWarps], warp_x[kJoinWarps][256];
+    __shared__ float warp_m[kJoinWarps], warp_l[kJoinWarps], warp_x[kJoinWarps][ATOMS * 128];
+    constexpr int kSide = 4, kV = 2 * ATOMS;     // parts whose loads are in flight, pairs of a lane
     const KvCache& c = p.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (kJoinWarps / share) + warp / share;
     griddep_wait();
-    const Cut cut = p.cuts[blockIdx.x];
-    const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parts = cut.parts;
-    if (parts == 0 || r >= cut.nrows) return;
     const int64_t step = static_cast<int64_t>(2) * p.slot_rows * (c.D + 2);
-    // part 0 is the second slot of this CTA, part i > 0 the first slot of CTA blockIdx.x + i
-    const float* first = p.parts + (static_cast<int64_t>(2 * blockIdx.x + 1) * p.slot_rows + r) *
-                                       (c.D + 2);
-    const float* rest = p.parts + (static_cast<int64_t>(2 * blockIdx.x) * p.slot_rows + r) *
-                                      (c.D + 2);
-    // warp w takes parts w, w + 4, ..: a running maximum, as in the attention itself
-    float m = -INFINITY, l = 0.0f, x[8] = {};
-    constexpr int kSide = 4;                     // parts whose loads are in flight together
-    for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kSide) {
-        float pm[kSide], pl[kSide];
-        float2 v[kSide][4];
+    // the block's CTAs are gridDim.x apart: neighbours' cuts go to different blocks
+    const int look = blockIdx.x + lane * gridDim.x;
+    uint32_t todo = __ballot_sync(0xFFFFFFFFu, lane < group && look < ctas && p.cuts[look].parts > 0);
+    for (; todo; todo &= todo - 1) {
+        const int cta = blockIdx.x + (__ffs(todo) - 1) * gridDim.x;
+        const Cut cut = p.cuts[cta];
+        const bool in = r < cut.nrows;
+        const int parts = in ? cut.parts : 0;
+        // part 0 is the second slot of this CTA, part i > 0 the first slot of CTA cta + i
+        const float* rest = p.parts + (static_cast<int64_t>(2 * cta) * p.slot_rows + r) * (c.D + 2);
+        const float* first = rest + step / 2;
+        // a warp takes every share-th part: a running maximum, as in the attention itself
+        float m = -INFINITY, l = 0.0f, x[2 * kV] = {};
+        for (int i0 = warp % share; i0 < parts; i0 += share * kSide) {
+            float pm[kSide], pl[kSide];
+            float2 v[kSide][kV];
 #pragma unroll
-        for (int k = 0; k < kSide; ++k) {
-            const int i = i0 + kJoinWarps * k;
-            const float* part = i ? rest + i * step : first;
-            pm[k] = i < parts ? part[c.D] : -INFINITY;
-            pl[k] = i < parts ? part[c.D + 1] : 0.0f;
+            for (int k = 0; k < kSide; ++k) {
+                const int i = i0 + share * k;
+                const float* part = i ? rest + i * step : first;
+                pm[k] = i < parts ? part[c.D] : -INFINITY;
+                pl[k] = i < parts ? part[c.D + 1] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int d = 2 * lane + 64 * j;
-                v[k][j] = make_float2(0.0f, 0.0f);
-                if (i < parts && d < c.D) v[k][j] = *reinterpret_cast<const float2*>(part + d);
+                for (int j = 0; j < kV; ++j) {
+                    const int d = 2 * lane + 64 * j;
+                    v[k][j] = make_float2(0.0f, 0.0f);
+                    if (i < parts && d < c.D) v[k][j] = *reinterpret_cast<const float2*>(part + d);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kSide; ++k) {
+                const float top = fmaxf(m, pm[k]), z = top == -INFINITY ? 0.0f : top;
+                const float old = ex2(m - z), w = pl[k] * ex2(pm[k] - z);
+                m = top;
+                l = fmaf(l, old, w);
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    x[2 * j] = fmaf(x[2 * j], old, w * v[k][j].x);
+                    x[2 * j + 1] = fmaf(x[2 * j + 1], old, w * v[k][j].y);
+                }
             }
         }
-#pragma unroll
-        for (int k = 0; k < kSide; ++k) {
-            const float top = fmaxf(m, pm[k]), z = top == -INFINITY ? 0.0f : top;
-            const float old = ex2(m - z), w = pl[k] * ex2(pm[k] - z);
-            m = top;
-            l = fmaf(l, old, w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = fmaf(x[2 * j], old, w * v[k][j].x);
-                x[2 * j + 1] = fmaf(x[2 * j + 1], old, w * v[k][j].y);
-            }
+        __syncthreads();                         // the last item is read
+        if (lane == 0) {
+            warp_m[warp] = m;
+            warp_l[warp] = l;
         }
-    }
-    if (lane == 0) {
-        warp_m[warp] = m;
-        warp_l[warp] = l;
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        warp_x[warp][2 * lane + 64 * j] = x[2 * j];
-        warp_x[warp][2 * lane + 64 * j + 1] = x[2 * j + 1];
+        for (int j = 0; j < kV; ++j)
+            *reinterpret_cast<float2*>(&warp_x[warp][2 * lane + 64 * j]) =
+                make_float2(x[2 * j], x[2 * j + 1]);
+        __syncthreads();
+        if (!in) continue;
+        const int w0 = warp / share * share;     // the row's first warp
+        float top = -INFINITY, sum = 0.0f;
+        for (int w = w0; w < w0 + share; ++w) top = fmaxf(top, warp_m[w]);
+        const float z = top == -INFINITY ? 0.0f : top;
+        for (int w = w0; w < w0 + share; ++w) sum = fmaf(warp_l[w], ex2(warp_m[w] - z), sum);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int rr = cut.row_base + r, tok = rr / p.G, head = cut.h * p.G + rr - tok * p.G;
+        const int64_t row = static_cast<int64_t>(cut.first + tok) * c.Hq + head;
+        for (int d = (warp - w0) * 32 + lane; d < c.D; d += share * 32) {
+            float y = 0.0f;
+            for (int w = w0; w < w0 + share; ++w) y = fmaf(ex2(warp_m[w] - z), warp_x[w][d], y);
+            p.out[row * c.D + d] = __float2bfloat16_rn(y * inv);
+        }
+        if (p.lse && warp == w0 && lane == 0) p.lse[row] = lse_of(top, sum);
     }
-    __syncthreads();
-    float top = -INFINITY, sum = 0.0f, f[kJoinWarps];
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, warp_m[w]);
-    const float z = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = ex2(warp_m[w] - z);
-        sum = fmaf(warp_l[w], f[w], sum);
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = cut.row_base + r, tok = rr / p.G, head = cut.h * p.G + rr - tok * p.G;
-    const int64_t row = static_cast<int64_t>(cut.first + tok) * c.Hq + head;
-    for (int d = threadIdx.x; d < c.D; d += kJoinThreads) {
-        float y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) y = fmaf(f[w], warp_x[w][d], y);
-        p.out[row * c.D + d] = __float2bfloat16_rn(y * inv);
-    }
-    if (p.lse && threadIdx.x == 0) p.lse[row] = lse_of(top, sum);
 }
 
 template <int R, int ATOMS>
@@ -1123,18 +1168,26 @@ int launch_attention(const AttnParams& p, const CUtensorMap& k, const CUtensorMa
         ready[dev].store(true, std::memory_order_release);
     }
     const unsigned ctas = static_cast<unsigned>(std::min(sms * C::kCtas, kMaxCtas));
+    // Items: at most the row tiles of the batch for each key head.  Where they are far fewer than the CTAs,
+    // the cuts are that far apart, and a block of the join looks at several CTAs and gives a row four
+    // warps; elsewhere it looks at one and gives a row one warp.
+    const int64_t items = (static_cast<int64_t>(p.c.T) * p.G / R + p.c.B) * p.c.Hkv;
+    const int group = static_cast<int>(std::clamp<int64_t>(ctas / (2 * items), 1, 16));
+    const int share = group > 1 ? kJoinWarps : 1;
+    const int rows = std::min(p.rows, p.slot_rows), per_block = kJoinWarps / share;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(ctas, std::min(p.rows, p.slot_rows), 1);
+    cfg.gridDim = dim3((ctas + group - 1) / group, (rows + per_block - 1) / per_block, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (launch_kernel(fp8kv_attention_kernel<R, ATOMS>, ctas, kThreads, C::kSmem, s, true, k, v,
                       p) != cudaSuccess ||
-        cudaLaunchKernelEx(&cfg, fp8kv_join_kernel, p) != cudaSuccess) {
+        cudaLaunchKernelEx(&cfg, fp8kv_join_kernel<ATOMS>, p, static_cast<int>(ctas), group,
+                           share) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
