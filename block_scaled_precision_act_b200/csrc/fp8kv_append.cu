@@ -34,13 +34,18 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[16], int at)
+// A lane's 16 elements of one token as loaded.
+struct Raw {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ void unpack(const Raw& w, float (&x)[16])
 {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t u[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[at + 2 * i] = bf16lo_to_f32(u[i]);
-        x[at + 2 * i + 1] = bf16hi_to_f32(u[i]);
+    for (int i = 0; i < 8; ++i) {
+        x[2 * i] = bf16lo_to_f32(u[i]);
+        x[2 * i + 1] = bf16hi_to_f32(u[i]);
     }
 }
 
@@ -97,9 +102,32 @@ __device__ __forceinline__ void rotate(const AppendParams& p, const Slot& s, con
     }
 }
 
-// NS: slots of one lane in a block (ceil(D / 32) rounded up to a power of two).
+// Where a task (one head's q, k or v of the unit) reads.
+struct Task {
+    const __nv_bfloat16* src;        // token 0 of the block
+    int64_t stride;
+    int h;
+    bool is_q, is_k;
+};
+
+__device__ __forceinline__ Task task_of(const AppendParams& p, int task, int64_t row0)
+{
+    const int nq = p.q ? p.c.Hq : 0;
+    Task t;
+    t.is_q = task < nq;
+    t.is_k = !t.is_q && task < nq + p.c.Hkv;
+    t.h = t.is_q ? task : (t.is_k ? task - nq : task - nq - p.c.Hkv);
+    t.stride = t.is_q ? p.q_stride : (t.is_k ? p.k_stride : p.v_stride);
+    t.src = (t.is_q ? p.q : (t.is_k ? p.k : p.v)) + row0 * t.stride + static_cast<int64_t>(t.h) * p.c.D;
+    return t;
+}
+
+// NS: slots of one lane in a block (ceil(D / 32) rounded up to a power of two).  A warp's loads of its
+// first task are on their way while the CTA makes the angles; they stay as loaded (8 registers a
+// slot), and are rotated again for the second pass over them, rather than held in fp32.
 template <int NS>
-__global__ void __launch_bounds__(kAppendThreads) fp8kv_append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
+    fp8kv_append_kernel(const AppendParams p)
 {
     extern __shared__ float2 cs[];                       // [16][rot / 2]
     const KvCache& c = p.c;
@@ -121,6 +149,30 @@ __global__ void __launch_bounds__(kAppendThreads) fp8kv_append_kernel(const Appe
     const int hi = len - pos0 < kKvBlock ? static_cast<int>(len - pos0) : kKvBlock;
     const int64_t row0 = rows.first + (pos0 - start);    // row of the block's token 0
 
+    const int lane = threadIdx.x & 31;
+    const int per_token = c.D >> 4;
+    const int slots = kKvBlock * per_token;
+    const int tasks = (p.q ? c.Hq : 0) + 2 * c.Hkv;
+    const int stride = gridDim.y * (kAppendThreads / 32);
+    int task = blockIdx.y * (kAppendThreads / 32) + (threadIdx.x >> 5);
+
+    Raw raw[NS];
+    const auto fresh = [&](const Slot& w, int s) { return s < slots && w.token >= lo && w.token < hi; };
+    const auto load = [&](const Task& t) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int s = lane + 32 * i;
+            const Slot w = slot_of(p, s, per_token);
+            if (!fresh(w, s)) continue;
+            const __nv_bfloat16* row = t.src + w.token * t.stride;
+            raw[i].a = *reinterpret_cast<const uint4*>(row + w.o1);
+            raw[i].b = *reinterpret_cast<const uint4*>(row + w.o2);
+        }
+    };
+    if (task < tasks) load(task_of(p, task, row0));
+    const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages +
+                               block / c.page_blocks);
+
     const int half = p.rot >> 1;
     for (int i = threadIdx.x; i < kKvBlock * half; i += kAppendThreads) {
         const int t = i / half, j = i - t * half;
@@ -135,67 +187,54 @@ __global__ void __launch_bounds__(kAppendThreads) fp8kv_append_kernel(const Appe
     }
     __syncthreads();
 
-    const int lane = threadIdx.x & 31;
-    const int per_token = c.D >> 4;
-    const int slots = kKvBlock * per_token;
-    const int nq = p.q ? c.Hq : 0;
-    const int tasks = nq + 2 * c.Hkv;
-    const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages +
-                               block / c.page_blocks);
     const bool page_ok = page >= 0 && page < c.pages;
     if (!page_ok && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
 
-    for (int task = blockIdx.y * (kAppendThreads / 32) + (threadIdx.x >> 5); task < tasks;
-         task += gridDim.y * (kAppendThreads / 32)) {
-        const bool is_q = task < nq;
-        const bool is_k = !is_q && task < nq + c.Hkv;
-        const int h = is_q ? task : (is_k ? task - nq : task - nq - c.Hkv);
-        const __nv_bfloat16* src = is_q ? p.q : (is_k ? p.k : p.v);
-        const int64_t stride = is_q ? p.q_stride : (is_k ? p.k_stride : p.v_stride);
-        src += row0 * stride + static_cast<int64_t>(h) * c.D;
-        if (!is_q && !page_ok) continue;
-
-        float x[NS][16];
+    for (bool first = true; task < tasks; task += stride, first = false) {
+        const Task t = task_of(p, task, row0);
+        if (!t.is_q && !page_ok) continue;
+        if (!first) load(t);
+        if (t.is_q) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int s = lane + 32 * i;
+                const Slot w = slot_of(p, s, per_token);
+                if (!fresh(w, s)) continue;
+                float x[16];
+                unpack(raw[i], x);
+                rotate(p, w, cs, x);
+                __nv_bfloat16* out = p.q_out + ((row0 + w.token) * c.Hq + t.h) * c.D;
+                *reinterpret_cast<uint4*>(out + w.o1) =
+                    make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
+                               pack2(x[6], x[7]));
+                *reinterpret_cast<uint4*>(out + w.o2) =
+                    make_uint4(pack2(x[8], x[9]), pack2(x[10], x[11]), pack2(x[12], x[13]),
+                               pack2(x[14], x[15]));
+            }
+            continue;
+        }
         uint32_t amax = 0;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int s = lane + 32 * i;
             const Slot w = slot_of(p, s, per_token);
-            if (s >= slots || w.token < lo || w.token >= hi) continue;
-            const __nv_bfloat16* row = src + w.token * stride;
-            unpack8(*reinterpret_cast<const uint4*>(row + w.o1), x[i], 0);
-            unpack8(*reinterpret_cast<const uint4*>(row + w.o2), x[i], 8);
-            if (is_q || is_k) rotate(p, w, cs, x[i]);
+            if (!fresh(w, s)) continue;
+            float x[16];
+            unpack(raw[i], x);
+            if (t.is_k) rotate(p, w, cs, x);
             // a NaN keeps no say in the scale
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const uint32_t a = __float_as_uint(x[i][j]) & 0x7FFFFFFFu;
+                const uint32_t a = __float_as_uint(x[j]) & 0x7FFFFFFFu;
                 amax = a <= 0x7F800000u && a > amax ? a : amax;
             }
         }
-        if (is_q) {
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const int s = lane + 32 * i;
-                const Slot w = slot_of(p, s, per_token);
-                if (s >= slots || w.token < lo || w.token >= hi) continue;
-                __nv_bfloat16* out = p.q_out + ((row0 + w.token) * c.Hq + h) * c.D;
-                uint4 a, d;
-                a = make_uint4(pack2(x[i][0], x[i][1]), pack2(x[i][2], x[i][3]),
-                               pack2(x[i][4], x[i][5]), pack2(x[i][6], x[i][7]));
-                d = make_uint4(pack2(x[i][8], x[i][9]), pack2(x[i][10], x[i][11]),
-                               pack2(x[i][12], x[i][13]), pack2(x[i][14], x[i][15]));
-                *reinterpret_cast<uint4*>(out + w.o1) = a;
-                *reinterpret_cast<uint4*>(out + w.o2) = d;
-            }
-            continue;
-        }
         amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        const int64_t group = static_cast<int64_t>(page) * c.Hkv + h;
+        const int64_t group = static_cast<int64_t>(page) * c.Hkv + t.h;
         const int in_page = static_cast<int>(block % c.page_blocks);
-        uint8_t* scale = (is_k ? c.k_scale : c.v_scale) + group * c.page_blocks + in_page;
+        uint8_t* scale = (t.is_k ? c.k_scale : c.v_scale) + group * c.page_blocks + in_page;
         uint8_t* codes =
-            (is_k ? c.k : c.v) + (group * c.page_blocks + in_page) * kKvBlock * c.D;
+            (t.is_k ? c.k : c.v) + (group * c.page_blocks + in_page) * kKvBlock * c.D;
         int e = kv_scale_exp(amax);
         if (lo > 0) {                                    // the block holds earlier tokens
             const int old = min(static_cast<int>(*scale), kKvMaxExp);
@@ -222,12 +261,15 @@ __global__ void __launch_bounds__(kAppendThreads) fp8kv_append_kernel(const Appe
         for (int i = 0; i < NS; ++i) {
             const int s = lane + 32 * i;
             const Slot w = slot_of(p, s, per_token);
-            if (s >= slots || w.token < lo || w.token >= hi) continue;
+            if (!fresh(w, s)) continue;
+            float x[16];
+            unpack(raw[i], x);
+            if (t.is_k) rotate(p, w, cs, x);
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[j] = cvt_e4m3x2(x[i][4 * j] * f1 * f2, x[i][4 * j + 1] * f1 * f2) |
-                       cvt_e4m3x2(x[i][4 * j + 2] * f1 * f2, x[i][4 * j + 3] * f1 * f2) << 16;
+                o[j] = cvt_e4m3x2(x[4 * j] * f1 * f2, x[4 * j + 1] * f1 * f2) |
+                       cvt_e4m3x2(x[4 * j + 2] * f1 * f2, x[4 * j + 3] * f1 * f2) << 16;
             uint8_t* out = codes + w.token * c.D;
             *reinterpret_cast<uint2*>(out + w.o1) = make_uint2(o[0], o[1]);
             *reinterpret_cast<uint2*>(out + w.o2) = make_uint2(o[2], o[3]);

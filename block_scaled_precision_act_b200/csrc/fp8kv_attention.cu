@@ -17,7 +17,7 @@
 //   values: an f16 cut to its upper byte is an E5M2, three bits of it, and the rest is an f16 again.
 //   e_ref is a common power of two of the values, no smaller than any block's e_V.
 // One thread holds one token of a tile: its scores of all rows, so a weight's bytes for all rows and
-// terms are one 16- to 128-byte store (the operand's rows are tokens).  The rows' reference
+// terms are 32 or 64 bytes side by side (the operand's rows are tokens).  The rows' reference
 // maxima move only when a score exceeds one by more than 7 (a factor 2^7 of the weights), which one
 // vote of the 128 threads finds; only then are maxima exchanged and O is rescaled.  The sums of the
 // weights stay in the threads, in fp32, until a run ends.
@@ -26,7 +26,7 @@
 // issues both products (that of tile i + 1's scores before that of tile i's values), 2-5 are
 // the 128 threads.  S and P have two buffers: the first product of tile i + 1 runs while tile i's
 // weights are made.  The token threads' work is a chain of latencies (one warp to a scheduler), so
-// several CTAs share an SM where tensor and shared memory have room (R <= 16): one's waits, and its
+// three CTAs share an SM (two where tensor or shared memory has no room for more): one's waits, and its
 // beginnings and ends of items, hide behind the others' tiles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kThreads = 192;                    // loads, issuer, 128 token threads
 constexpr int kTile = 128;                       // tokens of a tile
-constexpr int kMaxRows = 32;
+constexpr int kMaxRows = 16;
 constexpr int kMaxCtas = 480;
 constexpr int kQueue = 4;                        // segments that the loads are ahead by
 constexpr int kItemCost = 3;                     // of an item, in tiles
@@ -410,15 +410,15 @@ struct Cfg {
     static constexpr int kNO = 4 * R;                             // columns of O
     static constexpr int kOCol = 2 * kNS;                         // tensor memory: S at 0, then O
     static constexpr int kCols = kOCol + ATOMS * kNO;
-    static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static constexpr int kCtas = kTmemCols <= 128 && ATOMS == 1 ? 3 : kTmemCols <= 256 ? 2 : 1;  // of an SM
+    static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : 256;
+    static constexpr int kCtas = kTmemCols <= 128 && ATOMS == 1 ? 3 : 2;    // of an SM
     static constexpr int kSlot = ATOMS * kAtom;
     static constexpr int kQ = ATOMS * kNS * 128;
     static constexpr int kP = kTile * kNO;                        // one of two buffers
-    static constexpr int kRoom = (kCtas == 3 ? 73 : kCtas == 2 ? 110 : 220) * 1024;
+    static constexpr int kRoom = (kCtas == 3 ? 73 : 110) * 1024;
     static constexpr int kSlots = std::min(kMaxSlots, (kRoom - kQ - 2 * kP) / kSlot);
     static constexpr int kSmem = 1024 + kSlots * kSlot + kQ + 2 * kP;
-    static_assert(kSlots >= 2 && kCols <= 512, "shared and tensor memory");
+    static_assert((R == 8 || R == 16) && kSlots >= 2 && kCols <= 256, "shared and tensor memory");
 };
 
 template <int R>
@@ -889,42 +889,35 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 const int we = 127 + kPShift + ev - e_ref;
                 const float wf = seen && we > 0 ? kv_pow2(we) : 0.0f;
                 uint8_t* pt = ps + (i & 1) * C::kP + t * C::kNO;
+                uint32_t h[R / 2];
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 16) {
-                    constexpr int kW = R < 16 ? R : 16;
-                    uint32_t h[kW / 2];
+                for (int r = 0; r < R; r += 2) {
+                    const float p0 = ex2(s[r]), p1 = ex2(s[r + 1]);
+                    l[r] += p0;
+                    l[r + 1] += p1;
+                    h[r / 2] = pack_f16(p0 * wf, p1 * wf);
+                }
+                uint32_t bytes[4][R / 4];
 #pragma unroll
-                    for (int j = 0; j < kW; j += 2) {
-                        const int r = r0 + j;
-                        const float p0 = ex2(s[r]), p1 = ex2(s[r + 1]);
-                        l[r] += p0;
-                        l[r + 1] += p1;
-                        h[j / 2] = pack_f16(p0 * wf, p1 * wf);
-                    }
-                    uint32_t bytes[4][kW / 4];
+                for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int j = 0; j < R / 4; ++j)
+                        bytes[k][j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
 #pragma unroll
-                        for (int j = 0; j < kW / 4; ++j)
-                            bytes[k][j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
+                    for (int j = 0; j < R / 2; ++j) h[j] = sub_f16x2(h[j], h[j] & 0xFF00FF00u);
+                }
+                // 16-byte chunks of the token's row, swizzled over its 32 or 64 bytes
+                if constexpr (R == 8) {
+                    const int x = (t >> 2) & 1;
+                    *reinterpret_cast<uint4*>(pt + 16 * x) =
+                        make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
+                    *reinterpret_cast<uint4*>(pt + 16 * (x ^ 1)) =
+                        make_uint4(bytes[2][0], bytes[2][1], bytes[3][0], bytes[3][1]);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < kW / 2; ++j)
-                            h[j] = sub_f16x2(h[j], h[j] & 0xFF00FF00u);
-                    }
-                    // 16-byte chunks of the token's row, swizzled over its 32, 64 or 128 bytes
-                    if constexpr (R == 8) {
-                        const int x = (t >> 2) & 1;
-                        *reinterpret_cast<uint4*>(pt + 16 * x) =
-                            make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
-                        *reinterpret_cast<uint4*>(pt + 16 * (x ^ 1)) =
-                            make_uint4(bytes[2][0], bytes[2][1], bytes[3][0], bytes[3][1]);
-                    } else {
-                        const int x = R == 16 ? (t >> 1) & 3 : t & 7;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4*>(pt + 16 * ((k * (R / 16) + r0 / 16) ^ x)) =
-                                make_uint4(bytes[k][0], bytes[k][1], bytes[k][2], bytes[k][3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(pt + 16 * (k ^ ((t >> 1) & 3))) =
+                            make_uint4(bytes[k][0], bytes[k][1], bytes[k][2], bytes[k][3]);
                 }
 
                 // ---- A masked token's weight is 0, but 0 * NaN is not: the values of a token that no
@@ -1255,17 +1248,17 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     if (st != BSP_OK) return st;
     st = make_page_map(&tv, v_cache, D, page_size, pages * Hkv, p.box);
     if (st != BSP_OK) return st;
-    // rows of a row tile: enough for the average sequence's, at most 32
+    // Rows of a row tile: 8 when the average sequence has no more, else 16.  (56 rows of each of 17
+    // sequences: 89 us with 16, 99 with 8, which reads the cache from L2 more often, and 115 with 32, which
+    // leaves an SM one CTA and nothing to hide its latencies behind.)
     const int64_t rows = p.G * ((T + B - 1) / B);
-    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    p.rows = rows <= 8 ? 8 : 16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (D <= 128)
-        return p.rows == 8    ? launch_attention<8, 1>(p, tk, tv, dev, sms, s)
-               : p.rows == 16 ? launch_attention<16, 1>(p, tk, tv, dev, sms, s)
-                              : launch_attention<32, 1>(p, tk, tv, dev, sms, s);
-    return p.rows == 8    ? launch_attention<8, 2>(p, tk, tv, dev, sms, s)
-           : p.rows == 16 ? launch_attention<16, 2>(p, tk, tv, dev, sms, s)
-                          : launch_attention<32, 2>(p, tk, tv, dev, sms, s);
+        return p.rows == 8 ? launch_attention<8, 1>(p, tk, tv, dev, sms, s)
+                           : launch_attention<16, 1>(p, tk, tv, dev, sms, s);
+    return p.rows == 8 ? launch_attention<8, 2>(p, tk, tv, dev, sms, s)
+                       : launch_attention<16, 2>(p, tk, tv, dev, sms, s);
 }
 
 }  // extern "C"
