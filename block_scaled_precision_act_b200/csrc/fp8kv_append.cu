@@ -9,8 +9,8 @@
 // 16-token block that is new, and some of the heads; one warp takes one head of it, holds the
 // block in registers (amax and encode need no second read) and owns the block's scale, so no
 // atomics are needed.  The angles are the same for every head: the CTA makes them once, in
-// shared memory.  They are multiplied and reduced to [-pi, pi] in 64 bits (a position near
-// 2^20 times an fp32 frequency leaves no correct digit of the angle in 32), then sincosf.
+// shared memory.  They are multiplied and reduced to half a turn in 64 bits (a position near
+// 2^20 times an fp32 frequency leaves few correct digits of the angle in 32), then sincospif.
 #include <cuda_bf16.h>
 
 #include "fp8kv_common.cuh"
@@ -27,6 +27,8 @@ struct AppendParams {
     int64_t q_stride, k_stride, v_stride;
     const float* inv_freq;
     int32_t rot;
+    int32_t per;                     // units: see find_unit
+    int32_t extra;
     int32_t interleaved;
     float rope_scale;
     int* status;
@@ -55,10 +57,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<uint32_t*>(&b);
 }
 
-// One lane's 16 elements of one token: two groups of 8 at element offsets o1, o2, and the
-// cos / sin pair index j0 of the first (-1: not rotated).
+// One lane's 16 elements of one token: two groups of 8 at element offsets o1, o2, and the slot's place
+// among the token's rotated ones (-1: not rotated).
 struct Slot {
-    int token, o1, o2, j0;
+    int token, o1, o2, c;
 };
 
 __device__ __forceinline__ Slot slot_of(const AppendParams& p, int s, int per_token)
@@ -74,8 +76,15 @@ __device__ __forceinline__ Slot slot_of(const AppendParams& p, int s, int per_to
         r.o1 = 16 * c;
         r.o2 = 16 * c + 8;
     }
-    r.j0 = c < rs ? 8 * c : -1;
+    r.c = c < rs ? c : -1;
     return r;
+}
+
+// cos and sin of pair i (of 8) of slot c of a token: [8][16 tokens][rot / 16], so that the lanes of a
+// warp, whose slots are neighbours, read neighbouring words.
+__device__ __forceinline__ int angle_at(const AppendParams& p, int token, int c, int i)
+{
+    return (i * kKvBlock + token) * (p.rot >> 4) + c;
 }
 
 // Multiplications and sums are kept apart (no contraction), so the result does not depend on
@@ -91,14 +100,15 @@ __device__ __forceinline__ void turn(float2 a, float& x1, float& x2)
 __device__ __forceinline__ void rotate(const AppendParams& p, const Slot& s, const float2* cs,
                                        float (&x)[16])
 {
-    if (s.j0 < 0) return;
-    const float2* t = cs + s.token * (p.rot >> 1) + s.j0;
+    if (s.c < 0) return;
+    const float2* t = cs + angle_at(p, s.token, s.c, 0);
+    const int step = kKvBlock * (p.rot >> 4);
     if (p.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(t[i], x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) turn(t[i * step], x[2 * i], x[2 * i + 1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(t[i], x[i], x[i + 8]);
+        for (int i = 0; i < 8; ++i) turn(t[i * step], x[i], x[i + 8]);
     }
 }
 
@@ -122,6 +132,42 @@ __device__ __forceinline__ Task task_of(const AppendParams& p, int task, int64_t
     return t;
 }
 
+// Units: sequence b's begin at floor(cu_new[b] * per / 16) + extra * b.  With per = 1, extra = 2 they are
+// its blocks, of which it touches at most floor(n / 16) + 2; with per = 16, extra = 0 they are its
+// tokens, of which the first of each block does the block's work.  The host takes the fewer.
+// The sequence whose units contain unit u is found by all threads at once: one load and one barrier
+// for each blockDim.x sequences, not a chain of dependent loads.
+struct Unit {
+    int64_t begin;               // the sequence's first unit
+    int32_t b, first, n, len;
+};
+
+__device__ __forceinline__ bool find_unit(const AppendParams& p, int64_t u, Unit& unit)
+{
+    __shared__ Unit found;
+    const KvCache& c = p.c;
+    if (threadIdx.x == 0) found.b = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+        const KvRows r = kv_rows(c, i);
+        const int32_t len = kv_length(c, i);
+        const int64_t at = static_cast<int64_t>(r.first) * p.per / kKvBlock +
+                           static_cast<int64_t>(p.extra) * i;
+        const int64_t next = static_cast<int64_t>(r.first + r.n) * p.per / kKvBlock +
+                             static_cast<int64_t>(p.extra) * (i + 1);
+        // one sequence at most, unless cu_new descends: then whichever comes first, all of it
+        if (at <= u && u < next && atomicCAS(&found.b, -1, i) == -1) {
+            found.begin = at;
+            found.first = r.first;
+            found.n = r.n;
+            found.len = len;
+        }
+    }
+    __syncthreads();
+    unit = found;
+    return unit.b >= 0;
+}
+
 // NS: slots of one lane in a block (ceil(D / 32) rounded up to a power of two).  A warp's loads of its
 // first task are on their way while the CTA makes the angles; they stay as loaded (8 registers a
 // slot), and are rotated again for the second pass over them, rather than held in fp32.
@@ -129,25 +175,28 @@ template <int NS>
 __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
     fp8kv_append_kernel(const AppendParams p)
 {
-    extern __shared__ float2 cs[];                       // [16][rot / 2]
+    extern __shared__ float2 cs[];                       // see angle_at
     const KvCache& c = p.c;
     griddep_wait();
     griddep_launch_dependents();
 
-    int64_t begin;
+    Unit unit;
     const int64_t u = blockIdx.x;
-    const int b = kv_find_sequence(c, u, 1, 2, begin);
-    const KvRows rows = kv_rows(c, b);
-    const int32_t len = kv_length(c, b);
-    const int32_t start = len - rows.n;                  // position of the first new token
-    if (start < 0 && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
-    if (rows.n == 0 || start < 0 || u < begin) return;     // u < begin: cu_new descends
-    const int64_t block = start / kKvBlock + (u - begin);
+    if (!find_unit(p, u, unit)) return;
+    const int b = unit.b;
+    const int32_t len = unit.len, start = len - unit.n;  // position of the first new token
+    if (start < 0) {
+        if (u == unit.begin && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
+        return;
+    }
+    const int64_t off = u - unit.begin;
+    if (p.per != 1 && off > 0 && (start + off) % kKvBlock != 0) return;    // not a block's first token
+    const int64_t block = p.per == 1 ? start / kKvBlock + off : (start + off) / kKvBlock;
     const int64_t pos0 = block * kKvBlock;
     if (pos0 >= len) return;
     const int lo = start > pos0 ? static_cast<int>(start - pos0) : 0;     // new: [lo, hi)
     const int hi = len - pos0 < kKvBlock ? static_cast<int>(len - pos0) : kKvBlock;
-    const int64_t row0 = rows.first + (pos0 - start);    // row of the block's token 0
+    const int64_t row0 = unit.first + (pos0 - start);    // row of the block's token 0
 
     const int lane = threadIdx.x & 31;
     const int per_token = c.D >> 4;
@@ -156,14 +205,21 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
     const int stride = gridDim.y * (kAppendThreads / 32);
     int task = blockIdx.y * (kAppendThreads / 32) + (threadIdx.x >> 5);
 
+    // the lane's slots, the same for every task
+    Slot slot[NS];
+    bool fresh[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int s = lane + 32 * i;
+        slot[i] = slot_of(p, s, per_token);
+        fresh[i] = s < slots && slot[i].token >= lo && slot[i].token < hi;
+    }
     Raw raw[NS];
-    const auto fresh = [&](const Slot& w, int s) { return s < slots && w.token >= lo && w.token < hi; };
     const auto load = [&](const Task& t) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const int s = lane + 32 * i;
-            const Slot w = slot_of(p, s, per_token);
-            if (!fresh(w, s)) continue;
+            const Slot& w = slot[i];
+            if (!fresh[i]) continue;
             const __nv_bfloat16* row = t.src + w.token * t.stride;
             raw[i].a = *reinterpret_cast<const uint4*>(row + w.o1);
             raw[i].b = *reinterpret_cast<const uint4*>(row + w.o2);
@@ -178,12 +234,12 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
         const int t = i / half, j = i - t * half;
         if (t < lo || t >= hi) continue;
         const double x = static_cast<double>(pos0 + t) * static_cast<double>(__ldg(p.inv_freq + j));
-        const double n = rint(x * 0.15915494309189535);                 // 1 / (2 pi)
-        double r = fma(-n, 6.283185307179586, x);                       // 2 pi in two doubles
-        r = fma(-n, 2.4492935982947064e-16, r);
+        const double turns = x * 0.15915494309189535;                    // 1 / (2 pi)
         float sn, cn;
-        sincosf(static_cast<float>(r), &sn, &cn);
-        cs[i] = make_float2(__fmul_rn(cn, p.rope_scale), __fmul_rn(sn, p.rope_scale));
+        sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn, &cn);
+        // frequency j belongs to pair j % 8 of slot j / 8
+        cs[angle_at(p, t, j >> 3, j & 7)] =
+            make_float2(__fmul_rn(cn, p.rope_scale), __fmul_rn(sn, p.rope_scale));
     }
     __syncthreads();
 
@@ -197,9 +253,8 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
         if (t.is_q) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                const int s = lane + 32 * i;
-                const Slot w = slot_of(p, s, per_token);
-                if (!fresh(w, s)) continue;
+                const Slot& w = slot[i];
+                if (!fresh[i]) continue;
                 float x[16];
                 unpack(raw[i], x);
                 rotate(p, w, cs, x);
@@ -213,23 +268,18 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
             }
             continue;
         }
-        uint32_t amax = 0;
+        float top = 0.0f;                                // a NaN keeps no say in the scale
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const int s = lane + 32 * i;
-            const Slot w = slot_of(p, s, per_token);
-            if (!fresh(w, s)) continue;
+            const Slot& w = slot[i];
+            if (!fresh[i]) continue;
             float x[16];
             unpack(raw[i], x);
             if (t.is_k) rotate(p, w, cs, x);
-            // a NaN keeps no say in the scale
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t a = __float_as_uint(x[j]) & 0x7FFFFFFFu;
-                amax = a <= 0x7F800000u && a > amax ? a : amax;
-            }
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
         }
-        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+        const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
         const int64_t group = static_cast<int64_t>(page) * c.Hkv + t.h;
         const int in_page = static_cast<int>(block % c.page_blocks);
         uint8_t* scale = (t.is_k ? c.k_scale : c.v_scale) + group * c.page_blocks + in_page;
@@ -255,21 +305,19 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
         }
         __syncwarp();
         if (lane == 0) *scale = static_cast<uint8_t>(e);
-        // 2^(127 - e), as two factors: either alone is a normal number
-        const float f1 = kv_pow2(127 + (127 - e) / 2), f2 = kv_pow2(127 + (127 - e) - (127 - e) / 2);
+        const float f = kv_pow2(254 - e);                // 2^(127 - e), a normal number for every e
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const int s = lane + 32 * i;
-            const Slot w = slot_of(p, s, per_token);
-            if (!fresh(w, s)) continue;
+            const Slot& w = slot[i];
+            if (!fresh[i]) continue;
             float x[16];
             unpack(raw[i], x);
             if (t.is_k) rotate(p, w, cs, x);
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[j] = cvt_e4m3x2(x[4 * j] * f1 * f2, x[4 * j + 1] * f1 * f2) |
-                       cvt_e4m3x2(x[4 * j + 2] * f1 * f2, x[4 * j + 3] * f1 * f2) << 16;
+                o[j] = cvt_e4m3x2(x[4 * j] * f, x[4 * j + 1] * f) |
+                       cvt_e4m3x2(x[4 * j + 2] * f, x[4 * j + 3] * f) << 16;
             uint8_t* out = codes + w.token * c.D;
             *reinterpret_cast<uint2*>(out + w.o1) = make_uint2(o[0], o[1]);
             *reinterpret_cast<uint2*>(out + w.o2) = make_uint2(o[2], o[3]);
@@ -367,8 +415,10 @@ extern "C" int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_
     p.rope_scale = rope_scale;
     p.status = device_status_ptr(dev);
 
-    // room for each sequence's blocks: it touches at most floor(n / 16) + 2 of them
-    const int64_t units = T / kKvBlock + 2 * B;
+    const bool by_token = T < T / kKvBlock + 2 * B;
+    p.per = by_token ? kKvBlock : 1;
+    p.extra = by_token ? 0 : 2;
+    const int64_t units = by_token ? T : T / kKvBlock + 2 * B;
     const int64_t tasks = (q_bf16 ? Hq : 0) + 2 * Hkv;
     constexpr int kWarps = kAppendThreads / 32;
     const int64_t groups = (tasks + kWarps - 1) / kWarps;

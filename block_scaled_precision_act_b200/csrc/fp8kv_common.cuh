@@ -57,31 +57,6 @@ __device__ __forceinline__ int32_t kv_length(const KvCache& c, int b)
     return l < 0 ? 0 : (l > cap ? static_cast<int32_t>(cap) : l);
 }
 
-// The sequence whose work units contain unit u, when sequence b's begin at
-// floor(cu_new[b] * per / 16) + extra * b: the last b that begins at or before u.  Called by
-// every thread of the CTA (the CTA counts the beginnings, so the cost is one load and one
-// barrier for each blockDim.x sequences, not a chain of dependent loads).
-__device__ __forceinline__ int kv_find_sequence(const KvCache& c, int64_t u, int per, int extra,
-                                                int64_t& begin)
-{
-    int b = -1;
-    for (int base = 0; base < c.B; base += blockDim.x) {
-        const int i = base + threadIdx.x;
-        bool in = false;
-        if (i < c.B) {
-            const int64_t at =
-                static_cast<int64_t>(kv_clamp_row(__ldg(c.cu_new + i), c.T)) * per / kKvBlock +
-                static_cast<int64_t>(extra) * i;
-            in = at <= u;
-        }
-        b += __syncthreads_count(in);
-    }
-    if (b < 0) b = 0;
-    begin = static_cast<int64_t>(kv_clamp_row(__ldg(c.cu_new + b), c.T)) * per / kKvBlock +
-            static_cast<int64_t>(extra) * b;
-    return b;
-}
-
 // Smallest scale byte whose 448 multiples reach amax (bits of a non-negative fp32):
 // e = ceil(log2(amax / 448)) + 127, within [0, kKvMaxExp].  448 = 1.75 * 2^8.
 __device__ __forceinline__ int kv_scale_exp(uint32_t amax_bits)
