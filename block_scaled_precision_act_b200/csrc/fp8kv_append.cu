@@ -13,6 +13,8 @@
 // 2^20 times an fp32 frequency leaves few correct digits of the angle in 32), then sincospif.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "fp8kv_common.cuh"
 
 namespace bsp {
@@ -80,35 +82,68 @@ __device__ __forceinline__ Slot slot_of(const AppendParams& p, int s, int per_to
     return r;
 }
 
-// cos and sin of pair i (of 8) of slot c of a token: [8][16 tokens][rot / 16], so that the lanes of a
-// warp, whose slots are neighbours, read neighbouring words.
+// cos and sin of pairs 2 i and 2 i + 1 (of 8) of slot c of a token, as (cos, cos, sin, sin):
+// [4][16 tokens][rot / 16], so that the lanes of a warp, whose slots are neighbours, read neighbouring
+// words.
 __device__ __forceinline__ int angle_at(const AppendParams& p, int token, int c, int i)
 {
     return (i * kKvBlock + token) * (p.rot >> 4) + c;
 }
 
-// Multiplications and sums are kept apart (no contraction), so the result does not depend on
-// which of the two products a compiler fuses.
-__device__ __forceinline__ void turn(float2 a, float& x1, float& x2)
+// Two fp32 at a time.  Products and sums are kept apart (no contraction), so the result does not
+// depend on which of the two products a compiler fuses.
+struct Pair {
+    float a, b;
+};
+
+__device__ __forceinline__ Pair mul2(Pair x, Pair y)
 {
-    const float r1 = __fsub_rn(__fmul_rn(x1, a.x), __fmul_rn(x2, a.y));
-    const float r2 = __fadd_rn(__fmul_rn(x2, a.x), __fmul_rn(x1, a.y));
-    x1 = r1;
-    x2 = r2;
+    Pair d;
+    asm("{\n\t.reg .b64 x, y, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, x, y;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.a), "=f"(d.b)
+        : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b));
+    return d;
 }
 
-__device__ __forceinline__ void rotate(const AppendParams& p, const Slot& s, const float2* cs,
+__device__ __forceinline__ Pair add2(Pair x, Pair y)
+{
+    Pair d;
+    asm("{\n\t.reg .b64 x, y, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 d, x, y;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.a), "=f"(d.b)
+        : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b));
+    return d;
+}
+
+__device__ __forceinline__ void turn(float4 t, float& x1a, float& x1b, float& x2a, float& x2b)
+{
+    const Pair x1 = {x1a, x1b}, x2 = {x2a, x2b}, c = {t.x, t.y}, s = {t.z, t.w}, n = {-t.z, -t.w};
+    const Pair r1 = add2(mul2(x1, c), mul2(x2, n)), r2 = add2(mul2(x2, c), mul2(x1, s));
+    x1a = r1.a;
+    x1b = r1.b;
+    x2a = r2.a;
+    x2b = r2.b;
+}
+
+__device__ __forceinline__ void rotate(const AppendParams& p, const Slot& s, const float4* cs,
                                        float (&x)[16])
 {
     if (s.c < 0) return;
-    const float2* t = cs + angle_at(p, s.token, s.c, 0);
+    const float4* t = cs + angle_at(p, s.token, s.c, 0);
     const int step = kKvBlock * (p.rot >> 4);
     if (p.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(t[i * step], x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) turn(t[i * step], x[4 * i], x[4 * i + 2], x[4 * i + 1], x[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(t[i * step], x[i], x[i + 8]);
+        for (int i = 0; i < 4; ++i) turn(t[i * step], x[2 * i], x[2 * i + 1], x[2 * i + 8], x[2 * i + 9]);
     }
 }
 
@@ -175,7 +210,7 @@ template <int NS>
 __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
     fp8kv_append_kernel(const AppendParams p)
 {
-    extern __shared__ float2 cs[];                       // see angle_at
+    extern __shared__ float4 cs[];                       // see angle_at
     const KvCache& c = p.c;
     griddep_wait();
     griddep_launch_dependents();
@@ -238,8 +273,9 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
         float sn, cn;
         sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn, &cn);
         // frequency j belongs to pair j % 8 of slot j / 8
-        cs[angle_at(p, t, j >> 3, j & 7)] =
-            make_float2(__fmul_rn(cn, p.rope_scale), __fmul_rn(sn, p.rope_scale));
+        float* at = reinterpret_cast<float*>(cs + angle_at(p, t, j >> 3, (j & 7) >> 1)) + (j & 1);
+        at[0] = __fmul_rn(cn, p.rope_scale);
+        at[2] = __fmul_rn(sn, p.rope_scale);
     }
     __syncthreads();
 
@@ -421,7 +457,15 @@ extern "C" int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_
     const int64_t units = by_token ? T : T / kKvBlock + 2 * B;
     const int64_t tasks = (q_bf16 ? Hq : 0) + 2 * Hkv;
     constexpr int kWarps = kAppendThreads / 32;
-    const int64_t groups = (tasks + kWarps - 1) / kWarps;
+    // CTAs to a unit.  A warp takes one task where all CTAs are resident then; with more units, as
+    // many as still make one wave, but no more than three; with more than a wave of units, two (the
+    // angles serve both, and a third would end the overlap of one CTA's beginning with the others' loads:
+    // 68, 65 and 71 us with one, two and three for 12300 tokens of 48 heads, and 12.3, 10.1 and 8.6 us for
+    // 192 sequences of one token).
+    int64_t groups = (tasks + kWarps - 1) / kWarps;
+    const int64_t wave = 3 * static_cast<int64_t>(sms);
+    groups = units > wave ? (groups + 1) / 2
+                          : std::min(groups, std::max(wave / units, (groups + 2) / 3));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
