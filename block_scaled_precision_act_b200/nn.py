@@ -1,4 +1,5 @@
-"""QuantLinear: the quantized linear as a torch module, with the checkpoint tensor names.
+"""Torch modules: QuantLinear, the quantized linear with the checkpoint tensor names, and
+PagedKVCache, the block-scaled 8-bit key/value cache that a decode step keeps between them.
 
 "BFL (fp8r / nvfp4)" (Diffusers quantization doc), format bullets: an nvfp4 linear
 stores `weight` (E2M1 codes, two per byte), `weight_scale` (one E4M3 scale per 16
@@ -18,11 +19,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (SF_LINEAR, SF_MMA, BSPError, fp8r_gemm, fp8r_quantize_rows, nvfp4_gemv,
+from . import (SF_LINEAR, SF_MMA, BSPError, fp8kv_append, fp8kv_attention, fp8r_gemm, fp8r_quantize_rows, nvfp4_gemv,
                nvfp4_global_scale, nvfp4_linear, nvfp4_linear_workspace_bytes,
                nvfp4_quantize_act, nvfp4_sf_convert)
 
-__all__ = ["QuantLinear"]
+__all__ = ["QuantLinear", "PagedKVCache"]
 
 _E4M3 = getattr(torch, "float8_e4m3fn", None)
 
@@ -156,3 +157,50 @@ class QuantLinear(torch.nn.Module):
             aq, asc = fp8r_quantize_rows(x2)
             fp8r_gemm(aq, asc, _u8(self.weight), self.weight_scale, bias=self.bias, out=y)
         return y.reshape(*lead, N)
+
+
+class PagedKVCache(torch.nn.Module):
+    """One layer's keys and values in pages of `page_size` tokens: E4M3 codes with one
+    power-of-two scale (E8M0) for each block of 16 tokens and head.
+
+    The module holds the pool; which pages a sequence has, which rows are whose new tokens
+    and how long the sequences are with them is the caller's, as three int32 device tensors
+    that every layer of a step shares: block_table [B, max_pages], cu_new [B + 1], kv_len [B]
+    (see fp8kv_append in bsp.h).  A step of a layer is append(), then attend()."""
+
+    def __init__(self, num_pages: int, num_heads: int, head_dim: int, page_size: int = 64,
+                 device=None):
+        super().__init__()
+        if head_dim % 16 != 0 or not 0 < head_dim <= 256:
+            raise ValueError("head_dim must be a multiple of 16, at most 256")
+        if page_size % 16 != 0 or not 0 < page_size <= 4096:
+            raise ValueError("page_size must be a multiple of 16, at most 4096")
+        if num_pages <= 0 or num_heads <= 0:
+            raise ValueError("num_pages and num_heads must be positive")
+        self.num_heads, self.head_dim, self.page_size = num_heads, head_dim, page_size
+        codes = (num_pages, num_heads, page_size, head_dim)
+        scales = (num_pages, num_heads, page_size // 16)
+        for name, shape in (("k_cache", codes), ("v_cache", codes), ("k_scale", scales),
+                            ("v_scale", scales)):
+            self.register_buffer(name, torch.zeros(shape, dtype=torch.uint8, device=device),
+                                 persistent=False)
+
+    def extra_repr(self) -> str:
+        return (f"num_pages={self.k_cache.shape[0]}, num_heads={self.num_heads}, "
+                f"head_dim={self.head_dim}, page_size={self.page_size}")
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, block_table, cu_new, kv_len, q=None,
+               inv_freq=None, interleaved: bool = False, rope_scale: float = 1.0):
+        """Rotate the new tokens' k (and q) by their positions and store k and v; returns the
+        rotated q, or None without q.  See fp8kv_append."""
+        return fp8kv_append(k, v, self.k_cache, self.v_cache, self.k_scale, self.v_scale,
+                            block_table, cu_new, kv_len, q=q, inv_freq=inv_freq,
+                            interleaved=interleaved, rope_scale=rope_scale)
+
+    def attend(self, q: torch.Tensor, block_table, cu_new, kv_len, sm_scale: float | None = None,
+               window: int = 0, out=None, return_lse: bool = False):
+        """Attention of the new tokens' q over the cache, which holds their keys and values
+        already.  See fp8kv_attention."""
+        return fp8kv_attention(q, self.k_cache, self.v_cache, self.k_scale, self.v_scale,
+                               block_table, cu_new, kv_len, sm_scale=sm_scale, window=window,
+                               out=out, return_lse=return_lse)

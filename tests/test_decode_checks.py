@@ -176,3 +176,17 @@ def test_quant_linear_weight_only_rows():
         QuantLinear(64, 16, "nvfp4", weight_only_rows=33)
     with pytest.raises(ValueError):
         QuantLinear(64, 16, "fp8r", weight_only_rows=4)
+
+
+def test_paged_kv_cache_module():
+    from block_scaled_precision_act_b200.nn import PagedKVCache
+    c = PagedKVCache(5, 2, 64, page_size=32)
+    assert c.k_cache.shape == c.v_cache.shape == (5, 2, 32, 64) and c.k_scale.shape == (5, 2, 2)
+    assert not c.state_dict() and "page_size=32" in repr(c)
+    for bad in (dict(head_dim=72), dict(head_dim=272), dict(page_size=24), dict(num_pages=0),
+                dict(num_heads=0), dict(page_size=8192)):
+        with pytest.raises(ValueError):
+            PagedKVCache(**{**dict(num_pages=5, num_heads=2, head_dim=64), **bad})
+    with pytest.raises(bsp.BSPError, match=ON_CPU):
+        c.append(bf16(1, 2, 64), bf16(1, 2, 64), *[torch.zeros(s, dtype=torch.int32)
+                                                  for s in ((1, 1), (2,), (1,))])
