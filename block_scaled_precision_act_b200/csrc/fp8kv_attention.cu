@@ -52,7 +52,8 @@ constexpr int kMaxRows = 16;
 constexpr int kMaxCtas = 480;
 constexpr int kQueue = 4;                        // segments that the loads are ahead by
 constexpr int kItemCost = 3;                     // of an item, in tiles
-constexpr int kMinRun = kItemCost + 2;           // weight that a CTA takes at least
+constexpr int kWholeRun = kItemCost + 5;         // items of at most that weight are better not cut
+constexpr int kMinRun = kItemCost + 2;           // weight that a CTA takes at least, where they are
 constexpr int kMaxSlots = 12;
 constexpr int kAtom = kTile * 128;               // 128 tokens x 128 bytes
 constexpr int kPShift = 8;
@@ -75,6 +76,7 @@ struct AttnParams {
     Cut* cuts;               // [ctas]
     int32_t box;             // tokens of one load: the largest power of two that divides a page
     int32_t slots;           // of the ring
+    bool whole;              // every item fits in a run of kWholeRun and has its own CTA
     uint64_t wait_ns;
     int* status;
 };
@@ -98,8 +100,11 @@ __device__ __forceinline__ float lse_of(float m, float l)
 // whatever the lengths are: a run may end one item, hold whole ones and begin another.  Only the first
 // and the last item of a run can be cut, so a CTA leaves at most two parts; the CTA that begins an
 // item and does not end it notes that, and fp8kv_join_kernel adds the item's parts in order.
-// Where there is little work, so that runs of kMinRun do and every item can have its own, the items are
-// aligned to the runs: then no CTA goes through the end of one item and the beginning of another.
+// Where there is little work, the items are aligned to the runs: then no CTA goes through the end of one
+// item and the beginning of another.  If the tables are so short that every item fits in a run of
+// kWholeRun, and there are CTAs for all, none is cut and nothing joined (517 tokens x 8 heads: 12.9 us,
+// and 13.6 cut in two); else every item has its own runs of kMinRun, if the CTAs suffice for that
+// (9910 tokens x 5 heads: 21 us, 29 in runs of kWholeRun).
 struct SeqWork {
     int32_t first, n, len;       // rows, new tokens, length
     int32_t row_tiles, tile0, tiles;
@@ -120,15 +125,16 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
 }
 
 // Weight of an item of the sequence, and of all of them
-__device__ __forceinline__ int32_t item_weight(const SeqWork& s, bool aligned)
+__device__ __forceinline__ int32_t item_weight(const AttnParams& p, const SeqWork& s, bool aligned)
 {
     const int32_t w = s.tiles + kItemCost;
-    return aligned ? (w + kMinRun - 1) / kMinRun * kMinRun : w;
+    if (!aligned) return w;
+    return p.whole ? kWholeRun : (w + kMinRun - 1) / kMinRun * kMinRun;
 }
 
 __device__ __forceinline__ int64_t seq_weight(const AttnParams& p, const SeqWork& s, bool aligned)
 {
-    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * item_weight(s, aligned);
+    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * item_weight(p, s, aligned);
 }
 
 struct SplitShared {
@@ -167,14 +173,15 @@ struct Split {
     int b;
 };
 
-__device__ __forceinline__ bool cut_by(Split& s, int64_t total, bool aligned)
+__device__ __forceinline__ bool cut_by(const AttnParams& p, Split& s, int64_t total, bool aligned)
 {
     const int ctas = gridDim.x;
-    const bool few = total <= static_cast<int64_t>(ctas) * kMinRun;
     s.total = total;
     s.aligned = aligned;
-    s.per = few ? kMinRun : (total + ctas - 1) / ctas;
-    return few || !aligned;
+    s.per = aligned && p.whole ? kWholeRun : kMinRun;
+    if (total <= s.per * ctas) return true;
+    s.per = (total + ctas - 1) / ctas;
+    return !aligned;
 }
 
 // Up to 32 sequences: one warp finds it, without a barrier.
@@ -193,7 +200,7 @@ __device__ __forceinline__ Split find_run_warp(const AttnParams& p)
             const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
             if (lane >= o) inc += y;
         }
-        if (!cut_by(s, __shfl_sync(0xFFFFFFFFu, inc, 31), aligned)) continue;
+        if (!cut_by(p, s, __shfl_sync(0xFFFFFFFFu, inc, 31), aligned)) continue;
         const int64_t at = blockIdx.x * s.per;
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, at >= inc - w && at < inc);
         s.b = here ? __ffs(here) - 1 : 0;
@@ -209,7 +216,7 @@ __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
     const int threads = blockDim.x;
     Split s;
     int64_t w = 0, excl = 0, chunk = 0;
-    for (int aligned = 1; aligned >= 0; --aligned) {   // are the items short and few? if not, cut them anywhere
+    for (int aligned = 1; aligned >= 0; --aligned) {
         int64_t total = 0;
         for (int base = 0; base < p.c.B; base += threads) {
             const int i = base + threadIdx.x;
@@ -217,7 +224,7 @@ __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
             excl = chunk_scan(w, sh, chunk);
             total += chunk;
         }
-        if (cut_by(s, total, aligned)) break;
+        if (cut_by(p, s, total, aligned)) break;
     }
     const int64_t at = blockIdx.x * s.per;
     if (threadIdx.x == 0) {
@@ -267,7 +274,7 @@ struct SegmentWalk {
                 s.sw = seq_work(p, ++b);
                 mine = seq_weight(p, s.sw, split.aligned);
             }
-            const int weight = item_weight(s.sw, split.aligned);
+            const int weight = item_weight(p, s.sw, split.aligned);
             const int64_t off = at - before;
             const int64_t item = off < (int64_t{1} << 31)
                                      ? static_cast<uint32_t>(off) / static_cast<uint32_t>(weight)
@@ -1146,7 +1153,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int R, int ATOMS>
-int launch_attention(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int dev,
+int launch_attention(AttnParams p, const CUtensorMap& k, const CUtensorMap& v, int dev,
                      int sms, cudaStream_t s)
 {
     using C = Cfg<R, ATOMS>;
@@ -1165,6 +1172,8 @@ int launch_attention(const AttnParams& p, const CUtensorMap& k, const CUtensorMa
     // the cuts are that far apart, and a block of the join looks at several CTAs and gives a row four
     // warps; elsewhere it looks at one and gives a row one warp.
     const int64_t items = (static_cast<int64_t>(p.c.T) * p.G / R + p.c.B) * p.c.Hkv;
+    const int64_t longest = (p.c.max_pages * p.c.page_blocks * kKvBlock + kTile - 1) / kTile;
+    p.whole = longest + kItemCost <= kWholeRun && items <= ctas;
     const int group = static_cast<int>(std::clamp<int64_t>(ctas / (2 * items), 1, 16));
     const int share = group > 1 ? kJoinWarps : 1;
     const int rows = std::min(p.rows, p.slot_rows), per_block = kJoinWarps / share;
@@ -1178,7 +1187,11 @@ int launch_attention(const AttnParams& p, const CUtensorMap& k, const CUtensorMa
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (launch_kernel(fp8kv_attention_kernel<R, ATOMS>, ctas, kThreads, C::kSmem, s, true, k, v,
-                      p) != cudaSuccess ||
+                      p) != cudaSuccess) {
+        cudaGetLastError();
+        return BSP_ERR_CUDA;
+    }
+    if (!p.whole &&
         cudaLaunchKernelEx(&cfg, fp8kv_join_kernel<ATOMS>, p, static_cast<int>(ctas), group,
                            share) != cudaSuccess) {
         cudaGetLastError();
