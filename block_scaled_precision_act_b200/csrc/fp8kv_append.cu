@@ -32,6 +32,9 @@ struct AppendParams {
     int32_t per;                     // units: see find_unit
     int32_t extra;
     int32_t interleaved;
+    // floor(2^16 / n) + 1 for the n slots of a token that are rotated and the n that are not: times i,
+    // and shifted, it is floor(i / n), since i * n <= 256 * 16 < 2^16
+    int32_t by_rot, by_rest;
     float rope_scale;
     int* status;
 };
@@ -60,26 +63,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 }
 
 // One lane's 16 elements of one token: two groups of 8 at element offsets o1, o2, and the slot's place
-// among the token's rotated ones (-1: not rotated).
+// among the token's rotated ones (-1: not rotated).  The rotated slots of all tokens come first, so
+// that a warp's slots are all of one kind, or nearly.
+// All of it is in one register; 0 stands for a slot that is not there or not new.
 struct Slot {
-    int token, o1, o2, c;
+    uint32_t bits;
+    __device__ bool there() const { return bits != 0; }
+    __device__ int token() const { return bits & 15u; }
+    __device__ int c() const { return bits >> 4 & 15u; }
+    __device__ int o1() const { return bits >> 5 & 0xF8u; }
+    __device__ int o2() const { return bits >> 10 & 0xF8u; }
+    __device__ bool rotated() const { return bits & 1u << 18; }
 };
 
 __device__ __forceinline__ Slot slot_of(const AppendParams& p, int s, int per_token)
 {
-    const int token = s / per_token, c = s - token * per_token;
-    const int rs = p.rot >> 4;
-    Slot r;
-    r.token = token;
-    if (c < rs && !p.interleaved) {
-        r.o1 = 8 * c;
-        r.o2 = 8 * c + (p.rot >> 1);
-    } else {
-        r.o1 = 16 * c;
-        r.o2 = 16 * c + 8;
-    }
-    r.c = c < rs ? c : -1;
-    return r;
+    const int rs = p.rot >> 4, turned = kKvBlock * rs;
+    const bool rotated = s < turned;
+    const int of = rotated ? rs : per_token - rs, i = rotated ? s : s - turned;
+    const int token = i * (rotated ? p.by_rot : p.by_rest) >> 16;                 // i / of
+    const int c = i - token * of + (rotated ? 0 : rs);
+    // of 8 elements each
+    const int o1 = rotated && !p.interleaved ? c : 2 * c;
+    const int o2 = rotated && !p.interleaved ? c + (p.rot >> 4) : 2 * c + 1;
+    return {static_cast<uint32_t>(token | c << 4 | o1 << 8 | o2 << 13 | (rotated ? 1 << 18 : 0) |
+                                  1 << 19)};
 }
 
 // cos and sin of pairs 2 i and 2 i + 1 (of 8) of slot c of a token, as (cos, cos, sin, sin):
@@ -132,11 +140,21 @@ __device__ __forceinline__ void turn(float4 t, float& x1a, float& x1b, float& x2
     x2b = r2.b;
 }
 
+// The largest magnitude, of two elements at a time; a NaN keeps no say in it.
+__device__ __forceinline__ float largest(const Raw& w)
+{
+    const uint32_t u[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
+    __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[i])));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
 __device__ __forceinline__ void rotate(const AppendParams& p, const Slot& s, const float4* cs,
                                        float (&x)[16])
 {
-    if (s.c < 0) return;
-    const float4* t = cs + angle_at(p, s.token, s.c, 0);
+    const float4* t = cs + angle_at(p, s.token(), s.c(), 0);
     const int step = kKvBlock * (p.rot >> 4);
     if (p.interleaved) {
 #pragma unroll
@@ -242,22 +260,23 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
 
     // the lane's slots, the same for every task
     Slot slot[NS];
-    bool fresh[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         const int s = lane + 32 * i;
-        slot[i] = slot_of(p, s, per_token);
-        fresh[i] = s < slots && slot[i].token >= lo && slot[i].token < hi;
+        slot[i].bits = 0;
+        if (s >= slots) continue;
+        const Slot w = slot_of(p, s, per_token);
+        if (w.token() >= lo && w.token() < hi) slot[i] = w;
     }
     Raw raw[NS];
     const auto load = [&](const Task& t) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const Slot& w = slot[i];
-            if (!fresh[i]) continue;
-            const __nv_bfloat16* row = t.src + w.token * t.stride;
-            raw[i].a = *reinterpret_cast<const uint4*>(row + w.o1);
-            raw[i].b = *reinterpret_cast<const uint4*>(row + w.o2);
+            if (!w.there()) continue;
+            const __nv_bfloat16* row = t.src + w.token() * t.stride;
+            raw[i].a = *reinterpret_cast<const uint4*>(row + w.o1());
+            raw[i].b = *reinterpret_cast<const uint4*>(row + w.o2());
         }
     };
     if (task < tasks) load(task_of(p, task, row0));
@@ -290,17 +309,20 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 const Slot& w = slot[i];
-                if (!fresh[i]) continue;
-                float x[16];
-                unpack(raw[i], x);
-                rotate(p, w, cs, x);
-                __nv_bfloat16* out = p.q_out + ((row0 + w.token) * c.Hq + t.h) * c.D;
-                *reinterpret_cast<uint4*>(out + w.o1) =
-                    make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
-                               pack2(x[6], x[7]));
-                *reinterpret_cast<uint4*>(out + w.o2) =
-                    make_uint4(pack2(x[8], x[9]), pack2(x[10], x[11]), pack2(x[12], x[13]),
-                               pack2(x[14], x[15]));
+                if (!w.there()) continue;
+                Raw y = raw[i];
+                if (w.rotated()) {
+                    float x[16];
+                    unpack(y, x);
+                    rotate(p, w, cs, x);
+                    y.a = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
+                                     pack2(x[6], x[7]));
+                    y.b = make_uint4(pack2(x[8], x[9]), pack2(x[10], x[11]), pack2(x[12], x[13]),
+                                     pack2(x[14], x[15]));
+                }
+                __nv_bfloat16* out = p.q_out + ((row0 + w.token()) * c.Hq + t.h) * c.D;
+                *reinterpret_cast<uint4*>(out + w.o1()) = y.a;
+                *reinterpret_cast<uint4*>(out + w.o2()) = y.b;
             }
             continue;
         }
@@ -308,12 +330,16 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const Slot& w = slot[i];
-            if (!fresh[i]) continue;
-            float x[16];
-            unpack(raw[i], x);
-            if (t.is_k) rotate(p, w, cs, x);
+            if (!w.there()) continue;
+            if (t.is_k && w.rotated()) {
+                float x[16];
+                unpack(raw[i], x);
+                rotate(p, w, cs, x);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+                for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+            } else {
+                top = fmaxf(top, largest(raw[i]));
+            }
         }
         const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
         const int64_t group = static_cast<int64_t>(page) * c.Hkv + t.h;
@@ -345,18 +371,18 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const Slot& w = slot[i];
-            if (!fresh[i]) continue;
+            if (!w.there()) continue;
             float x[16];
             unpack(raw[i], x);
-            if (t.is_k) rotate(p, w, cs, x);
+            if (t.is_k && w.rotated()) rotate(p, w, cs, x);
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o[j] = cvt_e4m3x2(x[4 * j] * f, x[4 * j + 1] * f) |
                        cvt_e4m3x2(x[4 * j + 2] * f, x[4 * j + 3] * f) << 16;
-            uint8_t* out = codes + w.token * c.D;
-            *reinterpret_cast<uint2*>(out + w.o1) = make_uint2(o[0], o[1]);
-            *reinterpret_cast<uint2*>(out + w.o2) = make_uint2(o[2], o[3]);
+            uint8_t* out = codes + w.token() * c.D;
+            *reinterpret_cast<uint2*>(out + w.o1()) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2*>(out + w.o2()) = make_uint2(o[2], o[3]);
         }
     }
 }
@@ -448,6 +474,8 @@ extern "C" int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_
     p.inv_freq = inv_freq;
     p.rot = static_cast<int32_t>(rot);
     p.interleaved = interleaved;
+    p.by_rot = rot ? static_cast<int32_t>(65536 / (rot / 16) + 1) : 0;
+    p.by_rest = D > rot ? static_cast<int32_t>(65536 / ((D - rot) / 16) + 1) : 0;
     p.rope_scale = rope_scale;
     p.status = device_status_ptr(dev);
 
