@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
 FASTCALL = os.path.join(PKG, "_fastcall.so")
 SOURCES = ["api_common.cu", "quant.cu", "gemm.cu", "linear.cu", "linear_noalloc.cu", "gemv.cu",
-           "fp8kv_append.cu", "fp8kv_attention.cu"]
+           "gemv_direct.cu", "fp8kv_append.cu", "fp8kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

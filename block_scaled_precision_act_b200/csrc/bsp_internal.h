@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <utility>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "bsp.h"
@@ -32,6 +33,12 @@ int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t
 // the 128-byte swizzle (bytes past D are zeros).
 int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens, uint64_t groups,
                   uint32_t box_tokens);
+
+// nvfp4_gemv in one launch, and the sizes for which that is the faster way.
+bool gemv_is_small(int64_t M, int64_t N, int64_t K, int sms);
+int gemv_direct(const __nv_bfloat16* x, const uint8_t* w_codes, const uint8_t* w_sf,
+                const float* w_scale, const __nv_bfloat16* bias, __nv_bfloat16* out, int64_t M,
+                int64_t N, int64_t K, int dev, int sms, cudaStream_t stream);
 
 // nvfp4_gemm (nvf4) / fp8r_gemm launched right after the library's activation quantizer
 // wrote `a` (and `a_sf`): same results, but the weight operand's first stages are fetched

@@ -542,6 +542,11 @@ int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
     int dev = 0, sms = 0;
     st = check_device(&dev, &sms);
     if (st != BSP_OK) return st;
+    if (gemv_is_small(M, N, K, sms))
+        return gemv_direct(static_cast<const __nv_bfloat16*>(x_bf16), w_codes, w_sf, w_scale,
+                           static_cast<const __nv_bfloat16*>(bias_bf16),
+                           static_cast<__nv_bfloat16*>(out_bf16), M, N, K, dev, sms,
+                           reinterpret_cast<cudaStream_t>(stream));
     static std::atomic<bool> ready[kMaxDevices];
     constexpr int kSmem = kRingBytes + 1024;
     if (!ready[dev].load(std::memory_order_acquire)) {

@@ -1,0 +1,451 @@
+// gemv_direct.cu -- nvfp4_gemv of a small weight, in one launch:
+//     y[m][n] = bf16(g * sum_k x[m][k] w[n][k] + bias[n]),   w = e2m1(code) * e4m3(scale).
+//
+// A small weight is read in a microsecond or two, so what bounds the call is latency: the kernel that
+// splits x for the tensor cores' 4-bit operands, and the one that waits for it, take 7 to 9 us
+// however small the weight is.  Here x stays 16 bits wide and the weight becomes f16 (e2m1 * e4m3
+// has at most 6 significant bits and lies in [2^-10, 2688]: exact) on its way through
+// mma.sync m16n8k16 with fp32 sums, 16 weight rows against 8 rows of x.  x is bf16, whose range f16
+// lacks: it is scaled by a power of two per row of x and piece of K, so that its largest element is in
+// [2^14, 2^15); f16 then holds elements down to 2^-28 of that exactly and rounds smaller ones by
+// at most 2^-39 of it.
+//
+// A cluster of up to eight CTAs takes a 128-row tile of the weight (the tile of the scale layout),
+// each a piece of K, and adds its sums through distributed shared memory, in order.  A warp takes the
+// 32 rows r, r + 32, r + 64, r + 96 for 8 values of r, whose scales lie in the same 16-byte words, and
+// every other 256-element step of K: per step a lane reads 32 bytes of codes of each of its four rows
+// and one 16-byte word of scales, all of which it uses.  The products may run over k in any order, so
+// these 64 consecutive codes of a row are the k slots that the lane owns in 16 products.  All of a
+// warp's first step is asked for before x is staged, and each half of the next as soon as one is used.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "bsp_internal.h"
+#include "bsp_ptx.cuh"
+#include "nvfp4_block.cuh"
+
+namespace bsp {
+namespace {
+
+constexpr int kMaxRows = 16;                    // of x: two tiles of 8
+constexpr int kThreads = 256;
+constexpr int kTileRows = 128;
+constexpr int kStepK = 256;
+constexpr int kStepBytes = kStepK * 2;          // of one row of x in f16
+constexpr int kMaxPieces = 8;
+constexpr int kMaxCostWhole = 1500;             // of a CTA: see gemv_is_small
+constexpr int kMaxCostCut = 2200;
+constexpr int kMaxSteps = kMaxCostCut / 232;    // that such a CTA can have
+constexpr int kMaxStage = 76 * 1024;            // shared memory for x
+static_assert(kMaxRows * (kMaxSteps * kStepBytes + 32) <= kMaxStage, "x of a piece fits");
+
+struct GemvParams {
+    const __nv_bfloat16* x;
+    const uint8_t* codes;
+    const uint8_t* sf;
+    const float* scale;
+    const __nv_bfloat16* bias;
+    __nv_bfloat16* out;
+    int32_t M, N, K;
+    int32_t steps;            // of K in all
+    int32_t row_bytes;        // between the rows of x in shared memory
+};
+
+__device__ __forceinline__ float pow2_biased(int e)     // 2^(e - 127), e in [0, 254]
+{
+    return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
+}
+
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// the E4M3 scale in byte i of w, twice in an f16 pair
+__device__ __forceinline__ uint32_t scale_to_f16(uint32_t w, int i)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+        : "=r"(r)
+        : "r"(__byte_perm(w, 0, i * 0x11)));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word_of(uint4 v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A lane's loads of half a step (128 elements of K): 32 codes of each of its four rows, at t * 32
+// of the half, so that four lanes read 64 bytes of a row side by side; and the 16 scales of those
+// rows and the 64 elements that hold the lane's two blocks.  Rows past N and elements past K are
+// read from the last ones instead: the results of such rows are not stored, and x is zero there.
+struct HalfStep {
+    uint4 c[4];
+    uint4 s;                  // word q: row + 32 q
+};
+
+struct LaneRows {
+    const uint8_t* codes;     // of the lane's first row
+    const uint8_t* sf;
+    uint32_t off[3];          // from there to the other rows' codes
+};
+
+__device__ __forceinline__ uint4 ldg_once(const void* a)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(a));
+    return v;
+}
+
+__device__ __forceinline__ LaneRows lane_rows(const GemvParams& p, int tile, int row_in_tile)
+{
+    LaneRows r;
+    const int row = min(tile * kTileRows + row_in_tile, p.N - 1);
+    r.codes = p.codes + static_cast<int64_t>(row) * (p.K / 2);
+#pragma unroll
+    for (int q = 1; q < 4; ++q)
+        r.off[q - 1] = static_cast<uint32_t>(min(row + 32 * q, p.N - 1) - row) * (p.K / 2);
+    r.sf = p.sf + static_cast<int64_t>(tile) * (p.K / 64) * 512 + row_in_tile * 16;
+    return r;
+}
+
+__device__ __forceinline__ void load_half(const GemvParams& p, const LaneRows& r, int s, int t,
+                                          int half, HalfStep& d)
+{
+    const uint32_t kt = min(s * 4 + 2 * half + (t >> 1), p.K / 64 - 1);
+    const uint8_t* a = r.codes + (kt * 32 + (t & 1) * 16);
+    d.c[0] = ldg_once(a);
+    d.c[1] = ldg_once(a + r.off[0]);
+    d.c[2] = ldg_once(a + r.off[1]);
+    d.c[3] = ldg_once(a + r.off[2]);
+    d.s = __ldg(reinterpret_cast<const uint4*>(r.sf + kt * 512));
+}
+
+// Biased exponent that a row of x goes by: the row is multiplied by 2^(14 - (e - 127)).
+__device__ __forceinline__ int x_exponent(uint32_t amax_bits)
+{
+    return max(15, static_cast<int>(amax_bits >> 23));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+
+// Steps [a0, a1) of x, a1 > a0, to shared memory in f16; beyond K it is zeros.  Of the
+// 32 16-byte chunks of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped: with
+// that the eight lanes of one shared memory read (four t, two g) are in different banks.  amax:
+// bits of the largest |x| of each row, 0 before.  A warp takes one step of one row at a time and
+// copies all of its own first, so that their latencies overlap; a lane touches no other's.
+// Every thread calls; the stage is readable on return.
+__device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uint4* xs,
+                                        uint32_t* amax)
+{
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int steps = a1 - a0;
+    uint8_t* base = reinterpret_cast<uint8_t*>(xs) + (lane ^ ((lane >> 3) & 1)) * 16;
+    // units (row m, step s) go to the warps in turn
+    const int m0 = warp / steps, s0 = warp - m0 * steps;
+    const int dm = kWarps / steps, ds = kWarps - dm * steps;
+    for (int m = m0, s = s0; m < p.M;) {
+        const int k = (a0 + s) * kStepK + lane * 8;
+        const bool in = k < p.K;
+        cp_async16(smem_u32(base + m * p.row_bytes + s * kStepBytes),
+                   p.x + (in ? static_cast<int64_t>(m) * p.K + k : 0), in);
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int m = m0, s = s0; m < p.M;) {
+        const uint4 v = *reinterpret_cast<const uint4*>(base + m * p.row_bytes + s * kStepBytes);
+        const uint32_t a = max_bf16x2(max_bf16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                      max_bf16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(a << 16, a & 0xFFFF0000u));
+        if (lane == 0) atomicMax(&amax[m], top);
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
+        }
+    }
+    __syncthreads();
+    for (int m = m0, s = s0; m < p.M;) {
+        uint4* at = reinterpret_cast<uint4*>(base + m * p.row_bytes + s * kStepBytes);
+        const float up = pow2_biased(268 - x_exponent(amax[m]));     // 2^(14 - (e - 127))
+        const uint4 v = *at;
+        uint4 h;
+        h.x = pack_f16(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up);
+        h.y = pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up);
+        h.z = pack_f16(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up);
+        h.w = pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up);
+        *at = h;
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
+        }
+    }
+    __syncthreads();
+}
+
+// NT: 8-row tiles of x.  Grid: the row tiles' clusters.
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const GemvParams p)
+{
+    extern __shared__ uint4 xs[];               // x in f16
+    __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
+    __shared__ uint32_t amax[NT * 8];           // bits of the largest |x| of this piece
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int oct = warp & 3, kw = warp >> 2;
+    uint32_t rank, pieces;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(pieces));
+    const int tile = blockIdx.x / pieces;
+    const int c0 = p.steps * rank / pieces, c1 = p.steps * (rank + 1) / pieces;
+
+    // in registers: the two halves of the step at hand, each replaced by the next step's as soon
+    // as it is used
+    HalfStep w[2];
+    const LaneRows rows = lane_rows(p, tile, oct * 8 + g);
+    if (c0 + kw < c1) {
+        load_half(p, rows, c0 + kw, t, 0, w[0]);
+        load_half(p, rows, c0 + kw, t, 1, w[1]);
+    }
+    if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
+    __syncthreads();
+    stage_x(p, c0, c1, xs, amax);
+
+    // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
+    // Rows of a tile past M read the last row; their columns are not stored.
+    const uint8_t* xg[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, p.M - 1) * p.row_bytes +
+                 t * 64;
+    const int swap = (t >> 1) * 16;
+    float acc[2][NT][4] = {};
+    for (int s = c0 + kw; s < c1; s += 2) {
+        const int xo = (s - c0) * kStepBytes;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 b[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    b[nt] = *reinterpret_cast<const uint4*>(
+                        xg[nt] + xo + half * 256 + ((j * 16) ^ swap));
+                uint32_t h[4][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // scale byte 2 (t % 2) + j / 2 of the row's word
+                    const uint32_t sc =
+                        scale_to_f16(word_of(w[half].s, q), (t & 1) * 2 + (j >> 1));
+                    e2m1x8_to_f16(word_of(w[half].c[q], j), h[q]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(acc[0][nt], h[0][0], h[1][0], h[0][1], h[1][1], b[nt].x, b[nt].y);
+                    mma_f16(acc[1][nt], h[2][0], h[3][0], h[2][1], h[3][1], b[nt].x, b[nt].y);
+                    mma_f16(acc[0][nt], h[0][2], h[1][2], h[0][3], h[1][3], b[nt].z, b[nt].w);
+                    mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
+                }
+            }
+            if (s + 2 < c1) load_half(p, rows, s + 2, t, half, w[half]);
+        }
+    }
+
+    // sums of the two halves of the warps, then of the cluster's CTAs, in order
+    const float gs = __ldg(p.scale);
+#pragma unroll
+    for (int half = 1; half >= 0; --half) {
+        if (kw == half) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ta = 0; ta < 2; ++ta)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = oct * 8 + g + 64 * ta + 32 * (i >> 1);
+                        const int col = nt * 8 + 2 * t + (i & 1);
+                        // a row of x that is not finite gives NaN, whichever piece finds that
+                        const float v = amax[col] < 0x7F800000u
+                                            ? acc[ta][nt][i] * gs *
+                                                  pow2_biased(x_exponent(amax[col]) - 14)
+                                            : NAN;
+                        part[col][r] = half ? v : part[col][r] + v;
+                    }
+        }
+        __syncthreads();
+    }
+    if (pieces > 1) cluster_sync();
+    // a thread keeps its row n: 128 / pieces rows, and every (kThreads / that)-th row of x
+    const int share = kTileRows / pieces;
+    const int r = rank * share + (threadIdx.x & (share - 1)), n = tile * kTileRows + r;
+    const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f;
+    for (int m = threadIdx.x / share; m < p.M; m += kThreads / share) {
+        if (n >= p.N) break;
+        float v;
+        if (pieces == 1) {
+            v = part[m][r];
+        } else {
+            const uint32_t at = smem_u32(&part[m][r]);
+            float y[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                y[j] = 0.0f;
+                if (j < pieces)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(y[j])
+                                 : "r"(mapa_shared(at, j)));
+            }
+            v = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+        }
+        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(v + bias);
+    }
+    if (pieces > 1) cluster_sync();             // the others have read this CTA's sums before it ends
+}
+
+// Pieces of K: as many as leave each half of the warps of a CTA a step and, of all tiles, keep to two
+// CTAs an SM.
+int pieces_of(int64_t tiles, int64_t steps, int sms)
+{
+    int c = 1;
+    while (c < kMaxPieces && 4 * c <= steps && 2 * c * tiles <= 2 * sms) c *= 2;
+    return c;
+}
+
+template <int NT>
+int launch_direct(const GemvParams& p, int tiles, int pieces, int dev, cudaStream_t stream)
+{
+    static std::atomic<bool> ready[kMaxDevices];
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(nvfp4_gemv_direct_kernel<NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxStage) != cudaSuccess) {
+            cudaGetLastError();
+            return BSP_ERR_CUDA;
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = pieces;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles) * pieces, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * p.row_bytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, nvfp4_gemv_direct_kernel<NT>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return BSP_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+// The direct kernel is taken by what a CTA has to do, in instructions of a warp: for each 256-element
+// step 200, 32 for each 8 rows of x and 10 for bringing a row's step of x to shared memory, and as
+// much as a step's for the sums.  Where a tile of the weight is cut into four pieces or eight, the
+// limit is higher: there the other kernel cuts tiles too, and joins them through global memory.
+// Measured, us, here and with the two other kernels:
+//     4096 x 4096:  M = 1 6.4, 8.6;   M = 8 7.6, 8.8;    M = 16 9.0, 10.7    (costs 716 to 1112)
+//     2048 x 8192:  M = 1 6.8, 10.0;  M = 8 8.4, 10.2;   M = 16 11.5, 12.5   (1200 to 1960)
+//     4096 x 14336: M = 1 11.0, 14.3; M = 8 13.3, 14.6;  M = 16 17.9, 16.2   (1926, 2416, 3512)
+//     10368 x 2048: M = 1 7.3, 7.9;   M = 8 9.1, 8.1;    M = 16 12.0, 8.8    (1200, 1480, 1960; two pieces)
+//     65536 x 768:  M = 1 10.8, 15.6; M = 8 13.2, 16.0;  M = 16 17.1, 20.4   (958, 1168, 1536; one piece)
+//     131072 x 2048: M = 1 36.9, 34.0; M = 8 44.2, 35.0                      (2168, 2728; one piece)
+bool gemv_is_small(int64_t M, int64_t N, int64_t K, int sms)
+{
+    if (M > kMaxRows) return false;
+    const int64_t tiles = (N + kTileRows - 1) / kTileRows, steps = (K + kStepK - 1) / kStepK;
+    const int c = pieces_of(tiles, steps, sms);
+    const int64_t most = (steps + c - 1) / c;
+    return (most + 1) * (M <= 8 ? 232 : 264) + most * M * 10 <=
+           (c >= 4 ? kMaxCostCut : kMaxCostWhole);
+}
+
+int gemv_direct(const __nv_bfloat16* x, const uint8_t* w_codes, const uint8_t* w_sf,
+                const float* w_scale, const __nv_bfloat16* bias, __nv_bfloat16* out, int64_t M,
+                int64_t N, int64_t K, int dev, int sms, cudaStream_t stream)
+{
+    const int64_t tiles = (N + kTileRows - 1) / kTileRows, steps = (K + kStepK - 1) / kStepK;
+    const int c = pieces_of(tiles, steps, sms);
+    GemvParams p = {};
+    p.x = x;
+    p.codes = w_codes;
+    p.sf = w_sf;
+    p.scale = w_scale;
+    p.bias = bias;
+    p.out = out;
+    p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.steps = static_cast<int32_t>(steps);
+    p.row_bytes = static_cast<int32_t>((steps + c - 1) / c) * kStepBytes + 32;
+    return M <= 8 ? launch_direct<1>(p, static_cast<int>(tiles), c, dev, stream)
+                  : launch_direct<2>(p, static_cast<int>(tiles), c, dev, stream);
+}
+
+}  // namespace bsp

@@ -183,3 +183,28 @@ def test_vector_shapes_through_quant_linear(shape):
     q.weight_only_rows = 0                          # the default: activations quantized
     q8 = QuantLinear.from_state_dict(q.state_dict())
     assert torch.equal(q(x), q8(x))
+
+
+@pytest.mark.parametrize("N,K", [(40008, 192), (131072, 256), (16000, 1088), (8200, 2624), (136, 4416),
+                                 (2048, 16384)])
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 17])
+def test_small_weights_in_one_launch_and_two(M, N, K):
+    """The K of a tile in one, two, four and eight pieces of even and uneven lengths, and the sizes past
+    which the call goes the other way.  In one launch x is held in f16 to 2^-39 of the largest of its
+    piece, a warp's sum is a chain of at most 64 products of 16, and 11 sums join: inside the bound."""
+    codes, sf, g = weight(N, K, N + K)
+    x = synth.bf16_normal((M, K), 1.0, M, 0.01, 30.0).cuda()
+    bias = synth.bf16_normal((N,), 0.1, 7).cuda() if M % 2 else None
+    check(bsp.nvfp4_gemv(x, codes, sf, g, bias=bias), x, codes, sf, g, bias)
+
+
+@pytest.mark.parametrize("N,K", [(136, 4416), (8200, 2624), (40008, 192), (1024, 16640)])
+def test_a_row_that_is_not_finite(N, K):
+    codes, sf, g = weight(N, K, 51)
+    x = synth.bf16_normal((12, K), 1.0, 52).cuda()
+    clean = bsp.nvfp4_gemv(x, codes, sf, g)
+    for i, v in enumerate([math.inf, -math.inf, math.nan]):
+        for j, k in enumerate([0, K // 2, K - 1]):
+            x[3 * i + j, k] = v
+    y = bsp.nvfp4_gemv(x, codes, sf, g)
+    assert y[:9].isnan().all() and torch.equal(y[9:], clean[9:])
