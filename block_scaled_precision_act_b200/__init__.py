@@ -162,6 +162,17 @@ def _stream(stream):
     return int(stream)
 
 
+def _scratch(nbytes: int, device, stream):
+    """A call's own workspace, allocated for the stream that the call runs on: its memory may be
+    given away as soon as the call returns, and then only to work behind the call's kernels."""
+    if stream is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+
 def _dtype(t, dt, what):
     if t.dtype != dt:
         raise TypeError(f"{what} must be {dt}, got {t.dtype}")
@@ -423,8 +434,7 @@ def nvfp4_gemv(x: torch.Tensor, w_codes, w_sf, w_scale, bias=None, out=None, wor
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _buf(out, torch.bfloat16, "out", M * N)
     if workspace is None:
-        workspace = torch.empty((nvfp4_gemv_workspace_bytes(M, N, K),), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _scratch(nvfp4_gemv_workspace_bytes(M, N, K), x.device, stream)
     _buf(workspace, torch.uint8, "workspace", 0)
     _check("nvfp4_gemv",
            lib().nvfp4_gemv(_ptr(x), _ptr(w_codes), _ptr(w_sf), _ptr(w_scale), _ptr(bias),
@@ -552,8 +562,7 @@ def fp8kv_attention(q: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_t
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     _buf(lse, torch.float32, "lse", T * Hq)
     if workspace is None:
-        workspace = torch.empty((fp8kv_attention_workspace_bytes(T, Hq, Hkv, D),),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _scratch(fp8kv_attention_workspace_bytes(T, Hq, Hkv, D), q.device, stream)
     _buf(workspace, torch.uint8, "workspace", 0)
     _check("fp8kv_attention",
            lib().fp8kv_attention(_rows_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),

@@ -203,7 +203,7 @@ __device__ __forceinline__ bool find_unit(const AppendParams& p, int64_t u, Unit
     __syncthreads();
     for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
         const KvRows r = kv_rows(c, i);
-        const int32_t len = kv_length(c, i);
+        const int32_t len = c.kv_len[i];
         const int64_t at = static_cast<int64_t>(r.first) * p.per / kKvBlock +
                            static_cast<int64_t>(p.extra) * i;
         const int64_t next = static_cast<int64_t>(r.first + r.n) * p.per / kKvBlock +
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
     if (!find_unit(p, u, unit)) return;
     const int b = unit.b;
     const int32_t len = unit.len, start = len - unit.n;  // position of the first new token
-    if (start < 0) {
+    if (start < 0 || len > kv_capacity(c)) {
         if (u == unit.begin && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
         return;
     }
@@ -280,14 +280,13 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
         }
     };
     if (task < tasks) load(task_of(p, task, row0));
-    const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages +
-                               block / c.page_blocks);
+    const int32_t page = c.table[static_cast<int64_t>(b) * c.max_pages + block / c.page_blocks];
 
     const int half = p.rot >> 1;
     for (int i = threadIdx.x; i < kKvBlock * half; i += kAppendThreads) {
         const int t = i / half, j = i - t * half;
         if (t < lo || t >= hi) continue;
-        const double x = static_cast<double>(pos0 + t) * static_cast<double>(__ldg(p.inv_freq + j));
+        const double x = static_cast<double>(pos0 + t) * static_cast<double>(p.inv_freq[j]);
         const double turns = x * 0.15915494309189535;                    // 1 / (2 pi)
         float sn, cn;
         sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn, &cn);
@@ -400,7 +399,7 @@ int kv_check_cache(KvCache& c, const void* k_cache, const void* v_cache, const v
     constexpr int64_t kMost = int64_t{1} << 30;
     if (D % 16 != 0 || D > 256 || page_size % kKvBlock != 0 || page_size > 4096 ||
         Hq % Hkv != 0 || Hkv > 4096 || Hq > 4096 || B > (1 << 20) || T > kMost / 64 ||
-        pages > kMost || max_pages > kMost || T * Hq > kMost)
+        pages > kMost || max_pages > kMost / page_size || T * Hq > kMost)
         return BSP_ERR_UNSUPPORTED_SHAPE;
     c.k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
     c.v = static_cast<uint8_t*>(const_cast<void*>(v_cache));

@@ -110,18 +110,22 @@ struct SeqWork {
     int32_t row_tiles, tile0, tiles;
 };
 
-__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, KvRows r, int32_t len)
 {
     SeqWork s;
-    const KvRows r = kv_rows(p.c, b);
     s.first = r.first;
     s.n = r.n;
-    s.len = kv_length(p.c, b);
+    s.len = len;
     s.row_tiles = (s.n * p.G + p.rows - 1) / p.rows;
     const int32_t lo = p.window ? max(0, s.len - s.n - p.window + 1) : 0;
     s.tile0 = lo / kTile;
     s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
     return s;
+}
+
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
+{
+    return seq_work(p, kv_rows(p.c, b), kv_length(p.c, b));
 }
 
 // Weight of an item of the sequence, and of all of them
@@ -260,9 +264,30 @@ struct Segment {
     bool begins, whole;
 };
 
+// A whole warp walks: every lane holds the same state.
 struct SegmentWalk {
     int64_t at, end, before;
     int b;
+
+    // The next sequence that has new tokens (or the last of all), 32 looked at together: a padded batch
+    // may hold many that have none.
+    __device__ __forceinline__ SeqWork next_sequence(const AttnParams& p)
+    {
+        KvRows r;
+        int32_t len;
+        uint32_t found;
+        do {
+            const int i = min(b + 1 + static_cast<int>(threadIdx.x & 31), p.c.B - 1);
+            r = kv_rows(p.c, i);
+            len = kv_length(p.c, i);
+            found = __ballot_sync(0xFFFFFFFFu, r.n > 0);
+            b = min(b + (found ? __ffs(found) : 32), p.c.B - 1);
+        } while (!found && b + 1 < p.c.B);
+        const int from = found ? __ffs(found) - 1 : 31;
+        r.first = __shfl_sync(0xFFFFFFFFu, r.first, from);
+        r.n = __shfl_sync(0xFFFFFFFFu, r.n, from);
+        return seq_work(p, r, __shfl_sync(0xFFFFFFFFu, len, from));
+    }
 
     __device__ __forceinline__ bool next(const AttnParams& p, const Split& split, Segment& s)
     {
@@ -271,7 +296,7 @@ struct SegmentWalk {
             int64_t mine = seq_weight(p, s.sw, split.aligned);
             while (at >= before + mine && b + 1 < p.c.B) {
                 before += mine;
-                s.sw = seq_work(p, ++b);
+                s.sw = next_sequence(p);
                 mine = seq_weight(p, s.sw, split.aligned);
             }
             const int weight = item_weight(p, s.sw, split.aligned);
@@ -490,7 +515,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         tmem_relinquish();
     }
     griddep_wait();
-    griddep_launch_dependents();
     Split cut_up;                                // only the loads ask for it
     if (p.c.B > 32)
         cut_up = find_run(p, split);
@@ -499,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch_dependents();                 // not before this CTA has its tensor memory
     const uint32_t tbase = tmem_holder;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -529,13 +554,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             ok = __shfl_sync(0xFFFFFFFFu, room, 0);
             if (!ok || !more) break;
             const int len = seg.sw.len;
+            if (lane == 0 && c.kv_len[seg.b] != len) kv_report_bad_batch(p.status);
             const int lo = p.window ? max(0, len - seg.sw.n - p.window + 1) : 0;
             const int32_t* row = c.table + static_cast<int64_t>(seg.b) * c.max_pages;
             // lane i takes box i of a tile; -1: nothing to load
             const auto page_of = [&](int tile) {
                 const int tok = tile * kTile + lane * p.box;
                 return lane < boxes && tile < seg.tile_end && tok < len && tok + p.box > lo
-                           ? __ldg(row + tok / page)
+                           ? row[tok / page]
                            : -1;
             };
             int32_t next_page = page_of(seg.tile_begin);
@@ -689,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             }
             const auto page_of = [&](int tile) {
                 const int tok = tile * kTile + t;
-                return tile < seg.tile_end && tok < len && tok >= lo ? __ldg(table + at_page) : -1;
+                return tile < seg.tile_end && tok < len && tok >= lo ? table[at_page] : -1;
             };
             const auto forward = [&] {
                 at_page += step_pages;
@@ -704,8 +730,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 if (x.in) {
                     const int64_t at =
                         (static_cast<int64_t>(id) * c.Hkv + seg.h) * c.page_blocks + block;
-                    x.k = __ldg(c.k_scale + at);
-                    x.v = __ldg(c.v_scale + at);
+                    x.k = c.k_scale[at];
+                    x.v = c.v_scale[at];
                 }
                 return x;
             };

@@ -15,6 +15,9 @@
 
 namespace bsp {
 
+// What an earlier kernel of the stream may write is read by plain loads, after griddep_wait(): this
+// kernel may have begun before that one ended, so to it the data are not read-only.
+
 constexpr int kKvBlock = 16;        // tokens that share one scale
 constexpr int kKvMaxExp = 246;      // largest scale byte: 448 * 2^119 is the last finite multiple
 
@@ -44,17 +47,21 @@ __device__ __forceinline__ int32_t kv_clamp_row(int32_t r, int32_t T)
 
 __device__ __forceinline__ KvRows kv_rows(const KvCache& c, int b)
 {
-    const int32_t lo = kv_clamp_row(__ldg(c.cu_new + b), c.T);
-    const int32_t hi = kv_clamp_row(__ldg(c.cu_new + b + 1), c.T);
+    const int32_t lo = kv_clamp_row(c.cu_new[b], c.T);
+    const int32_t hi = kv_clamp_row(c.cu_new[b + 1], c.T);
     return {lo, hi > lo ? hi - lo : 0};
 }
 
-// kv_len[b], cut to what the table's row can address.
+// Tokens that a row of the table can address.
+__device__ __forceinline__ int32_t kv_capacity(const KvCache& c)
+{
+    return static_cast<int32_t>(c.max_pages) * c.page_blocks * kKvBlock;
+}
+
+// kv_len[b], cut to that.
 __device__ __forceinline__ int32_t kv_length(const KvCache& c, int b)
 {
-    const int64_t cap = c.max_pages * c.page_blocks * kKvBlock;
-    const int32_t l = __ldg(c.kv_len + b);
-    return l < 0 ? 0 : (l > cap ? static_cast<int32_t>(cap) : l);
+    return min(max(c.kv_len[b], 0), kv_capacity(c));
 }
 
 // Smallest scale byte whose 448 multiples reach amax (bits of a non-negative fp32):
@@ -92,8 +99,8 @@ __device__ __forceinline__ void f16x2_to_f32(uint32_t h, float& lo, float& hi)
         : "r"(h));
 }
 
-// Device status word: a page outside the pool, or a length below the new tokens' count (first
-// writer wins).
+// Device status word: a page outside the pool, or a length that does not fit the new tokens or the
+// table (first writer wins).
 __device__ __forceinline__ void kv_report_bad_batch(int* status)
 {
     if (atomicCAS(status, 0, BSP_ERR_INVALID_ARG) == 0) atomicCAS(status + 1, 0, 200);

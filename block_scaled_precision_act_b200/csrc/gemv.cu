@@ -132,9 +132,8 @@ __device__ __forceinline__ uint32_t max_bits(const uint4 (&v)[2])
 
 // One CTA per row of x; a thread takes 16-element blocks.  Also zeroes the counters of the tiles.
 __global__ void __launch_bounds__(1024)
-    nvfp4_gemv_split_kernel(const __nv_bfloat16* __restrict__ x, int K, int mp, int nb,
-                            uint8_t* __restrict__ xc, int32_t* __restrict__ rho,
-                            int32_t* __restrict__ done, int counters)
+    nvfp4_gemv_split_kernel(const __nv_bfloat16* x, int K, int mp, int nb,
+                            uint8_t* xc, int32_t* rho, int32_t* done, int counters)
 {
     __shared__ uint32_t warp_max[32];
     griddep_wait();
@@ -196,7 +195,6 @@ __device__ __forceinline__ int run_owner(int64_t total, int ctas, int64_t s)
 __global__ void __launch_bounds__(kThreads, 1)
     nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap tm_w, const GemvArgs args)
 {
-    griddep_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -280,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch_dependents();             // not before this CTA has its tensor memory
     const uint32_t tbase = tmem_holder;
 
     if (warp == 0) {
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3, row = q * 32 + lane;
         griddep_wait();                          // the exponents and the counters are written
-        const float g = __ldg(args.w_scale);
+        const float g = *args.w_scale;
         if (lane < args.M) {                     // each warp writes them all: the same values
             const int e = __ldcg(args.rho + lane);
             factor[lane] = e == kPoison ? make_float2(NAN, NAN)

@@ -127,10 +127,12 @@ struct LaneRows {
     uint32_t off[3];          // from there to the other rows' codes
 };
 
-__device__ __forceinline__ uint4 ldg_once(const void* a)
+// Not the read-only path: the weight may be an earlier kernel's output, and this kernel may have begun
+// before that one ended.
+__device__ __forceinline__ uint4 ld_once(const void* a)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(a));
     return v;
@@ -153,11 +155,11 @@ __device__ __forceinline__ void load_half(const GemvParams& p, const LaneRows& r
 {
     const uint32_t kt = min(s * 4 + 2 * half + (t >> 1), p.K / 64 - 1);
     const uint8_t* a = r.codes + (kt * 32 + (t & 1) * 16);
-    d.c[0] = ldg_once(a);
-    d.c[1] = ldg_once(a + r.off[0]);
-    d.c[2] = ldg_once(a + r.off[1]);
-    d.c[3] = ldg_once(a + r.off[2]);
-    d.s = __ldg(reinterpret_cast<const uint4*>(r.sf + kt * 512));
+    d.c[0] = ld_once(a);
+    d.c[1] = ld_once(a + r.off[0]);
+    d.c[2] = ld_once(a + r.off[1]);
+    d.c[3] = ld_once(a + r.off[2]);
+    d.s = ld_once(r.sf + kt * 512);
 }
 
 // Biased exponent that a row of x goes by: the row is multiplied by 2^(14 - (e - 127)).
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Ge
     }
 
     // sums of the two halves of the warps, then of the cluster's CTAs, in order
-    const float gs = __ldg(p.scale);
+    const float gs = *p.scale;
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
         if (kw == half) {

@@ -310,8 +310,8 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int layout,
  *           NULL, out_bf16 [M][N]: as nvfp4_gemm (block scales have no sign).
  *   Y[m][n] = bf16( w_scale * sum_k x[m][k] * e2m1(w[n][k]) * e4m3(sf[n][k/16]) + bias[n] ),
  *   sums in fp32.  x reaches the tensor cores held to 2^-19 of the largest element of its row (bf16
- *   holds an element to 2^-8 of itself).  A row that holds an infinity or a NaN gives NaN.  The rows
- *   do not affect one another.
+ *   holds an element to 2^-8 of itself), or to 2^-39 where the weight is small.  A row that holds an
+ *   infinity or a NaN gives NaN.  The rows do not affect one another.  out must not overlap x.
  *   workspace  device buffer of at least nvfp4_gemv_workspace_bytes(M, N, K) bytes, 16-byte
  *              aligned, any contents; not shared by calls that can run at the same time.
  * Constraints: K % 64 == 0, K >= 64; N % 8 == 0; M <= 32 (BSP_ERR_UNSUPPORTED_SHAPE).  The time
@@ -339,12 +339,13 @@ int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *               kv_len[b] - n .. kv_len[b] - 1.
  * Lengths, rows and pages are read on the device, so a captured graph can be replayed while
  * they change.  The kernels keep every access inside the arrays whatever these hold: rows
- * outside [0, T) and lengths outside [0, max_pages * page_size] are cut off, a page outside
- * [0, pages) is not touched (its tokens are neither stored nor attended to) and is reported by
- * bsp_last_device_status() as BSP_ERR_INVALID_ARG.  Table entries of pages that a call does not
- * reach are not read.
+ * outside [0, T) are cut off; of a sequence whose length is outside [0, max_pages * page_size]
+ * fp8kv_append stores nothing and fp8kv_attention reads what the table holds; a page outside
+ * [0, pages) is not touched (its tokens are neither stored nor attended to).  Such lengths and pages
+ * are reported by bsp_last_device_status() as BSP_ERR_INVALID_ARG.  Table entries of pages that a
+ * call does not reach are not read.
  * Constraints: D % 16 == 0, D <= 256; page_size % 16 == 0, page_size <= 4096; Hq % Hkv == 0,
- * Hq and Hkv <= 4096; B <= 2^20, T <= 2^24, T * Hq <= 2^30.
+ * Hq and Hkv <= 4096; B <= 2^20, T <= 2^24, T * Hq <= 2^30; max_pages * page_size <= 2^30.
  */
 
 /*
@@ -365,7 +366,8 @@ int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   saturating at +-448.  Infinities store as +-448 * 2^119, a NaN stores as NaN (only its own
  *   element).
  * Tokens of the block after the last new one are left as they are.  A page that is appended to
- * must belong to one sequence of the batch; a sequence with kv_len[b] < n is left out and reported.
+ * must belong to one sequence of the batch; a sequence with kv_len[b] < n is left out and reported
+ * (neither stored nor, in q_out, rotated).
  */
 int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
                  const void* v_bf16, int64_t v_stride, const float* inv_freq, int64_t rot,
@@ -382,12 +384,15 @@ int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64
  *   q_bf16  [T][Hq][D], q_stride elements between tokens (% 8 == 0).
  *   out     [T][Hq][D] bf16, contiguous; lse [T][Hq] fp32 or NULL: log of sum_t p_t.
  *   A row that sees no token gives zeros and lse = -infinity.  Softmax statistics and sums are
- *   fp32; the weights p are rounded once to 11 bits.  What masked tokens hold (NaN, stale
- *   bytes, stale scales of blocks behind the end) has no effect.
+ *   fp32; q is held to 2^-26 of the largest element of its head (bf16 elements above 2^-18 of that
+ *   exactly), and a weight p is rounded once, to 11 bits, or to 2^-33 of the row's largest where it is
+ *   below 2^-22 of that.  Values that lie in blocks whose scale is less than 2^-40 of another block's of the
+ *   sequence may count as zeros.  What masked tokens hold (NaN, stale bytes, stale scales of blocks
+ *   behind the end) has no effect.  out must not overlap q or the cache.
  *   workspace  device buffer of at least fp8kv_attention_workspace_bytes(T, Hq, Hkv, D) bytes,
  *              16-byte aligned, any contents; not shared by calls that can run at the same time.
- * Meant for one to a few new tokens per sequence: every 16 rows (new tokens * Hq / Hkv) of a
- * sequence read its keys and values once more.
+ * Meant for one to a few new tokens per sequence: every 8 or 16 rows (new tokens * Hq / Hkv) of a
+ * sequence read its keys and values once more.  Constraint besides the cache's: pages * Hkv < 2^31.
  */
 int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache,
                     const uint8_t* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,

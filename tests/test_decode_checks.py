@@ -190,3 +190,9 @@ def test_paged_kv_cache_module():
     with pytest.raises(bsp.BSPError, match=ON_CPU):
         c.append(bf16(1, 2, 64), bf16(1, 2, 64), *[torch.zeros(s, dtype=torch.int32)
                                                   for s in ((1, 1), (2,), (1,))])
+
+
+@pytest.mark.parametrize("call", [append, attend])
+def test_tables_past_2_to_30_tokens(call):
+    assert call(max_pages=(1 << 25) + 1) == SHAPE           # pages of 32
+    assert call(max_pages=1 << 40) == SHAPE

@@ -271,3 +271,15 @@ def test_other_stream_and_replayed_graph():
     assert torch.equal(q_out, q0)
     for x, a in zip(("k_cache", "v_cache", "k_scale", "v_scale"), args):
         assert torch.equal(a.cpu(), got[x])
+
+
+def test_lengths_past_the_table_store_nothing():
+    b = Batch([2, 3], [20, 30], 4, 2, 64, 16, seed=21)
+    b.kv_len[0] = b.table.shape[1] * 16 + 1
+    _, got = call(b, 64)
+    assert bsp.bsp_last_device_status() == -1 and bsp.bsp_last_device_status() == 0
+    for page in b.table[0, :2].tolist():
+        assert torch.equal(got["k_cache"][page], b.k_cache[page])
+        assert torch.equal(got["v_scale"][page], b.v_scale[page])
+    last = int(b.table[1, 1])
+    assert not torch.equal(got["k_cache"][last], b.k_cache[last])

@@ -238,3 +238,79 @@ def test_two_streams_at_once_with_their_own_workspaces():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("B,every", [(40, 3), (200, 1), (200, 67), (450, 5)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_padded_batches(B, every, wide):
+    """Many sequences, most of them without new tokens (stretches longer than a warp looks at at once),
+    and tables that are wider than the lengths need."""
+    n = [(1 + i % 2) if i % every == every - 1 else 0 for i in range(B)]
+    b = Batch(n, [5 + 37 * i % 600 for i in range(B)], 4, 2, 64, 16, seed=B + every)
+    if wide:
+        b.table = torch.cat((b.table, torch.full((B, 300), -9, dtype=torch.int32)), 1)
+    out, lse = call(b)
+    assert bsp.bsp_last_device_status() == 0
+    check(b, out, lse)
+
+
+@pytest.mark.parametrize("n,lens,Hq,Hkv,D,page", [([1], [5000], 16, 8, 128, 4096),
+                                                  ([3, 2], [900, 70], 24, 2, 256, 48),
+                                                  ([2], [33000], 8, 1, 192, 64),
+                                                  ([1] * 3, [640, 639, 1], 8, 8, 128, 64),
+                                                  ([1] * 3, [641, 640, 1], 8, 8, 128, 64)])
+def test_more_sizes(n, lens, Hq, Hkv, D, page):
+    """Large pages, pages that end inside a tile, 16 rows of wide heads, tables at which items are cut
+    and at which they are not."""
+    b = Batch(n, lens, Hq, Hkv, D, page, seed=sum(lens))
+    check(b, *call(b))
+
+
+def test_shared_pages():
+    """Two sequences that have read the same pages, and one page twice in a sequence."""
+    b = Batch([1, 1], [150, 190], 8, 2, 64, 32, seed=30)
+    b.table[1, :4] = b.table[0, :4]
+    b.table[1, 4] = b.table[1, 2]
+    check(b, *call(b))
+
+
+def test_lengths_past_the_table_are_reported():
+    b = Batch([1, 1], [64, 40], 4, 2, 64, 16, seed=31)
+    want, _ = call(b)
+    cap = b.table.shape[1] * 16
+    b.kv_len[0] = cap + 3
+    out, _ = call(b)
+    assert bsp.bsp_last_device_status() == -1 and bsp.bsp_last_device_status() == 0
+    assert torch.equal(out, want)                   # cut to the table: 64 tokens
+
+
+def test_workspace_ends_where_it_says():
+    b = Batch([2] * 5, [700 + 300 * i for i in range(5)], 16, 2, 128, 64, seed=32)
+    need = bsp.fp8kv_attention_workspace_bytes(b.T, b.Hq, b.Hkv, b.D)
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = call(b, workspace=room[:need])
+    check(b, out, lse)
+    assert (room[need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_own_workspace_on_another_stream(as_int):
+    """The memory of a workspace that the call made itself is not given to the current stream's next
+    tensor while the call's kernels, far behind on another stream, still use it."""
+    b = Batch([1], [9000], 16, 4, 128, 64, seed=33)
+    dev = b.to("cuda")
+    q, args = b.q.cuda(), [dev[x] for x in NAMES]
+    want = bsp.fp8kv_attention(q, *args)
+    out = torch.zeros_like(want)
+    side = torch.cuda.Stream()
+    need = bsp.fp8kv_attention_workspace_bytes(b.T, b.Hq, b.Hkv, b.D)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    bsp.fp8kv_attention(q, *args, out=out, stream=side.cuda_stream if as_int else side)
+    spoil = [torch.zeros((need,), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for _ in range(200):
+        for x in spoil:
+            x.zero_()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -208,3 +208,53 @@ def test_a_row_that_is_not_finite(N, K):
             x[3 * i + j, k] = v
     y = bsp.nvfp4_gemv(x, codes, sf, g)
     assert y[:9].isnan().all() and torch.equal(y[9:], clean[9:])
+
+
+@pytest.mark.parametrize("M,N,K", [(32, 4104, 8192), (7, 10376, 2624), (1, 520, 65536)])
+def test_workspace_ends_where_it_says(M, N, K):
+    codes, sf, g = weight(N, K, 61)
+    x = synth.bf16_normal((M, K), 1.0, 62).cuda()
+    need = bsp.nvfp4_gemv_workspace_bytes(M, N, K)
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = bsp.nvfp4_gemv(x, codes, sf, g, out=out[:M * N], workspace=room[:need])
+    check(y.view(M, N), x, codes, sf, g)
+    assert (room[need:] == 0xA5).all() and (out[M * N:] == 7).all()
+
+
+def test_own_workspace_on_another_stream():
+    """The workspace that the call made itself is not given away while its kernels wait."""
+    codes, sf, g = weight(2048, 16384, 71)
+    x = synth.bf16_normal((9, 16384), 1.0, 72).cuda()
+    want = bsp.nvfp4_gemv(x, codes, sf, g)
+    out = torch.zeros_like(want)
+    side = torch.cuda.Stream()
+    need = bsp.nvfp4_gemv_workspace_bytes(9, 2048, 16384)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    bsp.nvfp4_gemv(x, codes, sf, g, out=out, stream=side)
+    spoil = [torch.zeros((need,), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for _ in range(200):
+        for y in spoil:
+            y.zero_()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_a_weight_written_just_before():
+    """The weight, its scales, x and the factor as the kernels in front of the call leave them, with no
+    wait in between: what an SM read of them in the call before is not used again."""
+    N, K = 4096, 1024
+    ws = [weight(N, K, 80 + i) for i in range(2)]
+    xs = [synth.bf16_normal((2, K), 1.0, 90 + i).cuda() for i in range(2)]
+    want = [bsp.nvfp4_gemv(x, *w) for x, w in zip(xs, ws)]
+    now, x = [t.clone() for t in ws[0]], xs[0].clone()
+    outs = []
+    for i in range(40):
+        for a, b in zip(now, ws[i % 2]):
+            a.copy_(b)
+        x.copy_(xs[i % 2])
+        outs.append(bsp.nvfp4_gemv(x, *now))
+    for i, y in enumerate(outs):
+        assert torch.equal(y, want[i % 2])
