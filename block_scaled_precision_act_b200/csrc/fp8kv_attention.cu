@@ -110,22 +110,18 @@ struct SeqWork {
     int32_t row_tiles, tile0, tiles;
 };
 
-__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, KvRows r, int32_t len)
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
 {
     SeqWork s;
+    const KvRows r = kv_rows(p.c, b);
     s.first = r.first;
     s.n = r.n;
-    s.len = len;
+    s.len = kv_length(p.c, b);
     s.row_tiles = (s.n * p.G + p.rows - 1) / p.rows;
     const int32_t lo = p.window ? max(0, s.len - s.n - p.window + 1) : 0;
     s.tile0 = lo / kTile;
     s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
     return s;
-}
-
-__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
-{
-    return seq_work(p, kv_rows(p.c, b), kv_length(p.c, b));
 }
 
 // Weight of an item of the sequence, and of all of them
@@ -269,24 +265,15 @@ struct SegmentWalk {
     int64_t at, end, before;
     int b;
 
-    // The next sequence that has new tokens (or the last of all), 32 looked at together: a padded batch
-    // may hold many that have none.
-    __device__ __forceinline__ SeqWork next_sequence(const AttnParams& p)
+    // A padded batch may hold many sequences without new tokens: passes the ones behind b, 32 at a time
+    __device__ __forceinline__ void skip_empty(const AttnParams& p)
     {
-        KvRows r;
-        int32_t len;
-        uint32_t found;
-        do {
-            const int i = min(b + 1 + static_cast<int>(threadIdx.x & 31), p.c.B - 1);
-            r = kv_rows(p.c, i);
-            len = kv_length(p.c, i);
-            found = __ballot_sync(0xFFFFFFFFu, r.n > 0);
-            b = min(b + (found ? __ffs(found) : 32), p.c.B - 1);
-        } while (!found && b + 1 < p.c.B);
-        const int from = found ? __ffs(found) - 1 : 31;
-        r.first = __shfl_sync(0xFFFFFFFFu, r.first, from);
-        r.n = __shfl_sync(0xFFFFFFFFu, r.n, from);
-        return seq_work(p, r, __shfl_sync(0xFFFFFFFFu, len, from));
+        uint32_t found = 0;
+        while (!found && b + 1 < p.c.B) {
+            const int i = b + 1 + static_cast<int>(threadIdx.x & 31);
+            found = __ballot_sync(0xFFFFFFFFu, i < p.c.B && kv_rows(p.c, i).n > 0);
+            b = min(b + (found ? __ffs(found) - 1 : 32), p.c.B - 1);
+        }
     }
 
     __device__ __forceinline__ bool next(const AttnParams& p, const Split& split, Segment& s)
@@ -296,8 +283,9 @@ struct SegmentWalk {
             int64_t mine = seq_weight(p, s.sw, split.aligned);
             while (at >= before + mine && b + 1 < p.c.B) {
                 before += mine;
-                s.sw = next_sequence(p);
+                s.sw = seq_work(p, ++b);
                 mine = seq_weight(p, s.sw, split.aligned);
+                if (s.sw.n == 0) skip_empty(p);
             }
             const int weight = item_weight(p, s.sw, split.aligned);
             const int64_t off = at - before;

@@ -35,6 +35,8 @@ def _u8(t: torch.Tensor) -> torch.Tensor:
 class QuantLinear(torch.nn.Module):
     """y = x W^T (+ bias) with W stored as nvfp4 or fp8r; x is bf16 [..., in_features]."""
 
+    weight_only_rows = 0         # also of a module that was pickled without it
+
     def __init__(self, in_features: int, out_features: int, scheme: str = "nvfp4",
                  bias: bool = True, device=None, weight_only_rows: int = 0):
         super().__init__()
