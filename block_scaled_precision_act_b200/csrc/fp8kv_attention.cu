@@ -1074,6 +1074,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         tc_commit(&fin);
         drain_wait(&fin, 0, p.wait_ns, p.status);
     }
+    __syncwarp();                                // what follows is for whole warps
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -1,187 +1,89 @@
 // gemv.cu -- nvfp4_gemv: y[m][n] = bf16(g * sum_k x[m][k] w[n][k] + bias[n]) for a few rows of
 // bf16 x, w = e2m1(code) * e4m3(scale) in the layout of nvfp4_gemm.  The weight-only form.
 //
-// What bounds it is reading the weight, 9/16 byte for each.  Decoded by the CUDA cores, a weight
-// costs a conversion, a product with its scale and its share of the products with x: at 16 rows
-// that took 2.7 times as long as the reading.  So no CUDA core touches the weight: it goes from
-// global memory to shared memory and into tcgen05.mma kind::mxf4nvf4 as it is stored, as the M = 128
-// operand, and x is made to fit the other operand instead, as a sum of seven E2M1 rows:
-//     x[m][k] = rho_m * sum_i 2^(q_i) e2m1(c_i[m][k]),    q = 0, -2, -5, -8, -11, -14, -17,
-// rho_m the smallest power of two with |x[m][.]| <= 6 rho_m.  A term takes the nearest code of what
-// the terms before it left:
-//     term 1: |r| <= 6 leaves at most 1 (codes are 2 apart above 4) = 4 * 2^-2;
-//     term 2: |r| <= 4 units leaves at most half a unit (codes are at most 1 apart up to 4),
-//             2^-3 = 4 * 2^-5, and so on: 2^-18 after term 7, while the row's largest is above 3.
-// So x is held to 2^-19.5 of the largest of its row (bf16 has 2^-8 of the element).  The scale
-// vector of that operand is 1 throughout (it is laid down in tensor memory once, where loading one for
-// each stage cost the issuing thread 430 cycles of a budget of 790), and the epilogue adds the seven
-// columns of a row with their powers of two, smallest first.
+// What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read
+// (gemv_mma.cuh).  Small weights go another way (gemv_direct.cu).
 //
-// Two kernels.  nvfp4_gemv_split_kernel writes the seven rows of each x row to the workspace, in the
-// order in which shared memory will hold them.  nvfp4_gemv_kernel, one CTA per SM: the 256-element
-// K stages of all 128-row tiles in a row are cut into equal runs, one for each CTA, so that every SM
+// Two kernels.  nvfp4_gemv_rows_kernel writes x in f16, times a power of two for each row, to the
+// workspace, in the order in which shared memory will hold it.  nvfp4_gemv_kernel: the 256-element K
+// steps of all 128-row tiles in a row are cut into equal runs, one for each CTA, so that every SM
 // reads the same number of bytes whatever N and K are; a tile that is cut leaves fp32 parts, and the
-// last CTA to finish one adds them in order.  Its producer fills the ring with weights before the
-// split kernel has ended (that kernel begins only when everything before this call has).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+// last CTA to finish one adds them in order.  x comes to shared memory a few steps at a time,
+// asynchronously and one such chunk ahead; a lane's codes are one step ahead in registers, across
+// the ends of tiles too.
 #include <algorithm>
 #include <atomic>
 
 #include "bsp_internal.h"
 #include "bsp_ptx.cuh"
-#include "nvfp4_block.cuh"
+#include "gemv_mma.cuh"
 
 namespace bsp {
 namespace {
 
 constexpr int kGemvMaxRows = 32;
-constexpr int kTerms = 7;
-constexpr int kTileRows = 128;
-constexpr int kStageK = 256;
-constexpr int kABytes = kTileRows * kStageK / 2;
-constexpr int kSfBytes = 4 * 512;                // scales of 128 rows and one stage
-constexpr int kMaxStages = 8;
-constexpr int kMaxCtas = 160;
-constexpr int kThreads = 224;                    // producer, MMA issuer, four epilogue warps, issuer
-constexpr int kRingBytes = 224 * 1024;
-constexpr uint32_t kTmemCols = 512;
-constexpr int kAccCols = 448;                    // of the accumulators; then the scales
-constexpr int kSfaCol = kAccCols, kSfbCol = kSfaCol + 32;
-constexpr int kPoison = 0x7FFFFFFF;              // exponent of a row that is not finite
-
-__host__ __device__ constexpr int term_exp(int i) { return i == 0 ? 0 : 1 - 3 * i; }
+constexpr int kMaxCtas = 320;
+constexpr int kMinSteps = 4;                    // of a run
+constexpr int kRowPitch = kStepBytes + 32;      // of x in shared memory: see nvfp4_gemv_kernel
+constexpr int kChunkBytes = 36 * 1024;          // of x in shared memory, twice
+constexpr int kMaxChunk = 16;                   // steps
+constexpr int kPoison = 0x7FFFFFFF;             // exponent of a row that is not finite
 
 struct GemvArgs {
-    const uint8_t* sfa;
+    GemvWeight w;
     const float* w_scale;
     const __nv_bfloat16* bias;
     __nv_bfloat16* out;
-    const uint8_t* xc;           // [stages of K][nb rows][128 bytes], swizzled
-    const int32_t* rho;          // [M] exponent of a row's power of two, or kPoison
+    const uint8_t* xh;           // [steps][M][512 bytes] f16
+    const int32_t* exponent;     // [M] biased exponent that a row goes by, or kPoison
     float* parts;                // [2 * ctas][M][128]
-    int32_t* done;               // [tiles][4] parts that have arrived, zeroed by the split kernel
-    int32_t M, N, K;
-    int32_t mp;                  // rows of x rounded up to 8
-    int32_t nb;                  // 7 mp rounded up to 16: rows of the second operand
-    int32_t num_kt;
-    int32_t stages;              // of the ring
-    int64_t total;               // K stages of all tiles
-    uint64_t wait_ns;
-    int* status;
+    int32_t* done;               // [tiles] parts that have arrived, zeroed by the rows kernel
+    int32_t M;
+    int32_t steps;               // of K
+    int32_t chunk;               // steps of x in shared memory at a time, even
+    int64_t total;               // steps of all tiles
 };
 
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(taddr));
-}
-
-// 2^e as a float, e in [-126, 127]
-__device__ __forceinline__ float exp2_int(int e)
-{
-    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
-// ceil(log2(v / 6)) of a positive normal v
-__device__ __forceinline__ int log2_over_6(float v)
-{
-    const uint32_t b = __float_as_uint(v);
-    return static_cast<int>(b >> 23) - 127 - 2 + ((b & 0x7FFFFFu) > 0x400000u);
-}
-
-// Sixteen codes of r / 2^q (element 2j in the low nibble), and r minus what they stand for.
-__device__ __forceinline__ uint2 take_term(float (&r)[16], int q)
-{
-    const float down = exp2_int(-q), up = exp2_int(q);
-    uint2 w;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = r[8 * half + i] * down;
-        const uint32_t c = cvt_e2m1x8(y);
-        (half ? w.y : w.x) = c;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h2;
-            asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-                : "=r"(h2)
-                : "r"(c >> (8 * i) & 0xFFu));
-            const __half2 h = *reinterpret_cast<const __half2*>(&h2);
-            r[8 * half + 2 * i] = fmaf(-up, __low2float(h), r[8 * half + 2 * i]);
-            r[8 * half + 2 * i + 1] = fmaf(-up, __high2float(h), r[8 * half + 2 * i + 1]);
-        }
-    }
-    return w;
-}
-
-// Largest |x| of sixteen bf16 as fp32 bits; an infinity or NaN is the largest of all.
-__device__ __forceinline__ uint32_t max_bits(const uint4 (&v)[2])
-{
-    uint32_t m = 0;
-    const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, max(u[i] << 16 & 0x7FFFFFFFu, u[i] & 0x7FFF0000u));
-    return m;
-}
-
-// One CTA per row of x; a thread takes 16-element blocks.  Also zeroes the counters of the tiles.
+// One CTA per row of x; a thread takes 8-element pieces.  Also zeroes the counters of the tiles.
+// Of the 32 16-byte pieces of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped:
+// with that the eight lanes of one shared memory read (four t, two g) are in different banks.
 __global__ void __launch_bounds__(1024)
-    nvfp4_gemv_split_kernel(const __nv_bfloat16* x, int K, int mp, int nb,
-                            uint8_t* xc, int32_t* rho, int32_t* done, int counters)
+    nvfp4_gemv_rows_kernel(const __nv_bfloat16* x, int K, int steps, uint8_t* xh, int32_t* exponent,
+                           int32_t* done, int tiles)
 {
     __shared__ uint32_t warp_max[32];
     griddep_wait();
     griddep_launch_dependents();
-    const int m = blockIdx.x, blocks = K / 16;
+    const int m = blockIdx.x, M = gridDim.x, pieces = steps * (kStepK / 8);
     const uint4* row = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * K);
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < counters; i += gridDim.x * blockDim.x)
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < tiles; i += gridDim.x * blockDim.x)
         done[i] = 0;
-    uint4 v[2] = {};
-    uint32_t top = 0;
-    for (int b = threadIdx.x; b < blocks; b += blockDim.x) {
-        v[0] = row[2 * b];
-        v[1] = row[2 * b + 1];
-        top = max(top, max_bits(v));
+    uint4 v = make_uint4(0, 0, 0, 0);
+    uint32_t top = 0;            // bits of the largest |x|; an infinity or NaN is the largest of all
+    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+        v = i * 8 < K ? row[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] << 16 & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
     __syncthreads();
     top = threadIdx.x % 32 < blockDim.x / 32 ? warp_max[threadIdx.x & 31] : 0;
     top = __reduce_max_sync(0xFFFFFFFFu, top);
-    const bool finite = top < 0x7F800000u;
-    const int e = finite ? max(log2_over_6(fmaxf(__uint_as_float(top), 0x1p-120f)), -120) : 0;
-    if (threadIdx.x == 0) rho[m] = finite ? e : kPoison;
-    const float n1 = exp2_int(-e / 2), n2 = exp2_int(-e - -e / 2);
-    const bool held = blocks <= static_cast<int>(blockDim.x);      // v still has the block
-    for (int b = threadIdx.x; b < blocks; b += blockDim.x) {
-        if (!held) {
-            v[0] = row[2 * b];
-            v[1] = row[2 * b + 1];
-        }
-        const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-        float r[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            r[2 * i] = bf16lo_to_f32(u[i]) * n1 * n2;
-            r[2 * i + 1] = bf16hi_to_f32(u[i]) * n1 * n2;
-        }
-#pragma unroll
-        for (int i = 0; i < kTerms; ++i) {
-            const int j = i * mp + m;
-            const int64_t at = (static_cast<int64_t>(b >> 4) * nb + j) * 128;
-            *reinterpret_cast<uint2*>(xc + at + (((b >> 1 & 7) ^ (j & 7)) << 4) + (b & 1) * 8) =
-                take_term(r, term_exp(i));
-        }
+    const int e = x_exponent(top);
+    if (threadIdx.x == 0) exponent[m] = top < 0x7F800000u ? e : kPoison;
+    const float up = pow2_biased(268 - e);       // 2^(14 - (e - 127))
+    const bool held = pieces <= static_cast<int>(blockDim.x);      // v still has the piece
+    for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+        if (!held) v = i * 8 < K ? row[i] : make_uint4(0, 0, 0, 0);
+        const int step = i >> 5, c = i & 31;
+        *reinterpret_cast<uint4*>(xh + (static_cast<int64_t>(step) * M + m) * kStepBytes +
+                                  (c ^ ((c >> 3) & 1)) * 16) = pack_x8(v, up);
     }
 }
 
-// First K stage of CTA i's run, and the CTA whose run holds stage s.
+// First step of CTA i's run, and the CTA whose run holds step s.
 __device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int i)
 {
     return total * i / ctas;
@@ -192,314 +94,189 @@ __device__ __forceinline__ int run_owner(int64_t total, int ctas, int64_t s)
     return static_cast<int>(((s + 1) * ctas - 1) / total);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap tm_w, const GemvArgs args)
+// NT: 8-row tiles of x.
+template <int NT>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) nvfp4_gemv_kernel(const GemvArgs p)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* ring = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], ones_ready, fin[2];
-    __shared__ float2 factor[kGemvMaxRows];                      // 2^e g of a row, in two parts
-    __shared__ uint32_t tmem_holder;
-    __shared__ int abort_word;
-    __shared__ __align__(128) uint32_t ones[128];                // E4M3 1.0
-    volatile int* abort_flag = &abort_word;
+    extern __shared__ uint4 xs[];               // two chunks of x: [step][M][kRowPitch]
+    __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
+    __shared__ float2 factor[NT * 8];           // 2^e g of a row, in two parts
+    __shared__ int last;
+    griddep_wait();
+    griddep_launch_dependents();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int stages = args.stages, num_kt = args.num_kt, nb = args.nb;
-    const int b_bytes = nb * 128, stage_bytes = kABytes + b_bytes + kSfBytes;
-    const int ctas = gridDim.x;
-    const int64_t s0 = run_begin(args.total, ctas, blockIdx.x);
-    const int64_t s1 = run_begin(args.total, ctas, blockIdx.x + 1);
-    const int mine = static_cast<int>(s1 - s0);
-    // two issuers' accumulators, twice when they fit
-    const int bufs = 4 * nb <= kAccCols ? 2 : 1, acc_cols = kAccCols / (2 * bufs);
+    const int g = lane >> 2, t = lane & 3;
+    const int oct = warp & 3, kw = warp >> 2;
+    const int ctas = gridDim.x, steps = p.steps, M = p.M;
+    const int64_t s0 = run_begin(p.total, ctas, blockIdx.x);
+    const int run = static_cast<int>(run_begin(p.total, ctas, blockIdx.x + 1) - s0);
+    const int tile0 = static_cast<int>(s0 / steps), k0 = static_cast<int>(s0 - static_cast<int64_t>(tile0) * steps);
 
-    // a walk over the run's stages: K stage, tile, slot of the ring, and the slot's phase
-    struct Walk {
-        int tile, kt, slot;
-        uint32_t phase;
-    };
-    const int kb_all = args.K / 64;
-    const int tile0 = static_cast<int>(s0 / num_kt);
-    const Walk begin = {tile0, static_cast<int>(s0 - static_cast<int64_t>(tile0) * num_kt),
-                        0, 0};
-    const auto next = [&](Walk& w) {
-        if (++w.kt == num_kt) {
-            w.kt = 0;
-            ++w.tile;
-        }
-        if (++w.slot == stages) {
-            w.slot = 0;
-            w.phase ^= 1;
-        }
-    };
-    const auto weight = [&](const Walk& w) {
-        const int nkb = min(4, kb_all - 4 * w.kt);
-        uint8_t* dst = ring + w.slot * stage_bytes;
-        uint64_t* bar = full + w.slot;
-        mbar_arrive_expect_tx(bar, kABytes + b_bytes + nkb * 512);
-        tma_load_2d(dst, &tm_w, bar, w.kt * (kStageK / 2), w.tile * kTileRows);
-        bulk_load(dst + kABytes + b_bytes,
-                  args.sfa + (static_cast<int64_t>(w.tile) * kb_all + 4 * w.kt) * 512,
-                  nkb * 512, bar);
-    };
-    const auto rows = [&](const Walk& w) {
-        uint8_t* dst = ring + w.slot * stage_bytes;
-        bulk_load(dst + kABytes, args.xc + static_cast<int64_t>(w.kt) * b_bytes, b_bytes,
-                  full + w.slot);
-    };
-    const int early = min(mine, stages);
-    if (warp == 0 && lane == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, 1);
-        }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(tfull + a, 2);
-            mbar_init(tempty + a, 4);
-        }
-        mbar_init(&ones_ready, 1);
-        mbar_init(fin, 1);
-        mbar_init(fin + 1, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-        // The first weights are on their way before the split kernel has ended, and before this CTA is
-        // set up: nothing that this grid depends on writes them.
-        Walk w = begin;
-        for (int i = 0; i < early; ++i, next(w)) weight(w);
+    // the step of the run whose codes the warp holds: every other one is its own
+    HalfStep w[2];
+    int at_tile = tile0, at_k = k0 + kw;
+    while (at_k >= steps) {
+        at_k -= steps;
+        ++at_tile;
     }
-    if (warp == 1) {
-        tmem_alloc(&tmem_holder, kTmemCols);
-        tmem_relinquish();
+    LaneRows rows = lane_rows(p.w, at_tile, oct * 8 + g);
+    if (kw < run) {
+        load_half(p.w, rows, at_k, t, 0, w[0]);
+        load_half(p.w, rows, at_k, t, 1, w[1]);
     }
-    if (threadIdx.x < 128) ones[threadIdx.x] = 0x38383838u;
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    griddep_launch_dependents();             // not before this CTA has its tensor memory
-    const uint32_t tbase = tmem_holder;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            griddep_wait();                      // x is split
-            Walk w = begin;
-            for (int i = 0; i < early; ++i, next(w)) rows(w);
-            int i = early;
-            for (; i < mine; ++i, next(w)) {
-                if (!mbar_wait(empty + w.slot, w.phase ^ 1u, abort_flag, args.wait_ns, args.status,
-                               101))
-                    break;
-                weight(w);
-                rows(w);
+    // chunk c of the run's steps to its buffer
+    const int step_bytes = M * kRowPitch, buffer = p.chunk * step_bytes;
+    const auto bring = [&](int c) {
+        const int r0 = c * p.chunk, n = min(p.chunk, run - r0) * M * 32;
+        int k = static_cast<int>((k0 + static_cast<int64_t>(r0)) % steps);
+        const uint32_t to = smem_u32(xs) + (c & 1) * buffer;
+        int left = threadIdx.x;                  // piece of step k's
+        int s = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            while (left >= M * 32) {
+                left -= M * 32;
+                ++s;
+                if (++k == steps) k = 0;
             }
-            // the last loads must land before shared memory is freed
-            for (int j = max(0, i - stages); j < i; ++j)
-                drain_wait(full + j % stages, j / stages & 1, args.wait_ns, args.status);
+            cp_async16(to + s * step_bytes + (left >> 5) * kRowPitch + (left & 31) * 16,
+                       p.xh + static_cast<int64_t>(k) * M * kStepBytes + left * 16, true);
+            left += kThreads;
         }
-    } else if (warp == 1 || warp == 6) {
-        // ------------------------------------------------------------ MMA issuers
-        if (lane == 0) {
-            const int own = warp == 6;               // stages i with i % 2 == own
-            const uint32_t idesc = idesc_nvf4(kTileRows, nb);
-            const uint32_t sfa = tbase + kSfaCol + 16 * own, sfb = tbase + kSfbCol;
-            if (own == 0)
-                for (int c = 0; c < 2; ++c)          // scales of up to 256 rows of the second operand
-                    tmem_cp_32x128b_x4(sfb + 4 * c, sdesc_sf_block(smem_u32(ones)));
-            if (own == 0) {
-                tc_commit(&ones_ready);
-            } else if (!mbar_wait(&ones_ready, 0, abort_flag, args.wait_ns, args.status, 105)) {
-                *abort_flag = 1;
+    };
+    bring(0);
+    if (threadIdx.x < NT * 8) {
+        const int e = threadIdx.x < M ? p.exponent[threadIdx.x] : 127;
+        const float gs = *p.w_scale;
+        // x was multiplied by 2^(141 - e) and the weight by 2^-kDownBits
+        factor[threadIdx.x] = e == kPoison ? make_float2(NAN, NAN)
+                                           : make_float2(gs, pow2_biased(e - 14 + kDownBits));
+    }
+
+    // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
+    // Rows of a tile past M read the last row; their columns are not stored.
+    const uint8_t* xg[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, M - 1) * kRowPitch + t * 64;
+
+    int mine = kw;                               // step of the run
+    int r0 = 0;
+    for (int tile = tile0; r0 < run; ++tile) {
+        const int first = tile == tile0 ? k0 : 0;             // step of the tile that comes at r0
+        const int r_end = min(run, r0 + steps - first);
+        const bool begins = first == 0, whole = begins && r_end - r0 == steps;
+        float acc[2][NT][4] = {};
+        for (int r = r0; r < r_end;) {
+            const int c = r / p.chunk, in_chunk = r - c * p.chunk;
+            if (in_chunk == 0) {
+                // the chunk has come, and nobody reads the other buffer any more
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncthreads();
+                if ((c + 1) * p.chunk < run) bring(c + 1);
             }
-            tc_fence_after();
-            int seg = -1, kt = static_cast<int>(s0 % num_kt), s = 0;
-            uint32_t phase = 0;
-            bool fresh = true;                       // nothing of this segment is issued yet
-            for (int i = 0; i < mine; ++i) {
-                if (i == 0 || kt == 0) {
-                    if (seg >= 0) tc_commit(tfull + seg % bufs);
-                    ++seg;
-                    fresh = true;
-                    if (!mbar_wait(tempty + seg % bufs, (seg / bufs & 1) ^ 1u, abort_flag,
-                                   args.wait_ns, args.status, 102)) {
-                        seg = -1;
-                        break;
-                    }
+            const int r1 = min(r_end, (c + 1) * p.chunk);
+            const int base = (c & 1) * buffer - c * p.chunk * step_bytes;
+            for (; mine < r1; mine += 2) {
+                const int xo = base + mine * step_bytes;
+                const bool more = mine + 2 < run;
+                at_k += 2;
+                if (at_k >= steps) {             // the next one of the warp's is another tile's
+                    do {
+                        at_k -= steps;
+                        ++at_tile;
+                    } while (at_k >= steps);
+                    if (more) rows = lane_rows(p.w, at_tile, oct * 8 + g);
                 }
-                if ((i & 1) == own) {
-                    if (!mbar_wait(full + s, phase, abort_flag, args.wait_ns, args.status, 103)) {
-                        seg = -1;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = smem_u32(ring + s * stage_bytes);
-                    const uint64_t sf = sdesc_sf_block(a + kABytes + b_bytes);
-                    const uint64_t ad = sdesc_kmajor_sw128(a);
-                    const uint64_t bd = sdesc_kmajor_sw128(a + kABytes);
-                    const uint32_t d = tbase + (2 * (seg % bufs) + own) * acc_cols;
-                    const int nk = args.K / 64 - 4 * kt;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nk) tmem_cp_32x128b_x4(sfa + 4 * k, sf + 32 * k);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nk)
-                            mma_nvf4(d, ad + 2 * k, bd + 2 * k, idesc, sfa + 4 * k, sfb,
-                                     fresh && k == 0 ? 0u : 1u);
-                    tc_commit(empty + s);
-                    fresh = false;
-                }
-                if (++kt == num_kt) kt = 0;
-                if (++s == stages) {
-                    s = 0;
-                    phase ^= 1;
+                for (int half = 0; half < 2; ++half) {
+                    mma_half<NT>(acc, w[half], xg, xo + half * 256, t);
+                    if (more) load_half(p.w, rows, at_k, t, half, w[half]);
                 }
             }
-            if (seg >= 0) tc_commit(tfull + seg % bufs);
+            r = r1;
         }
-    } else {
-        // ------------------------------------------------------------ epilogue
-        const int q = warp & 3, row = q * 32 + lane;
-        griddep_wait();                          // the exponents and the counters are written
-        const float g = *args.w_scale;
-        if (lane < args.M) {                     // each warp writes them all: the same values
-            const int e = __ldcg(args.rho + lane);
-            factor[lane] = e == kPoison ? make_float2(NAN, NAN)
-                                        : make_float2(exp2_int(e / 2) * g, exp2_int(e - e / 2));
-        }
-        __syncwarp();
-        int seg = 0;
-        for (int64_t at = s0; at < s1; ++seg) {
-            const int tile = static_cast<int>(at / num_kt);
-            const int64_t t0 = static_cast<int64_t>(tile) * num_kt, t1 = t0 + num_kt;
-            const bool begins = at == t0, whole = begins && t1 <= s1;
-            const int n = tile * kTileRows + row;
-            const bool in = n < args.N;
-            const float bias = in && args.bias ? __bfloat162float(args.bias[n]) : 0.0f;
-            const int64_t end = min(t1, s1);
-            const bool one = end - at == 1;      // then one of the issuers had nothing to do
-            const int first_own = static_cast<int>(at - s0) & 1;
-            const bool ok = mbar_wait(tfull + seg % bufs, seg / bufs & 1, abort_flag, args.wait_ns,
-                                      args.status, 104);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            tc_fence_after();
-            const uint32_t acc = tbase + (static_cast<uint32_t>(q * 32) << 16) +
-                                 2 * (seg % bufs) * acc_cols;
-            const auto finish = [&](int m, float v) {
-                if (!in || m >= args.M) return;
-                const float2 f = factor[m];
-                args.out[static_cast<int64_t>(m) * args.N + n] =
-                    __float2bfloat16_rn(v * f.x * f.y + bias);
-            };
-            float* part = args.parts +
-                          static_cast<int64_t>(2 * blockIdx.x + begins) * args.M * kTileRows + row;
-            for (int c = 0; c < args.mp; c += 8) {
-                float v[8] = {};
+        r0 = r_end;
+
+        // sums of the two halves of the warps
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (k == 1 && one) break;
-                    const uint32_t from = acc + (first_own ^ k) * acc_cols + c;
-                    uint32_t r[kTerms][8];
+        for (int half = 1; half >= 0; --half) {
+            if (kw == half) {
 #pragma unroll
-                    for (int i = 0; i < kTerms; ++i) tmem_ld_x8(from + i * args.mp, r[i]);
-                    tmem_ld_wait();
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float y = 0.0f;          // the smallest terms first
+                    for (int ta = 0; ta < 2; ++ta)
 #pragma unroll
-                        for (int i = kTerms - 1; i >= 0; --i)
-                            y = fmaf(__uint_as_float(r[i][j]), 1.0f / (1 << -term_exp(i)), y);
-                        v[j] += y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (whole)
-                        finish(c + j, v[j]);
-                    else if (c + j < args.M)
-                        part[(c + j) * kTileRows] = v[j];
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty + seg % bufs);
-            if (!whole) {
-                // each of the four epilogue warps adds its own 32 rows when it is the last of the
-                // CTAs' warps to bring them
-                const int o0 = run_owner(args.total, ctas, t0), o1 = run_owner(args.total, ctas, t1 - 1);
-                __threadfence();
-                __syncwarp();
-                int before = 0;
-                if (lane == 0) before = atomicAdd(args.done + 4 * tile + q, 1);
-                before = __shfl_sync(0xFFFFFFFFu, before, 0);
-                if (before == o1 - o0) {
-                    __threadfence();
-                    const int64_t step = static_cast<int64_t>(2) * args.M * kTileRows;
-                    const float* first = args.parts + o0 * step + step / 2 + row;
-                    const float* rest = args.parts + o0 * step + row;
-                    for (int m = 0; m < args.M; m += 8) {
-                        float v[8];
-                        const int rows = min(8, args.M - m);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            v[j] = j < rows ? __ldcg(first + (m + j) * kTileRows) : 0.0f;
-                        for (int i0 = 1; i0 <= o1 - o0; i0 += 4) {
-                            float y[4][8];       // four parts' loads in flight
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    y[i][j] = i0 + i <= o1 - o0 && j < rows
-                                                  ? __ldcg(rest + (i0 + i) * step +
-                                                           (m + j) * kTileRows)
-                                                  : 0.0f;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) v[j] += y[i][j];
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = oct * 8 + g + 64 * ta + 32 * (i >> 1);
+                            const int col = nt * 8 + 2 * t + (i & 1);
+                            part[col][r] = half ? acc[ta][nt][i] : part[col][r] + acc[ta][nt][i];
                         }
+            }
+            __syncthreads();
+        }
+        const int r = threadIdx.x & (kTileRows - 1), m0 = threadIdx.x / kTileRows;
+        constexpr int kSide = kThreads / kTileRows;
+        const int n = tile * kTileRows + r;
+        const bool in = n < p.w.N;
+        const float bias = in && p.bias ? __bfloat162float(p.bias[n]) : 0.0f;
+        const auto finish = [&](int m, float v) {
+            const float2 f = factor[m];
+            if (in) p.out[static_cast<int64_t>(m) * p.w.N + n] = __float2bfloat16_rn(v * f.x * f.y + bias);
+        };
+        if (whole) {
+            for (int m = m0; m < M; m += kSide) finish(m, part[m][r]);
+        } else {
+            const int64_t step = static_cast<int64_t>(2) * M * kTileRows;
+            float* own = p.parts + blockIdx.x * step + (begins ? step / 2 : 0) + r;
+            for (int m = m0; m < M; m += kSide) own[m * kTileRows] = part[m][r];
+            const int64_t t0 = static_cast<int64_t>(tile) * steps;
+            const int o0 = run_owner(p.total, ctas, t0), o1 = run_owner(p.total, ctas, t0 + steps - 1);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) last = atomicAdd(p.done + tile, 1) == o1 - o0;
+            __syncthreads();
+            if (last) {
+                __threadfence();
+                // part 0 is the second slot of CTA o0, the others the first of theirs
+                const float* other = p.parts + o0 * step + r;
+                for (int m = m0; m < M; m += kSide) {
+                    const float* of = other + m * kTileRows;
+                    float v = __ldcg(of + step / 2);
+                    for (int i0 = 1; i0 <= o1 - o0; i0 += 4) {
+                        float y[4];              // four parts' loads in flight
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) finish(m + j, v[j]);
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = i0 + i <= o1 - o0 ? __ldcg(of + (i0 + i) * step) : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v += y[i];
                     }
+                    finish(m, v);
                 }
             }
-            at = end;
         }
+        __syncthreads();                         // `part` and `last` are read
     }
-
-    // ---------------------------------------------------------------- teardown
-    __syncwarp();
-    if ((warp == 1 || warp == 6) && lane == 0) {
-        tc_commit(fin + (warp == 6));
-        drain_wait(fin + (warp == 6), 0, args.wait_ns, args.status);
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc(tbase, kTmemCols);
 }
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: codes of the split x, parts, exponents, counters.
+// Workspace: x in f16, parts, exponents, counters.
 struct GemvLayout {
-    int64_t parts, rho, done, bytes;
-    int32_t mp, nb, num_kt, tiles;
+    int64_t parts, exponent, done, bytes;
+    int32_t steps, tiles;
 };
 
 GemvLayout gemv_layout(int64_t M, int64_t N, int64_t K)
 {
     GemvLayout l;
-    l.mp = static_cast<int32_t>((M + 7) / 8 * 8);
-    l.nb = (kTerms * l.mp + 15) / 16 * 16;
-    l.num_kt = static_cast<int32_t>((K + kStageK - 1) / kStageK);
+    l.steps = static_cast<int32_t>((K + kStepK - 1) / kStepK);
     l.tiles = static_cast<int32_t>((N + kTileRows - 1) / kTileRows);
-    l.parts = up256(static_cast<int64_t>(l.num_kt) * l.nb * 128);
-    l.rho = l.parts + static_cast<int64_t>(2) * kMaxCtas * M * kTileRows * 4;
-    l.done = up256(l.rho + M * 4);
-    l.bytes = up256(l.done + static_cast<int64_t>(l.tiles) * 16);
+    l.parts = up256(static_cast<int64_t>(l.steps) * M * kStepBytes);
+    l.exponent = l.parts + static_cast<int64_t>(2) * kMaxCtas * M * kTileRows * 4;
+    l.done = up256(l.exponent + M * 4);
+    l.bytes = up256(l.done + static_cast<int64_t>(l.tiles) * 4);
     return l;
 }
 
@@ -511,6 +288,33 @@ int gemv_check(int64_t M, int64_t N, int64_t K)
         return BSP_ERR_UNSUPPORTED_SHAPE;
     return BSP_OK;
 }
+
+template <int NT>
+int launch_gemv(GemvArgs a, int dev, int sms, cudaStream_t s)
+{
+    static std::atomic<bool> ready[kMaxDevices];
+    constexpr int kSmem = 2 * kChunkBytes;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(nvfp4_gemv_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return BSP_ERR_CUDA;
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
+    a.chunk = std::clamp(kChunkBytes / (a.M * kRowPitch) / 2 * 2, 2, kMaxChunk);
+    const int64_t slots = std::min(kMaxCtas, (NT <= 2 ? 2 : 1) * sms);
+    const int64_t ctas = std::min<int64_t>(slots, (a.total + kMinSteps - 1) / kMinSteps);
+    const size_t smem = static_cast<size_t>(2) * a.chunk * a.M * kRowPitch;
+    if (launch_kernel(nvfp4_gemv_kernel<NT>, static_cast<unsigned>(ctas), kThreads, smem, s, true,
+                      a) != cudaSuccess) {
+        cudaGetLastError();
+        return BSP_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+static_assert(2 * kGemvMaxRows * kRowPitch <= kChunkBytes, "two steps of 32 rows fit a chunk");
 
 }  // namespace
 }  // namespace bsp
@@ -541,71 +345,39 @@ int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
     int dev = 0, sms = 0;
     st = check_device(&dev, &sms);
     if (st != BSP_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (gemv_is_small(M, N, K, sms))
         return gemv_direct(static_cast<const __nv_bfloat16*>(x_bf16), w_codes, w_sf, w_scale,
                            static_cast<const __nv_bfloat16*>(bias_bf16),
-                           static_cast<__nv_bfloat16*>(out_bf16), M, N, K, dev, sms,
-                           reinterpret_cast<cudaStream_t>(stream));
-    static std::atomic<bool> ready[kMaxDevices];
-    constexpr int kSmem = kRingBytes + 1024;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(nvfp4_gemv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmem) != cudaSuccess) {
-            cudaGetLastError();
-            return BSP_ERR_CUDA;
-        }
-        ready[dev].store(true, std::memory_order_release);
-    }
-    CUtensorMap tm;
-    st = make_code_map(&tm, w_codes, static_cast<uint64_t>(K) / 2, static_cast<uint64_t>(N),
-                       kTileRows);
-    if (st != BSP_OK) return st;
+                           static_cast<__nv_bfloat16*>(out_bf16), M, N, K, dev, sms, s);
     auto* ws = static_cast<uint8_t*>(workspace);
     GemvArgs a = {};
-    a.sfa = w_sf;
+    a.w.codes = w_codes;
+    a.w.sf = w_sf;
+    a.w.N = static_cast<int32_t>(N);
+    a.w.K = static_cast<int32_t>(K);
     a.w_scale = w_scale;
     a.bias = static_cast<const __nv_bfloat16*>(bias_bf16);
     a.out = static_cast<__nv_bfloat16*>(out_bf16);
-    a.xc = ws;
-    a.rho = reinterpret_cast<int32_t*>(ws + l.rho);
+    a.xh = ws;
+    a.exponent = reinterpret_cast<int32_t*>(ws + l.exponent);
     a.parts = reinterpret_cast<float*>(ws + l.parts);
     a.done = reinterpret_cast<int32_t*>(ws + l.done);
     a.M = static_cast<int32_t>(M);
-    a.N = static_cast<int32_t>(N);
-    a.K = static_cast<int32_t>(K);
-    a.mp = l.mp;
-    a.nb = l.nb;
-    a.num_kt = l.num_kt;
-    const int stage_bytes = kABytes + l.nb * 128 + kSfBytes;
-    a.stages = std::min(kMaxStages, kRingBytes / stage_bytes);
-    a.total = static_cast<int64_t>(l.tiles) * l.num_kt;
-    a.wait_ns = wait_limit_ns();
-    a.status = device_status_ptr(dev);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned threads = static_cast<unsigned>(std::min<int64_t>(1024, (K / 16 + 31) / 32 * 32));
-    // CTAs.  At least sqrt(num_kt M / 20) stages to each: fewer leave more parts of a tile to its
-    // last CTA than they save in stages (about 0.4 us each, against 0.6 us for 32 rows of parts).
-    // Where the tiles are fewer than that many CTAs, a multiple of the tiles gives every CTA one whole
-    // tile or one even part of one; it is taken unless its runs are over 7 stages (3 us, what a
-    // second part in a run costs) longer than equal runs over all SMs.
-    int per = 1;
-    while (per * per * 20 < l.num_kt * M) ++per;
-    int64_t ctas = std::min<int64_t>(std::min(sms, kMaxCtas), (a.total + per - 1) / per);
-    if (l.tiles <= ctas) {
-        const int64_t even = ctas / l.tiles;
-        if ((l.num_kt + even - 1) / even <= (a.total + ctas - 1) / ctas + 7) ctas = even * l.tiles;
-    }
-    if (launch_kernel(nvfp4_gemv_split_kernel, static_cast<unsigned>(M), threads, 0, s, true,
-                      static_cast<const __nv_bfloat16*>(x_bf16), a.K, a.mp, a.nb, ws,
-                      reinterpret_cast<int32_t*>(ws + l.rho),
-                      reinterpret_cast<int32_t*>(ws + l.done), 4 * l.tiles) != cudaSuccess ||
-        launch_kernel(nvfp4_gemv_kernel, static_cast<unsigned>(ctas), kThreads,
-                      static_cast<size_t>(a.stages) * stage_bytes + 1024, s, true, tm,
-                      a) != cudaSuccess) {
+    a.steps = l.steps;
+    a.total = static_cast<int64_t>(l.tiles) * l.steps;
+    const int threads = std::min(1024, l.steps * (kStepK / 8));
+    if (launch_kernel(nvfp4_gemv_rows_kernel, static_cast<unsigned>(M), static_cast<unsigned>(threads), 0,
+                      s, true, static_cast<const __nv_bfloat16*>(x_bf16), a.w.K, a.steps, ws,
+                      reinterpret_cast<int32_t*>(ws + l.exponent),
+                      reinterpret_cast<int32_t*>(ws + l.done), l.tiles) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
-    return launch_status();
+    if (M <= 8) return launch_gemv<1>(a, dev, sms, s);
+    if (M <= 16) return launch_gemv<2>(a, dev, sms, s);
+    if (M <= 24) return launch_gemv<3>(a, dev, sms, s);
+    return launch_gemv<4>(a, dev, sms, s);
 }
 
 }  // extern "C"

@@ -17,24 +17,18 @@
 // and one 16-byte word of scales, all of which it uses.  The products may run over k in any order, so
 // these 64 consecutive codes of a row are the k slots that the lane owns in 16 products.  All of a
 // warp's first step is asked for before x is staged, and each half of the next as soon as one is used.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <atomic>
 
 #include "bsp_internal.h"
 #include "bsp_ptx.cuh"
+#include "gemv_mma.cuh"
 #include "nvfp4_block.cuh"
 
 namespace bsp {
 namespace {
 
 constexpr int kMaxRows = 16;                    // of x: two tiles of 8
-constexpr int kThreads = 256;
-constexpr int kTileRows = 128;
-constexpr int kStepK = 256;
-constexpr int kStepBytes = kStepK * 2;          // of one row of x in f16
 constexpr int kMaxPieces = 8;
 constexpr int kMaxCostWhole = 1500;             // of a CTA: see gemv_is_small
 constexpr int kMaxCostCut = 2200;
@@ -42,138 +36,16 @@ constexpr int kMaxSteps = kMaxCostCut / 232;    // that such a CTA can have
 constexpr int kMaxStage = 76 * 1024;            // shared memory for x
 static_assert(kMaxRows * (kMaxSteps * kStepBytes + 32) <= kMaxStage, "x of a piece fits");
 
-struct GemvParams {
+struct DirectParams {
+    GemvWeight w;
     const __nv_bfloat16* x;
-    const uint8_t* codes;
-    const uint8_t* sf;
     const float* scale;
     const __nv_bfloat16* bias;
     __nv_bfloat16* out;
-    int32_t M, N, K;
+    int32_t M;
     int32_t steps;            // of K in all
     int32_t row_bytes;        // between the rows of x in shared memory
 };
-
-__device__ __forceinline__ float pow2_biased(int e)     // 2^(e - 127), e in [0, 254]
-{
-    return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
-}
-
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
-{
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-
-// the E4M3 scale in byte i of w, twice in an f16 pair
-__device__ __forceinline__ uint32_t scale_to_f16(uint32_t w, int i)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
-        : "=r"(r)
-        : "r"(__byte_perm(w, 0, i * 0x11)));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t word_of(uint4 v, int i)
-{
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// A lane's loads of half a step (128 elements of K): 32 codes of each of its four rows, at t * 32
-// of the half, so that four lanes read 64 bytes of a row side by side; and the 16 scales of those
-// rows and the 64 elements that hold the lane's two blocks.  Rows past N and elements past K are
-// read from the last ones instead: the results of such rows are not stored, and x is zero there.
-struct HalfStep {
-    uint4 c[4];
-    uint4 s;                  // word q: row + 32 q
-};
-
-struct LaneRows {
-    const uint8_t* codes;     // of the lane's first row
-    const uint8_t* sf;
-    uint32_t off[3];          // from there to the other rows' codes
-};
-
-// Not the read-only path: the weight may be an earlier kernel's output, and this kernel may have begun
-// before that one ended.
-__device__ __forceinline__ uint4 ld_once(const void* a)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(a));
-    return v;
-}
-
-__device__ __forceinline__ LaneRows lane_rows(const GemvParams& p, int tile, int row_in_tile)
-{
-    LaneRows r;
-    const int row = min(tile * kTileRows + row_in_tile, p.N - 1);
-    r.codes = p.codes + static_cast<int64_t>(row) * (p.K / 2);
-#pragma unroll
-    for (int q = 1; q < 4; ++q)
-        r.off[q - 1] = static_cast<uint32_t>(min(row + 32 * q, p.N - 1) - row) * (p.K / 2);
-    r.sf = p.sf + static_cast<int64_t>(tile) * (p.K / 64) * 512 + row_in_tile * 16;
-    return r;
-}
-
-__device__ __forceinline__ void load_half(const GemvParams& p, const LaneRows& r, int s, int t,
-                                          int half, HalfStep& d)
-{
-    const uint32_t kt = min(s * 4 + 2 * half + (t >> 1), p.K / 64 - 1);
-    const uint8_t* a = r.codes + (kt * 32 + (t & 1) * 16);
-    d.c[0] = ld_once(a);
-    d.c[1] = ld_once(a + r.off[0]);
-    d.c[2] = ld_once(a + r.off[1]);
-    d.c[3] = ld_once(a + r.off[2]);
-    d.s = ld_once(r.sf + kt * 512);
-}
-
-// Biased exponent that a row of x goes by: the row is multiplied by 2^(14 - (e - 127)).
-__device__ __forceinline__ int x_exponent(uint32_t amax_bits)
-{
-    return max(15, static_cast<int>(amax_bits >> 23));
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
 
 // Steps [a0, a1) of x, a1 > a0, to shared memory in f16; beyond K it is zeros.  Of the
 // 32 16-byte chunks of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped: with
@@ -181,7 +53,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
 // bits of the largest |x| of each row, 0 before.  A warp takes one step of one row at a time and
 // copies all of its own first, so that their latencies overlap; a lane touches no other's.
 // Every thread calls; the stage is readable on return.
-__device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uint4* xs,
+__device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, uint4* xs,
                                         uint32_t* amax)
 {
     constexpr int kWarps = kThreads / 32;
@@ -193,9 +65,9 @@ __device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uin
     const int dm = kWarps / steps, ds = kWarps - dm * steps;
     for (int m = m0, s = s0; m < p.M;) {
         const int k = (a0 + s) * kStepK + lane * 8;
-        const bool in = k < p.K;
+        const bool in = k < p.w.K;
         cp_async16(smem_u32(base + m * p.row_bytes + s * kStepBytes),
-                   p.x + (in ? static_cast<int64_t>(m) * p.K + k : 0), in);
+                   p.x + (in ? static_cast<int64_t>(m) * p.w.K + k : 0), in);
         m += dm;
         s += ds;
         if (s >= steps) {
@@ -222,12 +94,7 @@ __device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uin
         uint4* at = reinterpret_cast<uint4*>(base + m * p.row_bytes + s * kStepBytes);
         const float up = pow2_biased(268 - x_exponent(amax[m]));     // 2^(14 - (e - 127))
         const uint4 v = *at;
-        uint4 h;
-        h.x = pack_f16(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up);
-        h.y = pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up);
-        h.z = pack_f16(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up);
-        h.w = pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up);
-        *at = h;
+        *at = pack_x8(v, up);
         m += dm;
         s += ds;
         if (s >= steps) {
@@ -240,7 +107,7 @@ __device__ __forceinline__ void stage_x(const GemvParams& p, int a0, int a1, uin
 
 // NT: 8-row tiles of x.  Grid: the row tiles' clusters.
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const GemvParams p)
+__global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const DirectParams p)
 {
     extern __shared__ uint4 xs[];               // x in f16
     __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
@@ -260,10 +127,10 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Ge
     // in registers: the two halves of the step at hand, each replaced by the next step's as soon
     // as it is used
     HalfStep w[2];
-    const LaneRows rows = lane_rows(p, tile, oct * 8 + g);
+    const LaneRows rows = lane_rows(p.w, tile, oct * 8 + g);
     if (c0 + kw < c1) {
-        load_half(p, rows, c0 + kw, t, 0, w[0]);
-        load_half(p, rows, c0 + kw, t, 1, w[1]);
+        load_half(p.w, rows, c0 + kw, t, 0, w[0]);
+        load_half(p.w, rows, c0 + kw, t, 1, w[1]);
     }
     if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
     __syncthreads();
@@ -276,38 +143,13 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Ge
     for (int nt = 0; nt < NT; ++nt)
         xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, p.M - 1) * p.row_bytes +
                  t * 64;
-    const int swap = (t >> 1) * 16;
     float acc[2][NT][4] = {};
     for (int s = c0 + kw; s < c1; s += 2) {
         const int xo = (s - c0) * kStepBytes;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4 b[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    b[nt] = *reinterpret_cast<const uint4*>(
-                        xg[nt] + xo + half * 256 + ((j * 16) ^ swap));
-                uint32_t h[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    // scale byte 2 (t % 2) + j / 2 of the row's word
-                    const uint32_t sc =
-                        scale_to_f16(word_of(w[half].s, q), (t & 1) * 2 + (j >> 1));
-                    e2m1x8_to_f16(word_of(w[half].c[q], j), h[q]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[0][nt], h[0][0], h[1][0], h[0][1], h[1][1], b[nt].x, b[nt].y);
-                    mma_f16(acc[1][nt], h[2][0], h[3][0], h[2][1], h[3][1], b[nt].x, b[nt].y);
-                    mma_f16(acc[0][nt], h[0][2], h[1][2], h[0][3], h[1][3], b[nt].z, b[nt].w);
-                    mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
-                }
-            }
-            if (s + 2 < c1) load_half(p, rows, s + 2, t, half, w[half]);
+            mma_half<NT>(acc, w[half], xg, xo + half * 256, t);
+            if (s + 2 < c1) load_half(p.w, rows, s + 2, t, half, w[half]);
         }
     }
 
@@ -327,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Ge
                         // a row of x that is not finite gives NaN, whichever piece finds that
                         const float v = amax[col] < 0x7F800000u
                                             ? acc[ta][nt][i] * gs *
-                                                  pow2_biased(x_exponent(amax[col]) - 14)
+                                                  pow2_biased(x_exponent(amax[col]) - 14 + kDownBits)
                                             : NAN;
                         part[col][r] = half ? v : part[col][r] + v;
                     }
@@ -338,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Ge
     // a thread keeps its row n: 128 / pieces rows, and every (kThreads / that)-th row of x
     const int share = kTileRows / pieces;
     const int r = rank * share + (threadIdx.x & (share - 1)), n = tile * kTileRows + r;
-    const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f;
+    const float bias = p.bias && n < p.w.N ? __bfloat162float(p.bias[n]) : 0.0f;
     for (int m = threadIdx.x / share; m < p.M; m += kThreads / share) {
-        if (n >= p.N) break;
+        if (n >= p.w.N) break;
         float v;
         if (pieces == 1) {
             v = part[m][r];
@@ -357,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Ge
             }
             v = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
         }
-        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(v + bias);
+        p.out[static_cast<int64_t>(m) * p.w.N + n] = __float2bfloat16_rn(v + bias);
     }
     if (pieces > 1) cluster_sync();             // the others have read this CTA's sums before it ends
 }
@@ -372,7 +214,7 @@ int pieces_of(int64_t tiles, int64_t steps, int sms)
 }
 
 template <int NT>
-int launch_direct(const GemvParams& p, int tiles, int pieces, int dev, cudaStream_t stream)
+int launch_direct(const DirectParams& p, int tiles, int pieces, int dev, cudaStream_t stream)
 {
     static std::atomic<bool> ready[kMaxDevices];
     if (!ready[dev].load(std::memory_order_acquire)) {
@@ -434,16 +276,16 @@ int gemv_direct(const __nv_bfloat16* x, const uint8_t* w_codes, const uint8_t* w
 {
     const int64_t tiles = (N + kTileRows - 1) / kTileRows, steps = (K + kStepK - 1) / kStepK;
     const int c = pieces_of(tiles, steps, sms);
-    GemvParams p = {};
+    DirectParams p = {};
     p.x = x;
-    p.codes = w_codes;
-    p.sf = w_sf;
+    p.w.codes = w_codes;
+    p.w.sf = w_sf;
     p.scale = w_scale;
     p.bias = bias;
     p.out = out;
     p.M = static_cast<int32_t>(M);
-    p.N = static_cast<int32_t>(N);
-    p.K = static_cast<int32_t>(K);
+    p.w.N = static_cast<int32_t>(N);
+    p.w.K = static_cast<int32_t>(K);
     p.steps = static_cast<int32_t>(steps);
     p.row_bytes = static_cast<int32_t>((steps + c - 1) / c) * kStepBytes + 32;
     return M <= 8 ? launch_direct<1>(p, static_cast<int>(tiles), c, dev, stream)
