@@ -24,21 +24,20 @@ int* device_status_ptr(int device);
 // Bounded-wait limit for kernels, in nanoseconds.
 uint64_t wait_limit_ns();
 
-// Tensor map of a 2-D byte tensor [rows][row_bytes] with boxes of box_rows x 128 bytes in the
-// 128-byte swizzle.
-int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
-                  uint32_t box_rows);
-
 // Tensor map of a paged cache [groups][tokens][D] of bytes, with boxes of box_tokens x 128 bytes in
 // the 128-byte swizzle (bytes past D are zeros).
 int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens, uint64_t groups,
                   uint32_t box_tokens);
 
-// nvfp4_gemv in one launch, and the sizes for which that is the faster way.
-bool gemv_is_small(int64_t M, int64_t N, int64_t K, int sms);
-int gemv_direct(const __nv_bfloat16* x, const uint8_t* w_codes, const uint8_t* w_sf,
-                const float* w_scale, const __nv_bfloat16* bias, __nv_bfloat16* out, int64_t M,
-                int64_t N, int64_t K, int dev, int sms, cudaStream_t stream);
+// nvfp4_gemv in one launch: the pieces of K that a tile is cut into and the CTAs of an SM, and the
+// launch.  No pieces: for these sizes it is not the faster way.
+struct GemvSplit {
+    int pieces, per_sm;
+};
+GemvSplit gemv_one_launch(int64_t M, int64_t N, int64_t K, int sms);
+int gemv_direct(const GemvSplit& split, const __nv_bfloat16* x, const uint8_t* w_codes,
+                const uint8_t* w_sf, const float* w_scale, const __nv_bfloat16* bias,
+                __nv_bfloat16* out, int64_t M, int64_t N, int64_t K, int dev, cudaStream_t stream);
 
 // nvfp4_gemm (nvf4) / fp8r_gemm launched right after the library's activation quantizer
 // wrote `a` (and `a_sf`): same results, but the weight operand's first stages are fetched

@@ -1405,12 +1405,6 @@ int gemm_entry(bool nvf4, const uint8_t* a, const uint8_t* sfa, const float* a_s
 
 }  // namespace
 
-int make_code_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
-                  uint32_t box_rows)
-{
-    return make_map(m, base, row_bytes, rows, box_rows);
-}
-
 int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens, uint64_t groups,
                   uint32_t box_tokens)
 {
@@ -1425,7 +1419,6 @@ int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_CUDA;
 }
-
 
 int gemm_after_quantizer(bool nvf4, const uint8_t* a, const uint8_t* a_sf, const float* a_scale,
                          const uint8_t* w, const uint8_t* w_sf, const float* w_scale,

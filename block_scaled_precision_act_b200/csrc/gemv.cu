@@ -1,8 +1,11 @@
 // gemv.cu -- nvfp4_gemv: y[m][n] = bf16(g * sum_k x[m][k] w[n][k] + bias[n]) for a few rows of
 // bf16 x, w = e2m1(code) * e4m3(scale) in the layout of nvfp4_gemm.  The weight-only form.
 //
-// What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read
-// (gemv_mma.cuh).  Small weights go another way (gemv_direct.cu).
+// What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read: at
+// 8 rows and less an SM issues in two of three cycles while it reads at 5.3 TB/s (131072 x 8192, one row:
+// 114 us).  With more rows the products' latencies add to that, since the registers leave room for four
+// warps on a scheduler (16384 x 12288, 16 rows: 44 us, 2.6 TB/s; three CTAs on an SM, with spilled
+// registers, took 57).  Small weights go another way (gemv_direct.cu).
 //
 // Two kernels.  nvfp4_gemv_rows_kernel writes x in f16, times a power of two for each row, to the
 // workspace, in the order in which shared memory will hold it.  nvfp4_gemv_kernel: the 256-element K
@@ -96,13 +99,12 @@ __device__ __forceinline__ int run_owner(int64_t total, int ctas, int64_t s)
 
 // NT: 8-row tiles of x.
 template <int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) nvfp4_gemv_kernel(const GemvArgs p)
+__global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs p)
 {
     extern __shared__ uint4 xs[];               // two chunks of x: [step][M][kRowPitch]
     __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
     __shared__ float2 factor[NT * 8];           // 2^e g of a row, in two parts
     __shared__ int last;
-    griddep_wait();
     griddep_launch_dependents();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -113,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) nvfp4_gemv_kernel(c
     const int run = static_cast<int>(run_begin(p.total, ctas, blockIdx.x + 1) - s0);
     const int tile0 = static_cast<int>(s0 / steps), k0 = static_cast<int>(s0 - static_cast<int64_t>(tile0) * steps);
 
-    // the step of the run whose codes the warp holds: every other one is its own
+    // The step of the run whose codes the warp holds: every other one is its own.  The first are on their
+    // way before the rows kernel has ended, which begins only when everything before this call has.
     HalfStep w[2];
     int at_tile = tile0, at_k = k0 + kw;
     while (at_k >= steps) {
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) nvfp4_gemv_kernel(c
         load_half(p.w, rows, at_k, t, 1, w[1]);
     }
 
+    griddep_wait();
     // chunk c of the run's steps to its buffer
     const int step_bytes = M * kRowPitch, buffer = p.chunk * step_bytes;
     const auto bring = [&](int c) {
@@ -149,9 +153,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) nvfp4_gemv_kernel(c
     if (threadIdx.x < NT * 8) {
         const int e = threadIdx.x < M ? p.exponent[threadIdx.x] : 127;
         const float gs = *p.w_scale;
-        // x was multiplied by 2^(141 - e) and the weight by 2^-kDownBits
+        // x was multiplied by 2^(141 - e)
         factor[threadIdx.x] = e == kPoison ? make_float2(NAN, NAN)
-                                           : make_float2(gs, pow2_biased(e - 14 + kDownBits));
+                                           : make_float2(gs, pow2_biased(e - 14));
     }
 
     // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
@@ -303,8 +307,7 @@ int launch_gemv(GemvArgs a, int dev, int sms, cudaStream_t s)
         ready[dev].store(true, std::memory_order_release);
     }
     a.chunk = std::clamp(kChunkBytes / (a.M * kRowPitch) / 2 * 2, 2, kMaxChunk);
-    const int64_t slots = std::min(kMaxCtas, (NT <= 2 ? 2 : 1) * sms);
-    const int64_t ctas = std::min<int64_t>(slots, (a.total + kMinSteps - 1) / kMinSteps);
+    const int64_t ctas = std::min<int64_t>(std::min(kMaxCtas, 2 * sms), (a.total + kMinSteps - 1) / kMinSteps);
     const size_t smem = static_cast<size_t>(2) * a.chunk * a.M * kRowPitch;
     if (launch_kernel(nvfp4_gemv_kernel<NT>, static_cast<unsigned>(ctas), kThreads, smem, s, true,
                       a) != cudaSuccess) {
@@ -346,10 +349,11 @@ int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
     st = check_device(&dev, &sms);
     if (st != BSP_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (gemv_is_small(M, N, K, sms))
-        return gemv_direct(static_cast<const __nv_bfloat16*>(x_bf16), w_codes, w_sf, w_scale,
+    const GemvSplit split = gemv_one_launch(M, N, K, sms);
+    if (split.pieces > 0)
+        return gemv_direct(split, static_cast<const __nv_bfloat16*>(x_bf16), w_codes, w_sf, w_scale,
                            static_cast<const __nv_bfloat16*>(bias_bf16),
-                           static_cast<__nv_bfloat16*>(out_bf16), M, N, K, dev, sms, s);
+                           static_cast<__nv_bfloat16*>(out_bf16), M, N, K, dev, s);
     auto* ws = static_cast<uint8_t*>(workspace);
     GemvArgs a = {};
     a.w.codes = w_codes;

@@ -1,22 +1,13 @@
-// gemv_direct.cu -- nvfp4_gemv of a small weight, in one launch:
+// gemv_direct.cu -- nvfp4_gemv in one launch, where the row tiles' CTAs run at once (or K is short):
 //     y[m][n] = bf16(g * sum_k x[m][k] w[n][k] + bias[n]),   w = e2m1(code) * e4m3(scale).
 //
-// A small weight is read in a microsecond or two, so what bounds the call is latency: the kernel that
-// splits x for the tensor cores' 4-bit operands, and the one that waits for it, take 7 to 9 us
-// however small the weight is.  Here x stays 16 bits wide and the weight becomes f16 (e2m1 * e4m3
-// has at most 6 significant bits and lies in [2^-10, 2688]: exact) on its way through
-// mma.sync m16n8k16 with fp32 sums, 16 weight rows against 8 rows of x.  x is bf16, whose range f16
-// lacks: it is scaled by a power of two per row of x and piece of K, so that its largest element is in
-// [2^14, 2^15); f16 then holds elements down to 2^-28 of that exactly and rounds smaller ones by
-// at most 2^-39 of it.
-//
-// A cluster of up to eight CTAs takes a 128-row tile of the weight (the tile of the scale layout),
-// each a piece of K, and adds its sums through distributed shared memory, in order.  A warp takes the
-// 32 rows r, r + 32, r + 64, r + 96 for 8 values of r, whose scales lie in the same 16-byte words, and
-// every other 256-element step of K: per step a lane reads 32 bytes of codes of each of its four rows
-// and one 16-byte word of scales, all of which it uses.  The products may run over k in any order, so
-// these 64 consecutive codes of a row are the k slots that the lane owns in 16 products.  All of a
-// warp's first step is asked for before x is staged, and each half of the next as soon as one is used.
+// A small weight is read in a microsecond or two, so what bounds the call is latency: a launch, one
+// round to memory and one through the sums.  A cluster of up to eight CTAs takes a 128-row tile of
+// the weight (the tile of the scale layout), each a piece of K, and adds its sums through distributed
+// shared memory, in order.  Every other 256-element step of a piece belongs to one half of the warps
+// (gemv_mma.cuh).  All of a warp's first step is asked for before x is staged, and each half of the
+// next as soon as one is used.  x is scaled for each row and piece of K.
+// 1024 x 1024, one row: 3.9 us; 4096 x 4096: 6.2 us (1.5 TB/s); 18944 x 2048: 8.3 us (2.6 TB/s).
 #include <algorithm>
 #include <atomic>
 
@@ -28,13 +19,9 @@
 namespace bsp {
 namespace {
 
-constexpr int kMaxRows = 16;                    // of x: two tiles of 8
 constexpr int kMaxPieces = 8;
-constexpr int kMaxCostWhole = 1500;             // of a CTA: see gemv_is_small
-constexpr int kMaxCostCut = 2200;
-constexpr int kMaxSteps = kMaxCostCut / 232;    // that such a CTA can have
-constexpr int kMaxStage = 76 * 1024;            // shared memory for x
-static_assert(kMaxRows * (kMaxSteps * kStepBytes + 32) <= kMaxStage, "x of a piece fits");
+constexpr int kMaxStage = 96 * 1024;            // shared memory for x: two CTAs fit an SM
+constexpr int kFewSteps = 6;
 
 struct DirectParams {
     GemvWeight w;
@@ -105,9 +92,9 @@ __device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, u
     __syncthreads();
 }
 
-// NT: 8-row tiles of x.  Grid: the row tiles' clusters.
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const DirectParams p)
+// NT: 8-row tiles of x; PER: CTAs of an SM.  Grid: the row tiles' clusters.
+template <int NT, int PER>
+__global__ void __launch_bounds__(kThreads, PER) nvfp4_gemv_direct_kernel(const DirectParams p)
 {
     extern __shared__ uint4 xs[];               // x in f16
     __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
@@ -169,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Di
                         // a row of x that is not finite gives NaN, whichever piece finds that
                         const float v = amax[col] < 0x7F800000u
                                             ? acc[ta][nt][i] * gs *
-                                                  pow2_biased(x_exponent(amax[col]) - 14 + kDownBits)
+                                                  pow2_biased(x_exponent(amax[col]) - 14)
                                             : NAN;
                         part[col][r] = half ? v : part[col][r] + v;
                     }
@@ -204,21 +191,12 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_direct_kernel(const Di
     if (pieces > 1) cluster_sync();             // the others have read this CTA's sums before it ends
 }
 
-// Pieces of K: as many as leave each half of the warps of a CTA a step and, of all tiles, keep to two
-// CTAs an SM.
-int pieces_of(int64_t tiles, int64_t steps, int sms)
-{
-    int c = 1;
-    while (c < kMaxPieces && 4 * c <= steps && 2 * c * tiles <= 2 * sms) c *= 2;
-    return c;
-}
-
-template <int NT>
-int launch_direct(const DirectParams& p, int tiles, int pieces, int dev, cudaStream_t stream)
+template <int NT, int PER>
+int launch_direct(const DirectParams& p, int64_t ctas, int pieces, int dev, cudaStream_t stream)
 {
     static std::atomic<bool> ready[kMaxDevices];
     if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(nvfp4_gemv_direct_kernel<NT>,
+        if (cudaFuncSetAttribute(nvfp4_gemv_direct_kernel<NT, PER>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kMaxStage) != cudaSuccess) {
             cudaGetLastError();
@@ -234,13 +212,13 @@ int launch_direct(const DirectParams& p, int tiles, int pieces, int dev, cudaStr
     attr[1].val.clusterDim.x = pieces;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles) * pieces, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * p.row_bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, nvfp4_gemv_direct_kernel<NT>, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, nvfp4_gemv_direct_kernel<NT, PER>, p) != cudaSuccess) {
         cudaGetLastError();
         return BSP_ERR_CUDA;
     }
@@ -249,47 +227,58 @@ int launch_direct(const DirectParams& p, int tiles, int pieces, int dev, cudaStr
 
 }  // namespace
 
-// The direct kernel is taken by what a CTA has to do, in instructions of a warp: for each 256-element
-// step 200, 32 for each 8 rows of x and 10 for bringing a row's step of x to shared memory, and as
-// much as a step's for the sums.  Where a tile of the weight is cut into four pieces or eight, the
-// limit is higher: there the other kernel cuts tiles too, and joins them through global memory.
-// Measured, us, here and with the two other kernels:
-//     4096 x 4096:  M = 1 6.4, 8.6;   M = 8 7.6, 8.8;    M = 16 9.0, 10.7    (costs 716 to 1112)
-//     2048 x 8192:  M = 1 6.8, 10.0;  M = 8 8.4, 10.2;   M = 16 11.5, 12.5   (1200 to 1960)
-//     4096 x 14336: M = 1 11.0, 14.3; M = 8 13.3, 14.6;  M = 16 17.9, 16.2   (1926, 2416, 3512)
-//     10368 x 2048: M = 1 7.3, 7.9;   M = 8 9.1, 8.1;    M = 16 12.0, 8.8    (1200, 1480, 1960; two pieces)
-//     65536 x 768:  M = 1 10.8, 15.6; M = 8 13.2, 16.0;  M = 16 17.1, 20.4   (958, 1168, 1536; one piece)
-//     131072 x 2048: M = 1 36.9, 34.0; M = 8 44.2, 35.0                      (2168, 2728; one piece)
-bool gemv_is_small(int64_t M, int64_t N, int64_t K, int sms)
+// Pieces of K: as many as leave each half of the warps of a CTA a step and, of all tiles, keep to two
+// CTAs an SM; or to three, which up to 8 rows of x leave registers for, where that makes it twice as
+// many (10368 x 2560: 9.7 us and 10.7 for 4 and 8 rows, 11.7 and 13.9 with two; where two do, the third's
+// registers cost 10 to 20 %).
+//
+// One launch does better than two where all CTAs run at once, or K is short, as long as a CTA's piece of
+// x fits.  Measured, us, with one and with two launches:
+//     4096 x 14336 (8 pieces):  8 rows 13.3, 21.9;    16 rows 17.9, 25.0
+//     14336 x 4096 (2 pieces):  1 row 11.5, 13.9;     8 rows 14.2, 16.8;   16 rows 19.0, 21.6
+//     65536 x 1280 (1 piece, two waves):  1 row 15.3, 18.5;    16 rows 24.6, 27.2
+//     131072 x 2048 (1 piece, four waves): 1 row 38.1, 38.5;   16 rows 60.9, 57.1
+GemvSplit gemv_one_launch(int64_t M, int64_t N, int64_t K, int sms)
 {
-    if (M > kMaxRows) return false;
     const int64_t tiles = (N + kTileRows - 1) / kTileRows, steps = (K + kStepK - 1) / kStepK;
-    const int c = pieces_of(tiles, steps, sms);
-    const int64_t most = (steps + c - 1) / c;
-    return (most + 1) * (M <= 8 ? 232 : 264) + most * M * 10 <=
-           (c >= 4 ? kMaxCostCut : kMaxCostWhole);
+    const auto pieces = [&](int per) {
+        int c = 1;
+        while (c < kMaxPieces && 4 * c <= steps && 2 * c * tiles <= per * sms) c *= 2;
+        return c;
+    };
+    GemvSplit s = {pieces(2), 2};
+    if (M <= 8 && pieces(3) > s.pieces) s = {pieces(3), 3};
+    const int64_t most = (steps + s.pieces - 1) / s.pieces;
+    const int64_t room = s.per_sm == 2 ? kMaxStage : kMaxStage / 2;
+    if (M * (most * kStepBytes + 32) > room || (tiles * s.pieces > s.per_sm * sms && steps > kFewSteps))
+        s.pieces = 0;
+    return s;
 }
 
-int gemv_direct(const __nv_bfloat16* x, const uint8_t* w_codes, const uint8_t* w_sf,
-                const float* w_scale, const __nv_bfloat16* bias, __nv_bfloat16* out, int64_t M,
-                int64_t N, int64_t K, int dev, int sms, cudaStream_t stream)
+int gemv_direct(const GemvSplit& split, const __nv_bfloat16* x, const uint8_t* w_codes,
+                const uint8_t* w_sf, const float* w_scale, const __nv_bfloat16* bias,
+                __nv_bfloat16* out, int64_t M, int64_t N, int64_t K, int dev, cudaStream_t stream)
 {
     const int64_t tiles = (N + kTileRows - 1) / kTileRows, steps = (K + kStepK - 1) / kStepK;
-    const int c = pieces_of(tiles, steps, sms);
+    const int c = split.pieces;
     DirectParams p = {};
     p.x = x;
     p.w.codes = w_codes;
     p.w.sf = w_sf;
+    p.w.N = static_cast<int32_t>(N);
+    p.w.K = static_cast<int32_t>(K);
     p.scale = w_scale;
     p.bias = bias;
     p.out = out;
     p.M = static_cast<int32_t>(M);
-    p.w.N = static_cast<int32_t>(N);
-    p.w.K = static_cast<int32_t>(K);
     p.steps = static_cast<int32_t>(steps);
     p.row_bytes = static_cast<int32_t>((steps + c - 1) / c) * kStepBytes + 32;
-    return M <= 8 ? launch_direct<1>(p, static_cast<int>(tiles), c, dev, stream)
-                  : launch_direct<2>(p, static_cast<int>(tiles), c, dev, stream);
+    if (M <= 8)
+        return split.per_sm == 3 ? launch_direct<1, 3>(p, tiles * c, c, dev, stream)
+                                 : launch_direct<1, 2>(p, tiles * c, c, dev, stream);
+    if (M <= 16) return launch_direct<2, 2>(p, tiles * c, c, dev, stream);
+    if (M <= 24) return launch_direct<3, 2>(p, tiles * c, c, dev, stream);
+    return launch_direct<4, 2>(p, tiles * c, c, dev, stream);
 }
 
 }  // namespace bsp

@@ -3,7 +3,7 @@
 // A warp takes 32 rows of a 128-row tile, r, r + 32, r + 64, r + 96 for 8 values of r, whose scales lie in
 // the same 16-byte words, and 256 elements of K at a time: a lane reads 2 x 16 bytes of codes of each of
 // its four rows and as many scales, all of which it uses.  Each weight becomes f16 (e2m1 * e4m3 has at
-// most 6 significant bits and lies in [2^-10, 2688]; 2^-7 of it is exact too) on its way through
+// most 6 significant bits and lies in [2^-10, 2688]: exact) on its way through
 // mma.sync m16n8k16 with fp32 sums, 16 weight rows against 8 rows of x.  The products may run over k
 // in any order, so the 64 consecutive codes of a lane's row are the k slots that it owns in 16 products.
 // x is bf16, whose range f16 lacks: it is scaled by a power of two, so that its largest element is in
@@ -22,27 +22,23 @@ constexpr int kTileRows = 128;
 constexpr int kStepK = 256;
 constexpr int kStepBytes = kStepK * 2;          // of one row of x in f16
 constexpr int kThreads = 256;                   // four octets of rows r, two halves of the steps
-constexpr int kDownBits = 7;                    // sums hold the weight times 2^-7
 
 __device__ __forceinline__ float pow2_biased(int e)     // 2^(e - 127), e in [0, 254]
 {
     return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
 }
 
-// Eight codes of w as f16, in pairs: codes (0, 4) and (1, 5) times 2^-14, (2, 3) and (6, 7) as they are.
-// One conversion instruction makes a pair, but an SM has only 16 lanes for it in a cycle: with all
-// four pairs that way it bounds the kernel at 32 weights a cycle, where the memory brings 42.  Two pairs
-// are therefore made of the bits: sign, exponent and mantissa of E2M1 at their places in an f16 are the
-// same number (subnormals too) with the exponent's bias 14 off.
+// Eight codes of w as f16.  (Half of them made of the codes' bits, with shifts and masks, instead of
+// by conversions: 134 us for 131072 x 8192 where this takes 114.)
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
 {
-    h[0] = (w << 12 & 0x80008000u) | (w << 9 & 0x0E000E00u);
-    h[1] = (w << 8 & 0x80008000u) | (w << 5 & 0x0E000E00u);
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b3;\n\t}"
-        : "=r"(h[2]), "=r"(h[3])
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
 }
 
@@ -73,8 +69,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -87,15 +82,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 
-// Eight bf16 of x times `up` in f16, in the order of e2m1x8_to_f16's pairs
+// Eight bf16 of x times `up` in f16
 __device__ __forceinline__ uint4 pack_x8(uint4 v, float up)
 {
-    uint4 h;
-    h.x = pack_f16(bf16lo_to_f32(v.x) * up, bf16lo_to_f32(v.z) * up);
-    h.y = pack_f16(bf16hi_to_f32(v.x) * up, bf16hi_to_f32(v.z) * up);
-    h.z = pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up);
-    h.w = pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up);
-    return h;
+    return make_uint4(pack_f16(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up),
+                      pack_f16(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up),
+                      pack_f16(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up),
+                      pack_f16(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up));
 }
 
 // A lane's loads of half a step (128 elements of K): 32 codes of each of its four rows, at t * 32
@@ -167,7 +160,6 @@ __device__ __forceinline__ void mma_half(float (&acc)[2][NT][4], const HalfStep&
                                          const uint8_t* const (&xg)[NT], int offset, int t)
 {
     const int swap = (t >> 1) * 16;
-    uint32_t up[4], down[4];                    // a row's scale times 2^7 and 2^-7
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint4 b[NT];
@@ -177,22 +169,19 @@ __device__ __forceinline__ void mma_half(float (&acc)[2][NT][4], const HalfStep&
         uint32_t h[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (j % 2 == 0) {
-                // scale byte 2 (t % 2) + j / 2 of the row's word; 2^7 and 2^-7 in f16 are 0x5800, 0x2000
-                const uint32_t sc = scale_to_f16(word_of(w.s, q), (t & 1) * 2 + (j >> 1));
-                up[q] = mul_f16x2(sc, 0x58005800u);
-                down[q] = mul_f16x2(sc, 0x20002000u);
-            }
+            // scale byte 2 (t % 2) + j / 2 of the row's word
+            const uint32_t sc = scale_to_f16(word_of(w.s, q), (t & 1) * 2 + (j >> 1));
             e2m1x8_to_f16(word_of(w.c[q], j), h[q]);
-            h[q][0] = mul_f16x2(h[q][0], up[q]);
-            h[q][1] = mul_f16x2(h[q][1], up[q]);
-            h[q][2] = mul_f16x2(h[q][2], down[q]);
-            h[q][3] = mul_f16x2(h[q][3], down[q]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[q][i] = mul_f16x2(h[q][i], sc);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             mma_f16(acc[0][nt], h[0][0], h[1][0], h[0][1], h[1][1], b[nt].x, b[nt].y);
             mma_f16(acc[1][nt], h[2][0], h[3][0], h[2][1], h[3][1], b[nt].x, b[nt].y);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             mma_f16(acc[0][nt], h[0][2], h[1][2], h[0][3], h[1][3], b[nt].z, b[nt].w);
             mma_f16(acc[1][nt], h[2][2], h[3][2], h[2][3], h[3][3], b[nt].z, b[nt].w);
         }
