@@ -22,6 +22,7 @@ namespace {
 constexpr int kMaxPieces = 8;
 constexpr int kMaxStage = 96 * 1024;            // shared memory for x: two CTAs fit an SM
 constexpr int kFewSteps = 6;
+constexpr int kManySteps = 24;
 
 struct DirectParams {
     GemvWeight w;
@@ -233,10 +234,12 @@ int launch_direct(const DirectParams& p, int64_t ctas, int pieces, int dev, cuda
 // registers cost 10 to 20 %).
 //
 // One launch does better than two where all CTAs run at once, or K is short, as long as a CTA's piece of
-// x fits.  Measured, us, with one and with two launches:
+// x fits and, where there are fewer CTAs than SMs, is not long.  Measured, us, with one and with two launches:
 //     4096 x 14336 (8 pieces):  8 rows 13.3, 21.9;    16 rows 17.9, 25.0
 //     14336 x 4096 (2 pieces):  1 row 11.5, 13.9;     8 rows 14.2, 16.8;   16 rows 19.0, 21.6
 //     65536 x 1280 (1 piece, two waves):  1 row 15.3, 18.5;    16 rows 24.6, 27.2
+//     128 x 65536 (8 pieces of 32 steps): 1 row 18.8, 14.2;    4 rows 22.5, 17.8
+//     128 x 16384 (8 pieces of 8 steps):  1 row 6.6, 8.6;      16 rows 11.7, 17.1
 //     131072 x 2048 (1 piece, four waves): 1 row 38.1, 38.5;   16 rows 60.9, 57.1
 GemvSplit gemv_one_launch(int64_t M, int64_t N, int64_t K, int sms)
 {
@@ -250,7 +253,9 @@ GemvSplit gemv_one_launch(int64_t M, int64_t N, int64_t K, int sms)
     if (M <= 8 && pieces(3) > s.pieces) s = {pieces(3), 3};
     const int64_t most = (steps + s.pieces - 1) / s.pieces;
     const int64_t room = s.per_sm == 2 ? kMaxStage : kMaxStage / 2;
-    if (M * (most * kStepBytes + 32) > room || (tiles * s.pieces > s.per_sm * sms && steps > kFewSteps))
+    const int64_t ctas = tiles * s.pieces;
+    if (M * (most * kStepBytes + 32) > room || (ctas > s.per_sm * sms && steps > kFewSteps) ||
+        (ctas < sms && most > kManySteps))
         s.pieces = 0;
     return s;
 }

@@ -309,13 +309,14 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int layout,
  *   w_codes [N][K/2], w_sf (BSP_SF_MMA, rows = N), w_scale (device, 1 fp32), bias_bf16 [N] or
  *           NULL, out_bf16 [M][N]: as nvfp4_gemm (block scales have no sign).
  *   Y[m][n] = bf16( w_scale * sum_k x[m][k] * e2m1(w[n][k]) * e4m3(sf[n][k/16]) + bias[n] ),
- *   sums in fp32.  x reaches the tensor cores held to 2^-19 of the largest element of its row (bf16
- *   holds an element to 2^-8 of itself), or to 2^-39 where the weight is small.  A row that holds an
- *   infinity or a NaN gives NaN.  The rows do not affect one another.  out must not overlap x.
+ *   sums in fp32.  x reaches the tensor cores in f16 times a power of two for each row: elements down
+ *   to 2^-28 of the row's largest exactly, smaller ones to 2^-39 of it.  A row that holds an infinity or
+ *   a NaN gives NaN.  The rows do not affect one another.  out must not overlap x.
  *   workspace  device buffer of at least nvfp4_gemv_workspace_bytes(M, N, K) bytes, 16-byte
  *              aligned, any contents; not shared by calls that can run at the same time.
- * Constraints: K % 64 == 0, K >= 64; N % 8 == 0; M <= 32 (BSP_ERR_UNSUPPORTED_SHAPE).  The time
- * is that of reading the weight; above 32 rows nvfp4_linear is the faster form.
+ * Constraints: K % 64 == 0, K >= 64; N % 8 == 0; M <= 32 (BSP_ERR_UNSUPPORTED_SHAPE).  Up to
+ * 8 rows the time is nearly that of reading the weight; 16 rows of a large weight take twice that, 32
+ * rows four times, and above nvfp4_linear is the faster form.
  */
 int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
                const float* w_scale, const void* bias_bf16, void* out_bf16, int64_t M, int64_t N,

@@ -1,13 +1,13 @@
 """nvfp4_gemv on the GPU against the 64-bit product of the decoded weight.
 
-Bound.  x enters as seven E2M1 terms, a row's power of two apart.  A term's nearest code leaves at most
-half the codes' distance: 1 unit where |x| <= 6 (distance 2 above 4), which is 4 units of the next
-term, 2^-2; from there half a unit of 2^-2, 2^-5, ... 2^-17, so 2^-18 in the end, and the row's largest
-element is above 3: 2^-19.58 of it.  Products of codes and scales are exact in fp32; a term's sum over K
-is a chain of at most K / 64 + 64 additions (a product instruction takes 64), each off by at most
-2^-22 of sum |term||w|, and a term is at most 4 of its units where 6 units of the first are the most: the
-terms' sizes come to at most |x| + 2^-19.58 top + 2 (1 + 2^-3 + ...) top / 3 <= |x| + top.  The seven sums
-are joined (2^-22 each), the factors and the bias add 2^-21 of the result, the output 2^-8."""
+Bound.  The bounds' first form was for x as seven E2M1 terms, held to 2^-19.58 of the row's largest
+element (`top`); the kernels hold x in f16 to 2^-39 of it, which is inside.  Weights and their scales'
+products are exact in f16 and their products with x in fp32.  A sum over K is made by two halves of the
+warps, each in a chain of at most K / 32 product instructions (K / 512 + 1 steps of 16), and each adds 16
+products to the sum with an error of at most one unit, 2^-23 of sum |x||w|, cut or rounded: K / 64 + 8 times
+2^-22 in all, and half of what it is where the halves have half of the sum.  At most
+K / 1024 + 2 parts are added after that, 2^-24 each.  (K / 64 + 72) 2^-22 (S + top) covers it.  The factors and the bias add 2^-21 of
+the result, the output 2^-8."""
 import math
 
 import numpy as np
@@ -190,8 +190,7 @@ def test_vector_shapes_through_quant_linear(shape):
 @pytest.mark.parametrize("M", [1, 8, 9, 16, 17])
 def test_small_weights_in_one_launch_and_two(M, N, K):
     """The K of a tile in one, two, four and eight pieces of even and uneven lengths, and the sizes past
-    which the call goes the other way.  In one launch x is held in f16 to 2^-39 of the largest of its
-    piece, a warp's sum is a chain of at most 64 products of 16, and 11 sums join: inside the bound."""
+    which the call goes the other way."""
     codes, sf, g = weight(N, K, N + K)
     x = synth.bf16_normal((M, K), 1.0, M, 0.01, 30.0).cuda()
     bias = synth.bf16_normal((N,), 0.1, 7).cuda() if M % 2 else None
@@ -258,3 +257,54 @@ def test_a_weight_written_just_before():
         outs.append(bsp.nvfp4_gemv(x, *now))
     for i, y in enumerate(outs):
         assert torch.equal(y, want[i % 2])
+
+
+@pytest.mark.parametrize("N,K", [(40968, 2112), (600, 50048), (136, 98368), (20008, 6464)])
+@pytest.mark.parametrize("M", [1, 7, 9, 16, 23, 32])
+def test_large_weights(M, N, K):
+    """Tiles that runs begin, end and pass through, steps of K that are not full."""
+    codes, sf, g = weight(N, K, N + K)
+    x = synth.bf16_normal((M, K), 1.0, M, 0.01, 30.0).cuda()
+    bias = synth.bf16_normal((N,), 0.1, 7).cuda() if M % 2 else None
+    y = bsp.nvfp4_gemv(x, codes, sf, g, bias=bias)
+    check(y, x, codes, sf, g, bias)
+    assert torch.equal(y, bsp.nvfp4_gemv(x, codes, sf, g, bias=bias))
+
+
+def test_large_weight_rows_that_are_not_finite():
+    N, K = 38408, 2048
+    codes, sf, g = weight(N, K, 53)
+    x = synth.bf16_normal((12, K), 1.0, 54).cuda()
+    clean = bsp.nvfp4_gemv(x, codes, sf, g)
+    for i, v in enumerate([math.inf, -math.inf, math.nan]):
+        for j, k in enumerate([0, K // 2, K - 1]):
+            x[3 * i + j, k] = v
+    y = bsp.nvfp4_gemv(x, codes, sf, g)
+    assert y[:9].isnan().all() and torch.equal(y[9:], clean[9:])
+
+
+@pytest.mark.parametrize("N,K", [(38408, 2048), (136, 98368), (2048, 4096)])
+def test_streams_at_once_and_graphs_that_share_a_workspace(N, K):
+    M = 9
+    ws = [weight(N, K, 55 + i) for i in range(2)]
+    xs = [synth.bf16_normal((M, K), 1.0, 56 + i).cuda() for i in range(2)]
+    want = [bsp.nvfp4_gemv(x, *w) for x, w in zip(xs, ws)]
+    outs = [torch.zeros_like(want[0]) for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, x, w, o in zip(streams, xs, ws, outs):
+            bsp.nvfp4_gemv(x, *w, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    need = bsp.nvfp4_gemv_workspace_bytes(M, N, K)
+    room = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for gr, x, w, o in zip(graphs, xs, ws, outs):
+        with torch.cuda.graph(gr):
+            bsp.nvfp4_gemv(x, *w, out=o, workspace=room)
+    for i in (0, 1, 0, 1, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
