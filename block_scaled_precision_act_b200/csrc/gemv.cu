@@ -1,11 +1,12 @@
 // gemv.cu -- nvfp4_gemv: y[m][n] = bf16(g * sum_k x[m][k] w[n][k] + bias[n]) for a few rows of
 // bf16 x, w = e2m1(code) * e4m3(scale) in the layout of nvfp4_gemm.  The weight-only form.
 //
-// What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read: at
-// 8 rows and less an SM issues in two of three cycles while it reads at 5.3 TB/s (131072 x 8192, one row:
-// 114 us).  With more rows the products' latencies add to that, since the registers leave room for four
-// warps on a scheduler (16384 x 12288, 16 rows: 44 us, 2.6 TB/s; three CTAs on an SM, with spilled
-// registers, took 57).  Small weights go another way (gemv_direct.cu).
+// What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read: 14
+// instructions for 8 weights of a lane keep the schedulers busy in half of the cycles, and the loads
+// that four warps on each can have in flight bring 5.3 TB/s (131072 x 8192, one row: 114 us; three CTAs on
+// an SM, 111).  With more rows the products and the parts' sums come on top (16384 x 12288, 16 rows: 44 us,
+// 2.6 TB/s; three CTAs on an SM, whose registers spill, 57).  Where all CTAs run at once it goes another
+// way (gemv_direct.cu).
 //
 // Two kernels.  nvfp4_gemv_rows_kernel writes x in f16, times a power of two for each row, to the
 // workspace, in the order in which shared memory will hold it.  nvfp4_gemv_kernel: the 256-element K
