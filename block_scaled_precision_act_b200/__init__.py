@@ -168,7 +168,8 @@ def _scratch(nbytes: int, device, stream):
     if stream is None:
         return torch.empty((nbytes,), dtype=torch.uint8, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
         return torch.empty((nbytes,), dtype=torch.uint8, device=device)
 

@@ -10,18 +10,19 @@ tensors present, as that page's loader does.
 
 The module only marshals: forward() is one nvfp4_linear call (activation quantizer +
 FP4 GEMM) or fp8r_quantize_rows + fp8r_gemm, all in libbsp.so.  An nvfp4 module with
-`weight_only_rows` = r > 0 sends inputs of at most r rows (single tokens of a decode step)
-to nvfp4_gemv instead, which reads the same weight and does not quantize the activations.  `weight_scale` is kept
-in the checkpoint's row-major [N][K/16] layout (the state-dict form); the tensor-core
-layout the GEMM reads is built from it on the device once and rebuilt after a load.
+`weight_only_rows` = r > 0 sends inputs of at most r rows (single tokens of a decode step; 32
+at most) to nvfp4_gemv instead, which reads the same weight and does not quantize the
+activations.  `weight_scale` is kept in the checkpoint's row-major [N][K/16] layout (the
+state-dict form); the tensor-core layout the GEMM reads is built from it on the device once
+and rebuilt after a load.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (SF_LINEAR, SF_MMA, BSPError, fp8kv_append, fp8kv_attention, fp8r_gemm, fp8r_quantize_rows, nvfp4_gemv,
-               nvfp4_global_scale, nvfp4_linear, nvfp4_linear_workspace_bytes,
-               nvfp4_quantize_act, nvfp4_sf_convert)
+from . import (SF_LINEAR, SF_MMA, BSPError, fp8kv_append, fp8kv_attention, fp8r_gemm,
+               fp8r_quantize_rows, nvfp4_gemv, nvfp4_global_scale, nvfp4_linear,
+               nvfp4_linear_workspace_bytes, nvfp4_quantize_act, nvfp4_sf_convert)
 
 __all__ = ["QuantLinear", "PagedKVCache"]
 
@@ -145,7 +146,7 @@ class QuantLinear(torch.nn.Module):
             if self._sf_mma is None:
                 self._sf_mma = nvfp4_sf_convert(_u8(self.weight_scale).contiguous(), N, K,
                                                 SF_LINEAR, SF_MMA)
-            if M <= self.weight_only_rows:
+            if M <= min(self.weight_only_rows, 32):
                 nvfp4_gemv(x2, self.weight, self._sf_mma, self.weight_scale_2, bias=self.bias,
                            out=y)
                 return y.reshape(*lead, N)

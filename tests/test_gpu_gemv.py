@@ -308,3 +308,24 @@ def test_streams_at_once_and_graphs_that_share_a_workspace(N, K):
         graphs[i].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_the_default_stream_by_its_handle():
+    codes, sf, g = weight(2048, 16384, 91)
+    x = synth.bf16_normal((9, 16384), 1.0, 92).cuda()
+    want = bsp.nvfp4_gemv(x, codes, sf, g)
+    torch.cuda.synchronize()
+    got = bsp.nvfp4_gemv(x, codes, sf, g, stream=0)
+    assert torch.equal(got, want)
+    assert torch.equal(bsp.nvfp4_gemv(x, codes, sf, g, stream=torch.cuda.default_stream()), want)
+
+
+def test_quant_linear_past_the_rows_of_the_gemv():
+    lin = torch.nn.Linear(128, 64).to(torch.bfloat16).cuda()
+    q = QuantLinear.from_linear(lin, "nvfp4", input_scale=0.01)
+    x = torch.randn(40, 128, device="cuda").bfloat16()
+    want = q(x)
+    q.weight_only_rows = 64
+    assert torch.equal(q(x), want)
+    few = q(x[:32])
+    check(few, x[:32], q.weight, q._sf_mma, q.weight_scale_2, q.bias)
