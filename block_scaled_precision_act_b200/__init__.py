@@ -23,7 +23,8 @@ __all__ = [
     "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_quant", "fp8r_quantize_rows", "fp8r_gemm",
     "nvfp4_linear", "nvfp4_linear_dynamic", "nvfp4_linear_workspace_bytes", "nvfp4_linear_noalloc",
     "nvfp4_linear_noalloc_max_bytes", "fp8r_linear", "fp8r_linear_workspace_bytes",
-    "nvfp4_gemv", "nvfp4_gemv_workspace_bytes", "fp8kv_append", "fp8kv_attention", "fp8kv_attention_workspace_bytes",
+    "nvfp4_gemv", "nvfp4_gemv_workspace_bytes", "fp8kv_append", "fp8kv_attention",
+    "fp8kv_attention_workspace_bytes",
     "nvfp4_global_scale", "nvfp4_sf_convert", "nvfp4_sf_bytes", "nvfp4_dequantize",
     "bsp_last_device_status", "bsp_set_wait_limit_ms", "bsp_status_string", "bsp_version",
     "bsp_testing_gemm_stall", "bsp_testing_set_gemm_kernel", "bsp_testing_set_quant_kernel",

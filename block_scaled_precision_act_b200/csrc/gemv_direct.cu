@@ -234,7 +234,8 @@ int launch_direct(const DirectParams& p, int64_t ctas, int pieces, int dev, cuda
 // registers cost 10 to 20 %).
 //
 // One launch does better than two where all CTAs run at once, or K is short, as long as a CTA's piece of
-// x fits and, where there are fewer CTAs than SMs, is not long.  Measured, us, with one and with two launches:
+// x fits and, where there are fewer CTAs than SMs, is not long.  Measured, us, with one and with two
+// launches:
 //     4096 x 14336 (8 pieces):  8 rows 13.3, 21.9;    16 rows 17.9, 25.0
 //     14336 x 4096 (2 pieces):  1 row 11.5, 13.9;     8 rows 14.2, 16.8;   16 rows 19.0, 21.6
 //     65536 x 1280 (1 piece, two waves):  1 row 15.3, 18.5;    16 rows 24.6, 27.2

@@ -5,9 +5,9 @@ element (`top`); the kernels hold x in f16 to 2^-39 of it, which is inside.  Wei
 products are exact in f16 and their products with x in fp32.  A sum over K is made by two halves of the
 warps, each in a chain of at most K / 32 product instructions (K / 512 + 1 steps of 16), and each adds 16
 products to the sum with an error of at most one unit, 2^-23 of sum |x||w|, cut or rounded: K / 64 + 8 times
-2^-22 in all, and half of what it is where the halves have half of the sum.  At most
-K / 1024 + 2 parts are added after that, 2^-24 each.  (K / 64 + 72) 2^-22 (S + top) covers it.  The factors and the bias add 2^-21 of
-the result, the output 2^-8."""
+2^-22 in all, and half of what it is where the halves have half of the sum.  At most K / 1024 + 2 parts
+are added after that, 2^-24 each.  (K / 64 + 72) 2^-22 (S + top) covers it.  The factors and the bias add
+2^-21 of the result, the output 2^-8."""
 import math
 
 import numpy as np
