@@ -53,9 +53,6 @@ constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kMaxRows = 16;
 constexpr int kMaxCtas = 480;
 constexpr int kQueue = 4;                        // segments that the loads are ahead by
-constexpr int kItemCost = 3;                     // of an item, in tiles
-constexpr int kWholeRun = kItemCost + 5;         // items of at most that weight are better not cut
-constexpr int kMinRun = kItemCost + 2;           // weight that a CTA takes at least, where they are
 constexpr int kMaxSlots = 12;
 constexpr int kAtom = kTile * 128;               // 128 tokens x 128 bytes
 constexpr int kPShift = 8;
@@ -78,7 +75,7 @@ struct AttnParams {
     Cut* cuts;               // [ctas]
     int32_t box;             // tokens of one load: the largest power of two that divides a page
     int32_t slots;           // of the ring
-    bool whole;              // every item fits in a run of kWholeRun and has its own CTA
+    bool whole;              // every item fits in a run of W::kWhole and has its own CTA
     uint64_t wait_ns;
     int* status;
 };
@@ -97,16 +94,16 @@ __device__ __forceinline__ float lse_of(float m, float l)
 }
 
 // ---- how the work is split.  An item is one row tile of one key head of a sequence; sequence b
-// has items(b) = row tiles * Hkv of tiles(b) token tiles each.  An item weighs its tiles and kItemCost
+// has items(b) = row tiles * Hkv of tiles(b) token tiles each.  An item weighs its tiles and W::kItem
 // for its beginning and end.  All items in a row are cut into runs of equal weight, one for each CTA,
 // whatever the lengths are: a run may end one item, hold whole ones and begin another.  Only the first
 // and the last item of a run can be cut, so a CTA leaves at most two parts; the CTA that begins an
 // item and does not end it notes that, and fp8kv_join_kernel adds the item's parts in order.
 // Where there is little work, the items are aligned to the runs: then no CTA goes through the end of one
 // item and the beginning of another.  If the tables are so short that every item fits in a run of
-// kWholeRun, and there are CTAs for all, none is cut and nothing joined (517 tokens x 8 heads: 12.9 us,
-// and 13.6 cut in two); else every item has its own runs of kMinRun, if the CTAs suffice for that
-// (9910 tokens x 5 heads: 21 us, 29 in runs of kWholeRun).
+// W::kWhole, and there are CTAs for all, none is cut and nothing joined (517 tokens x 8 heads: 12.9 us,
+// and 13.6 cut in two); else every item has its own runs of W::kMin, if the CTAs suffice for that
+// (9910 tokens x 5 heads: 21 us, 29 in runs of W::kWhole).
 struct SeqWork {
     int32_t first, n, len;       // rows, new tokens, length
     int32_t row_tiles, tile0, tiles;
@@ -126,17 +123,28 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b)
     return s;
 }
 
+// Weights, in tiles.  A tile of a wide head takes twice as long, its beginning and end do not (11863
+// tokens of 192: 29 us, 31 with 3; 131071 of 128 take 60 either way, ragged batches 1 to 5 % more with 2 or 4).
+template <int COST>
+struct Weights {
+    static constexpr int kItem = COST;           // of an item, besides its tiles
+    static constexpr int kWhole = COST + 5;      // items of at most that weight are better not cut
+    static constexpr int kMin = COST + 2;        // what a CTA takes at least, where they are
+};
+
 // Weight of an item of the sequence, and of all of them
+template <class W>
 __device__ __forceinline__ int32_t item_weight(const AttnParams& p, const SeqWork& s, bool aligned)
 {
-    const int32_t w = s.tiles + kItemCost;
+    const int32_t w = s.tiles + W::kItem;
     if (!aligned) return w;
-    return p.whole ? kWholeRun : (w + kMinRun - 1) / kMinRun * kMinRun;
+    return p.whole ? W::kWhole : (w + W::kMin - 1) / W::kMin * W::kMin;
 }
 
+template <class W>
 __device__ __forceinline__ int64_t seq_weight(const AttnParams& p, const SeqWork& s, bool aligned)
 {
-    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * item_weight(p, s, aligned);
+    return static_cast<int64_t>(s.row_tiles) * p.c.Hkv * item_weight<W>(p, s, aligned);
 }
 
 struct SplitShared {
@@ -175,18 +183,20 @@ struct Split {
     int b;
 };
 
+template <class W>
 __device__ __forceinline__ bool cut_by(const AttnParams& p, Split& s, int64_t total, bool aligned)
 {
     const int ctas = gridDim.x;
     s.total = total;
     s.aligned = aligned;
-    s.per = aligned && p.whole ? kWholeRun : kMinRun;
+    s.per = aligned && p.whole ? W::kWhole : W::kMin;
     if (total <= s.per * ctas) return true;
     s.per = (total + ctas - 1) / ctas;
     return !aligned;
 }
 
 // Up to 32 sequences: one warp finds it, without a barrier.
+template <class W>
 __device__ __forceinline__ Split find_run_warp(const AttnParams& p)
 {
     const int lane = threadIdx.x & 31;
@@ -195,14 +205,14 @@ __device__ __forceinline__ Split find_run_warp(const AttnParams& p)
     if (in) sw = seq_work(p, lane);
     Split s;
     for (int aligned = 1; aligned >= 0; --aligned) {
-        const int64_t w = in ? seq_weight(p, sw, aligned) : 0;
+        const int64_t w = in ? seq_weight<W>(p, sw, aligned) : 0;
         int64_t inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
             if (lane >= o) inc += y;
         }
-        if (!cut_by(p, s, __shfl_sync(0xFFFFFFFFu, inc, 31), aligned)) continue;
+        if (!cut_by<W>(p, s, __shfl_sync(0xFFFFFFFFu, inc, 31), aligned)) continue;
         const int64_t at = blockIdx.x * s.per;
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, at >= inc - w && at < inc);
         s.b = here ? __ffs(here) - 1 : 0;
@@ -213,6 +223,7 @@ __device__ __forceinline__ Split find_run_warp(const AttnParams& p)
 }
 
 // Any number of them: called by every thread.
+template <class W>
 __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
 {
     const int threads = blockDim.x;
@@ -222,11 +233,11 @@ __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
         int64_t total = 0;
         for (int base = 0; base < p.c.B; base += threads) {
             const int i = base + threadIdx.x;
-            w = i < p.c.B ? seq_weight(p, seq_work(p, i), aligned) : 0;
+            w = i < p.c.B ? seq_weight<W>(p, seq_work(p, i), aligned) : 0;
             excl = chunk_scan(w, sh, chunk);
             total += chunk;
         }
-        if (cut_by(p, s, total, aligned)) break;
+        if (cut_by<W>(p, s, total, aligned)) break;
     }
     const int64_t at = blockIdx.x * s.per;
     if (threadIdx.x == 0) {
@@ -238,7 +249,7 @@ __device__ __forceinline__ Split find_run(const AttnParams& p, SplitShared& sh)
     for (int base = 0; base < p.c.B; base += threads) {
         const int i = base + threadIdx.x;
         if (p.c.B > threads) {                   // otherwise it is still in registers
-            w = i < p.c.B ? seq_weight(p, seq_work(p, i), s.aligned) : 0;
+            w = i < p.c.B ? seq_weight<W>(p, seq_work(p, i), s.aligned) : 0;
             excl = chunk_scan(w, sh, chunk) + carry;
             carry += chunk;
         }
@@ -263,6 +274,7 @@ struct Segment {
 };
 
 // A whole warp walks: every lane holds the same state.
+template <class W>
 struct SegmentWalk {
     int64_t at, end, before;
     int b;
@@ -282,14 +294,14 @@ struct SegmentWalk {
     {
         while (at < end) {
             s.sw = seq_work(p, b);
-            int64_t mine = seq_weight(p, s.sw, split.aligned);
+            int64_t mine = seq_weight<W>(p, s.sw, split.aligned);
             while (at >= before + mine && b + 1 < p.c.B) {
                 before += mine;
                 s.sw = seq_work(p, ++b);
-                mine = seq_weight(p, s.sw, split.aligned);
+                mine = seq_weight<W>(p, s.sw, split.aligned);
                 if (s.sw.n == 0) skip_empty(p);
             }
-            const int weight = item_weight(p, s.sw, split.aligned);
+            const int weight = item_weight<W>(p, s.sw, split.aligned);
             const int64_t off = at - before;
             const int64_t item = off < (int64_t{1} << 31)
                                      ? static_cast<uint32_t>(off) / static_cast<uint32_t>(weight)
@@ -297,15 +309,15 @@ struct SegmentWalk {
             const int from = static_cast<int>(off - item * weight);
             const int to = static_cast<int>(min(static_cast<int64_t>(weight), from + (end - at)));
             at += to - from;
-            // the item's first kItemCost units hold no tile, and none follows its tiles
-            const int seg0 = max(0, from - kItemCost);
-            const int seg1 = min(s.sw.tiles, max(0, to - kItemCost));
+            // the item's first W::kItem units hold no tile, and none follows its tiles
+            const int seg0 = max(0, from - W::kItem);
+            const int seg1 = min(s.sw.tiles, max(0, to - W::kItem));
             if (seg0 >= seg1) continue;
             s.b = b;
             s.begins = seg0 == 0;
             s.whole = seg0 == 0 && seg1 == s.sw.tiles;
             // the run that holds the item's last tile, counted from this one, whose last unit is at - 1
-            s.parts = static_cast<int>((before + item * weight + kItemCost + s.sw.tiles - 1) / split.per -
+            s.parts = static_cast<int>((before + item * weight + W::kItem + s.sw.tiles - 1) / split.per -
                                        (at - 1) / split.per) + 1;
             s.h = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(s.sw.row_tiles));
             s.row_base = static_cast<int>(item - static_cast<int64_t>(s.h) * s.sw.row_tiles) * p.rows;
@@ -428,6 +440,7 @@ __device__ __forceinline__ float from_ordered(int i)
 // R: rows of a row tile; ATOMS: 128-byte pieces of a head.
 template <int R, int ATOMS>
 struct Cfg {
+    using W = Weights<ATOMS == 1 ? 3 : 2>;
     static constexpr int kNS = (3 * R + 15) / 16 * 16;            // columns of S
     static constexpr int kNO = 4 * R;                             // columns of O
     static constexpr int kOCol = 2 * kNS;                         // tensor memory: S at 0, then O
@@ -507,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
     griddep_wait();
     Split cut_up;                                // only the loads ask for it
     if (p.c.B > 32)
-        cut_up = find_run(p, split);
+        cut_up = find_run<typename C::W>(p, split);
     else if (warp == 0)
-        cut_up = find_run_warp(p);
+        cut_up = find_run_warp<typename C::W>(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -522,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         int slot = 0, used = 0;
         uint32_t phase = 1;                      // of an empty slot's barrier, for the first round
         bool ok = true;
-        SegmentWalk walk;
+        SegmentWalk<typename C::W> walk;
         walk.at = blockIdx.x * cut_up.per;
         walk.end = min(walk.at + cut_up.per, cut_up.total);
         walk.before = cut_up.before;
@@ -1190,7 +1203,7 @@ int launch_attention(AttnParams p, const CUtensorMap& k, const CUtensorMap& v, i
     // warps; elsewhere it looks at one and gives a row one warp.
     const int64_t items = (static_cast<int64_t>(p.c.T) * p.G / R + p.c.B) * p.c.Hkv;
     const int64_t longest = (p.c.max_pages * p.c.page_blocks * kKvBlock + kTile - 1) / kTile;
-    p.whole = longest + kItemCost <= kWholeRun && items <= ctas;
+    p.whole = longest + C::W::kItem <= C::W::kWhole && items <= ctas;
     const int group = static_cast<int>(std::clamp<int64_t>(ctas / (2 * items), 1, 16));
     const int share = group > 1 ? kJoinWarps : 1;
     const int rows = std::min(p.rows, p.slot_rows), per_block = kJoinWarps / share;
