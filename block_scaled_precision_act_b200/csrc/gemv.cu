@@ -3,18 +3,18 @@
 //
 // What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read: 14
 // instructions for 8 weights of a lane keep the schedulers busy in half of the cycles, and the loads
-// that four warps on each can have in flight bring 5.3 TB/s (131072 x 8192, one row: 114 us; three CTAs on
-// an SM, 111).  With more rows the products and the parts' sums come on top (16384 x 12288, 16 rows: 44 us,
-// 2.6 TB/s; three CTAs on an SM, whose registers spill, 57).  Where all CTAs run at once it goes another
-// way (gemv_direct.cu).
+// that four warps on each can have in flight bring 5.4 TB/s (131072 x 8192, one row: 111 us).  With more rows
+// the products come on top (16384 x 12288, 16 rows: 40 us, 2.9 TB/s; three CTAs on an SM, whose registers
+// spill, took a quarter longer).  Where all CTAs run at once it goes another way (gemv_direct.cu).
 //
 // Two kernels.  nvfp4_gemv_rows_kernel writes x in f16, times a power of two for each row, to the
 // workspace, in the order in which shared memory will hold it.  nvfp4_gemv_kernel: the 256-element K
 // steps of all 128-row tiles in a row are cut into equal runs, one for each CTA, so that every SM
 // reads the same number of bytes whatever N and K are; a tile that is cut leaves fp32 parts, and the
-// last CTA to finish one adds them in order.  x comes to shared memory a few steps at a time,
-// asynchronously and one such chunk ahead; a lane's codes are one step ahead in registers, across
-// the ends of tiles too.
+// last CTA to finish one adds them in order, when its own run has ended.  x comes to shared memory a few
+// steps at a time, by one bulk copy and one such chunk ahead; a lane's codes are one step ahead in
+// registers, across the ends of tiles too.  (Sums of parts at each end of a tile, with a fence of every
+// thread, and 16-byte copies of x by all threads: 44 us for the 16 rows above.)
 #include <algorithm>
 #include <atomic>
 
@@ -28,9 +28,8 @@ namespace {
 constexpr int kGemvMaxRows = 32;
 constexpr int kMaxCtas = 320;
 constexpr int kMinSteps = 4;                    // of a run
-constexpr int kRowPitch = kStepBytes + 32;      // of x in shared memory: see nvfp4_gemv_kernel
 // Of x in shared memory, twice.  More of it takes from the L1, where loads under way wait: 8 rows of
-// 16384 x 12288 take 34 us, 34 with 18 KB and 44 with 51 KB.
+// 16384 x 12288 took 34 us, 34 with 18 KB and 44 with 51 KB.
 constexpr int kChunkBytes = 36 * 1024;
 constexpr int kMaxChunk = 16;                   // steps
 constexpr int kPoison = 0x7FFFFFFF;             // exponent of a row that is not finite
@@ -48,11 +47,11 @@ struct GemvArgs {
     int32_t steps;               // of K
     int32_t chunk;               // steps of x in shared memory at a time, even
     int64_t total;               // steps of all tiles
+    uint64_t wait_ns;
+    int* status;
 };
 
 // One CTA per row of x; a thread takes 8-element pieces.  Also zeroes the counters of the tiles.
-// Of the 32 16-byte pieces of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped:
-// with that the eight lanes of one shared memory read (four t, two g) are in different banks.
 __global__ void __launch_bounds__(1024)
     nvfp4_gemv_rows_kernel(const __nv_bfloat16* x, int K, int steps, uint8_t* xh, int32_t* exponent,
                            int32_t* done, int tiles)
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(1024)
         if (!held) v = i * 8 < K ? row[i] : make_uint4(0, 0, 0, 0);
         const int step = i >> 5, c = i & 31;
         *reinterpret_cast<uint4*>(xh + (static_cast<int64_t>(step) * M + m) * kStepBytes +
-                                  (c ^ ((c >> 3) & 1)) * 16) = pack_x8(v, up);
+                                  (c ^ x_key(m, c)) * 16) = pack_x8(v, up);
     }
 }
 
@@ -104,10 +103,12 @@ __device__ __forceinline__ int run_owner(int64_t total, int ctas, int64_t s)
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs p)
 {
-    extern __shared__ uint4 xs[];               // two chunks of x: [step][M][kRowPitch]
+    extern __shared__ uint8_t raw[];            // two chunks of x: [step][M][kStepBytes]
     __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
     __shared__ float2 factor[NT * 8];           // 2^e g of a row, in two parts
-    __shared__ int last;
+    __shared__ uint64_t full[2];
+    __shared__ int abort_word, joins[2];
+    volatile int* abort_flag = &abort_word;
     griddep_launch_dependents();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -134,26 +135,31 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs 
     }
 
     griddep_wait();
-    // chunk c of the run's steps to its buffer
-    const int step_bytes = M * kRowPitch, buffer = p.chunk * step_bytes;
+    // Chunk c of the run's steps to its buffer: steps follow one another in the workspace, up to the
+    // last of K.  Thread 0.
+    const uint32_t pad = -smem_u32(raw) & 127u;
+    uint8_t* xs = raw + pad;
+    const int step_bytes = M * kStepBytes, buffer = p.chunk * step_bytes;
     const auto bring = [&](int c) {
-        const int r0 = c * p.chunk, n = min(p.chunk, run - r0) * M * 32;
-        int k = static_cast<int>((k0 + static_cast<int64_t>(r0)) % steps);
-        const uint32_t to = smem_u32(xs) + (c & 1) * buffer;
-        int left = threadIdx.x;                  // piece of step k's
-        int s = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            while (left >= M * 32) {
-                left -= M * 32;
-                ++s;
-                if (++k == steps) k = 0;
-            }
-            cp_async16(to + s * step_bytes + (left >> 5) * kRowPitch + (left & 31) * 16,
-                       p.xh + static_cast<int64_t>(k) * M * kStepBytes + left * 16, true);
-            left += kThreads;
+        int left = min(p.chunk, run - c * p.chunk);
+        int k = static_cast<int>((k0 + static_cast<int64_t>(c) * p.chunk) % steps);
+        uint8_t* to = xs + (c & 1) * buffer;
+        mbar_arrive_expect_tx(full + (c & 1), left * step_bytes);
+        while (left > 0) {
+            const int n = min(left, steps - k);
+            bulk_load(to, p.xh + static_cast<int64_t>(k) * step_bytes, n * step_bytes, full + (c & 1));
+            to += n * step_bytes;
+            left -= n;
+            k = 0;
         }
     };
-    bring(0);
+    if (threadIdx.x == 0) {
+        mbar_init(full, 1);
+        mbar_init(full + 1, 1);
+        abort_word = 0;
+        fence_mbar_init();
+        bring(0);
+    }
     if (threadIdx.x < NT * 8) {
         const int e = threadIdx.x < M ? p.exponent[threadIdx.x] : 127;
         const float gs = *p.w_scale;
@@ -162,13 +168,16 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs 
                                            : make_float2(gs, pow2_biased(e - 14));
     }
 
-    // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
-    // Rows of a tile past M read the last row; their columns are not stored.
-    const uint8_t* xg[NT];
+    // rows of a tile past M read the last row; their columns are not stored
+    uint32_t xg[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, M - 1) * kRowPitch + t * 64;
+    for (int nt = 0; nt < NT; ++nt) {
+        const int m = min(nt * 8 + g, M - 1);
+        xg[nt] = x_address(smem_u32(xs) + m * kStepBytes, m, t);
+    }
 
+    // thread 0: which of the (at most two) tiles that the run cuts are to be joined here
+    int cuts = 0, arrived[2] = {};
     int mine = kw;                               // step of the run
     int r0 = 0;
     for (int tile = tile0; r0 < run; ++tile) {
@@ -179,13 +188,14 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs 
         for (int r = r0; r < r_end;) {
             const int c = r / p.chunk, in_chunk = r - c * p.chunk;
             if (in_chunk == 0) {
-                // the chunk has come, and nobody reads the other buffer any more
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                __syncthreads();
-                if ((c + 1) * p.chunk < run) bring(c + 1);
+                __syncthreads();                 // nobody reads the other buffer any more
+                if (threadIdx.x == 0 && (c + 1) * p.chunk < run) bring(c + 1);
+                // if that runs out it is reported, and the results are wrong
+                mbar_wait(full + (c & 1), c >> 1 & 1, abort_flag, p.wait_ns, p.status, 130);
+                __syncwarp();
             }
             const int r1 = min(r_end, (c + 1) * p.chunk);
-            const int base = (c & 1) * buffer - c * p.chunk * step_bytes;
+            const int base = (c & 1) * buffer - c * buffer;
             for (; mine < r1; mine += 2) {
                 const int xo = base + mine * step_bytes;
                 const bool more = mine + 2 < run;
@@ -239,33 +249,67 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs 
             const int64_t step = static_cast<int64_t>(2) * M * kTileRows;
             float* own = p.parts + blockIdx.x * step + (begins ? step / 2 : 0) + r;
             for (int m = m0; m < M; m += kSide) own[m * kTileRows] = part[m][r];
-            const int64_t t0 = static_cast<int64_t>(tile) * steps;
-            const int o0 = run_owner(p.total, ctas, t0), o1 = run_owner(p.total, ctas, t0 + steps - 1);
-            __threadfence();
             __syncthreads();
-            if (threadIdx.x == 0) last = atomicAdd(p.done + tile, 1) == o1 - o0;
-            __syncthreads();
-            if (last) {
+            if (threadIdx.x == 0) {              // what comes back is looked at when the run has ended
                 __threadfence();
-                // part 0 is the second slot of CTA o0, the others the first of theirs
-                const float* other = p.parts + o0 * step + r;
-                for (int m = m0; m < M; m += kSide) {
-                    const float* of = other + m * kTileRows;
-                    float v = __ldcg(of + step / 2);
-                    for (int i0 = 1; i0 <= o1 - o0; i0 += 4) {
-                        float y[4];              // four parts' loads in flight
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            y[i] = i0 + i <= o1 - o0 ? __ldcg(of + (i0 + i) * step) : 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v += y[i];
-                    }
-                    finish(m, v);
-                }
+                const int n = atomicAdd(p.done + tile, 1);
+                if (cuts == 0)
+                    arrived[0] = n;
+                else
+                    arrived[1] = n;
+                ++cuts;
             }
         }
-        __syncthreads();                         // `part` and `last` are read
+        __syncthreads();                         // `part` is read
     }
+
+    // The parts of the tiles whose last part was brought here.  Cut tiles of a run: its first, its last.
+    const int tile1 = static_cast<int>((s0 + run - 1) / steps);
+    const bool first_cut = k0 != 0 || run < steps, last_cut = (s0 + run) % steps != 0;
+    if (threadIdx.x == 0) {
+        int i = 0;
+        for (int k = 0; k < 2; ++k) {
+            const int tile = k ? tile1 : tile0;
+            joins[k] = -1;
+            if (k ? !last_cut || tile1 == tile0 : !first_cut) continue;
+            const int64_t t0 = static_cast<int64_t>(tile) * steps;
+            const int others = run_owner(p.total, ctas, t0 + steps - 1) - run_owner(p.total, ctas, t0);
+            if ((i++ ? arrived[1] : arrived[0]) == others) joins[k] = tile;
+        }
+        __threadfence();
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        const int tile = joins[k];
+        if (tile < 0) continue;
+        __threadfence();
+        const int64_t t0 = static_cast<int64_t>(tile) * steps;
+        const int o0 = run_owner(p.total, ctas, t0), o1 = run_owner(p.total, ctas, t0 + steps - 1);
+        const int r = threadIdx.x & (kTileRows - 1), n = tile * kTileRows + r;
+        const float bias = n < p.w.N && p.bias ? __bfloat162float(p.bias[n]) : 0.0f;
+        // part 0 is the second slot of CTA o0, the others the first of theirs
+        const int64_t step = static_cast<int64_t>(2) * M * kTileRows;
+        const float* other = p.parts + o0 * step + r;
+        for (int m = threadIdx.x / kTileRows; m < M; m += kThreads / kTileRows) {
+            const float* of = other + m * kTileRows;
+            float v = __ldcg(of + step / 2);
+            for (int i0 = 1; i0 <= o1 - o0; i0 += 4) {
+                float y[4];                      // four parts' loads in flight
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = i0 + i <= o1 - o0 ? __ldcg(of + (i0 + i) * step) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v += y[i];
+            }
+            const float2 f = factor[m];
+            if (n < p.w.N)
+                p.out[static_cast<int64_t>(m) * p.w.N + n] = __float2bfloat16_rn(v * f.x * f.y + bias);
+        }
+    }
+    // a load that was waited for in vain must land before shared memory is freed
+    if (threadIdx.x == 0 && *abort_flag)
+        for (int c = max(0, (run - 1) / p.chunk - 1); c <= (run - 1) / p.chunk; ++c)
+            drain_wait(full + (c & 1), c >> 1 & 1, p.wait_ns, p.status);
 }
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -301,7 +345,7 @@ template <int NT>
 int launch_gemv(GemvArgs a, int dev, int sms, cudaStream_t s)
 {
     static std::atomic<bool> ready[kMaxDevices];
-    constexpr int kSmem = 2 * kChunkBytes;
+    constexpr int kSmem = 2 * kChunkBytes + 128;
     if (!ready[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(nvfp4_gemv_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmem) != cudaSuccess) {
@@ -310,10 +354,10 @@ int launch_gemv(GemvArgs a, int dev, int sms, cudaStream_t s)
         }
         ready[dev].store(true, std::memory_order_release);
     }
-    a.chunk = std::clamp(kChunkBytes / (a.M * kRowPitch) / 2 * 2, 2, kMaxChunk);
+    a.chunk = std::clamp(kChunkBytes / (a.M * kStepBytes) / 2 * 2, 2, kMaxChunk);
     const int64_t ctas = std::min<int64_t>(std::min(kMaxCtas, 2 * sms),
                                            (a.total + kMinSteps - 1) / kMinSteps);
-    const size_t smem = static_cast<size_t>(2) * a.chunk * a.M * kRowPitch;
+    const size_t smem = static_cast<size_t>(2) * a.chunk * a.M * kStepBytes + 128;
     if (launch_kernel(nvfp4_gemv_kernel<NT>, static_cast<unsigned>(ctas), kThreads, smem, s, true,
                       a) != cudaSuccess) {
         cudaGetLastError();
@@ -322,7 +366,7 @@ int launch_gemv(GemvArgs a, int dev, int sms, cudaStream_t s)
     return launch_status();
 }
 
-static_assert(2 * kGemvMaxRows * kRowPitch <= kChunkBytes, "two steps of 32 rows fit a chunk");
+static_assert(2 * kGemvMaxRows * kStepBytes <= kChunkBytes, "two steps of 32 rows fit a chunk");
 
 }  // namespace
 }  // namespace bsp
@@ -375,6 +419,8 @@ int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
     a.M = static_cast<int32_t>(M);
     a.steps = l.steps;
     a.total = static_cast<int64_t>(l.tiles) * l.steps;
+    a.wait_ns = wait_limit_ns();
+    a.status = device_status_ptr(dev);
     const int threads = std::min(1024, l.steps * (kStepK / 8));
     if (launch_kernel(nvfp4_gemv_rows_kernel, static_cast<unsigned>(M), static_cast<unsigned>(threads), 0,
                       s, true, static_cast<const __nv_bfloat16*>(x_bf16), a.w.K, a.steps, ws,

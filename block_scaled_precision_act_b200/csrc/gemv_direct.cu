@@ -32,29 +32,29 @@ struct DirectParams {
     __nv_bfloat16* out;
     int32_t M;
     int32_t steps;            // of K in all
-    int32_t row_bytes;        // between the rows of x in shared memory
+    int32_t row_bytes;        // of a row of x in shared memory
 };
 
-// Steps [a0, a1) of x, a1 > a0, to shared memory in f16; beyond K it is zeros.  Of the
-// 32 16-byte chunks of a step, each pair (2 i, 2 i + 1) in the second half of eight is swapped: with
-// that the eight lanes of one shared memory read (four t, two g) are in different banks.  amax:
-// bits of the largest |x| of each row, 0 before.  A warp takes one step of one row at a time and
-// copies all of its own first, so that their latencies overlap; a lane touches no other's.
-// Every thread calls; the stage is readable on return.
-__device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, uint4* xs,
+// Steps [a0, a1) of x, a1 > a0, to shared memory in f16; beyond K it is zeros.  amax: bits of the largest
+// |x| of each row, 0 before.  A warp takes one step of one row at a time and copies all of its own first,
+// so that their latencies overlap; a lane touches no other's.  Every thread calls; the stage is readable
+// on return.
+__device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, uint8_t* xs,
                                         uint32_t* amax)
 {
     constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int steps = a1 - a0;
-    uint8_t* base = reinterpret_cast<uint8_t*>(xs) + (lane ^ ((lane >> 3) & 1)) * 16;
+    const auto piece = [&](int m, int s) {
+        return reinterpret_cast<uint4*>(xs + m * p.row_bytes + s * kStepBytes) + (lane ^ x_key(m, lane));
+    };
     // units (row m, step s) go to the warps in turn
     const int m0 = warp / steps, s0 = warp - m0 * steps;
     const int dm = kWarps / steps, ds = kWarps - dm * steps;
     for (int m = m0, s = s0; m < p.M;) {
         const int k = (a0 + s) * kStepK + lane * 8;
         const bool in = k < p.w.K;
-        cp_async16(smem_u32(base + m * p.row_bytes + s * kStepBytes),
+        cp_async16(smem_u32(piece(m, s)),
                    p.x + (in ? static_cast<int64_t>(m) * p.w.K + k : 0), in);
         m += dm;
         s += ds;
@@ -65,7 +65,7 @@ __device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, u
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     for (int m = m0, s = s0; m < p.M;) {
-        const uint4 v = *reinterpret_cast<const uint4*>(base + m * p.row_bytes + s * kStepBytes);
+        const uint4 v = *piece(m, s);
         const uint32_t a = max_bf16x2(max_bf16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                       max_bf16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
         const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(a << 16, a & 0xFFFF0000u));
@@ -79,7 +79,7 @@ __device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, u
     }
     __syncthreads();
     for (int m = m0, s = s0; m < p.M;) {
-        uint4* at = reinterpret_cast<uint4*>(base + m * p.row_bytes + s * kStepBytes);
+        uint4* at = piece(m, s);
         const float up = pow2_biased(268 - x_exponent(amax[m]));     // 2^(14 - (e - 127))
         const uint4 v = *at;
         *at = pack_x8(v, up);
@@ -97,7 +97,7 @@ __device__ __forceinline__ void stage_x(const DirectParams& p, int a0, int a1, u
 template <int NT, int PER>
 __global__ void __launch_bounds__(kThreads, PER) nvfp4_gemv_direct_kernel(const DirectParams p)
 {
-    extern __shared__ uint4 xs[];               // x in f16
+    extern __shared__ uint8_t raw[];            // x in f16, from the next multiple of 128
     __shared__ float part[NT * 8][kTileRows + 4];   // the padding spreads a store over the banks
     __shared__ uint32_t amax[NT * 8];           // bits of the largest |x| of this piece
     griddep_wait();
@@ -122,15 +122,16 @@ __global__ void __launch_bounds__(kThreads, PER) nvfp4_gemv_direct_kernel(const 
     }
     if (threadIdx.x < NT * 8) amax[threadIdx.x] = 0;
     __syncthreads();
-    stage_x(p, c0, c1, xs, amax);
+    const uint32_t pad = -smem_u32(raw) & 127u;
+    stage_x(p, c0, c1, raw + pad, amax);
 
-    // 32 bytes of padding: the rows of two neighbouring g start in different halves of the banks.
-    // Rows of a tile past M read the last row; their columns are not stored.
-    const uint8_t* xg[NT];
+    // rows of a tile past M read the last row; their columns are not stored
+    uint32_t xg[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        xg[nt] = reinterpret_cast<const uint8_t*>(xs) + min(nt * 8 + g, p.M - 1) * p.row_bytes +
-                 t * 64;
+    for (int nt = 0; nt < NT; ++nt) {
+        const int m = min(nt * 8 + g, p.M - 1);
+        xg[nt] = x_address(smem_u32(raw) + pad + m * p.row_bytes, m, t);
+    }
     float acc[2][NT][4] = {};
     for (int s = c0 + kw; s < c1; s += 2) {
         const int xo = (s - c0) * kStepBytes;
@@ -215,7 +216,7 @@ int launch_direct(const DirectParams& p, int64_t ctas, int pieces, int dev, cuda
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * p.row_bytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * p.row_bytes + 128;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -234,14 +235,14 @@ int launch_direct(const DirectParams& p, int64_t ctas, int pieces, int dev, cuda
 // registers cost 10 to 20 %).
 //
 // One launch does better than two where all CTAs run at once, or K is short, as long as a CTA's piece of
-// x fits and, where there are fewer CTAs than SMs, is not long.  Measured, us, with one and with two
-// launches:
-//     4096 x 14336 (8 pieces):  8 rows 13.3, 21.9;    16 rows 17.9, 25.0
-//     14336 x 4096 (2 pieces):  1 row 11.5, 13.9;     8 rows 14.2, 16.8;   16 rows 19.0, 21.6
-//     65536 x 1280 (1 piece, two waves):  1 row 15.3, 18.5;    16 rows 24.6, 27.2
-//     128 x 65536 (8 pieces of 32 steps): 1 row 18.8, 14.2;    4 rows 22.5, 17.8
-//     128 x 16384 (8 pieces of 8 steps):  1 row 6.6, 8.6;      16 rows 11.7, 17.1
-//     131072 x 2048 (1 piece, four waves): 1 row 38.1, 38.5;   16 rows 60.9, 57.1
+// x fits and is not long.  Measured, us, with one and with two launches:
+//     4096 x 14336 (8 pieces of 7 steps):  8 rows 13.3, 21.9;   16 rows 17.9, 25.0
+//     14336 x 4096 (2 pieces of 8 steps):  1 row 11.5, 13.9;    16 rows 19.0, 21.6
+//     14336 x 8192 (2 pieces of 16 steps): 1 row 20.0, 20.2;    4 rows 21.9, 21.3
+//     28672 x 8192 (1 piece of 32 steps):  4 rows 37.6, 33.6
+//     128 x 65536 (8 pieces of 32 steps):  1 row 18.8, 14.2;    4 rows 22.5, 17.8
+//     65536 x 1280 (1 piece, two waves):   1 row 15.3, 18.5;    16 rows 24.6, 27.2
+//     131072 x 2048 (1 piece, four waves): 1 row 38.1, 38.5;    16 rows 60.9, 57.1
 GemvSplit gemv_one_launch(int64_t M, int64_t N, int64_t K, int sms)
 {
     const int64_t tiles = (N + kTileRows - 1) / kTileRows, steps = (K + kStepK - 1) / kStepK;
@@ -255,8 +256,8 @@ GemvSplit gemv_one_launch(int64_t M, int64_t N, int64_t K, int sms)
     const int64_t most = (steps + s.pieces - 1) / s.pieces;
     const int64_t room = s.per_sm == 2 ? kMaxStage : kMaxStage / 2;
     const int64_t ctas = tiles * s.pieces;
-    if (M * (most * kStepBytes + 32) > room || (ctas > s.per_sm * sms && steps > kFewSteps) ||
-        (ctas < sms && most > kManySteps))
+    if (M * most * kStepBytes + 128 > room || (ctas > s.per_sm * sms && steps > kFewSteps) ||
+        most > kManySteps)
         s.pieces = 0;
     return s;
 }
@@ -278,7 +279,7 @@ int gemv_direct(const GemvSplit& split, const __nv_bfloat16* x, const uint8_t* w
     p.out = out;
     p.M = static_cast<int32_t>(M);
     p.steps = static_cast<int32_t>(steps);
-    p.row_bytes = static_cast<int32_t>((steps + c - 1) / c) * kStepBytes + 32;
+    p.row_bytes = static_cast<int32_t>((steps + c - 1) / c) * kStepBytes;
     if (M <= 8)
         return split.per_sm == 3 ? launch_direct<1, 3>(p, tiles * c, c, dev, stream)
                                  : launch_direct<1, 2>(p, tiles * c, c, dev, stream);

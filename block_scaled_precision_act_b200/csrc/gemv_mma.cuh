@@ -153,19 +153,38 @@ __device__ __forceinline__ int x_exponent(uint32_t amax_bits)
     return max(15, static_cast<int>(amax_bits >> 23));
 }
 
-// The products of half a step: acc[16-row tile][8 rows of x], and xg[nt]: the lane's 128 bytes of x
-// of 8 rows each, in the half.
+// x in shared memory: rows of whole steps, a multiple of 128 bytes apart, whose 16-byte pieces c lie at
+// c ^ x_key(m, c), so that the eight lanes of one read (four t, two g) are in different banks.
+__device__ __forceinline__ int x_key(int m, int c) { return (m & 7) ^ ((c >> 3 & 1) << 1); }
+
+// Where lane t's 16-byte pieces of row m begin (of piece j: that address ^ 16 j).
+__device__ __forceinline__ uint32_t x_address(uint32_t row, int m, int t)
+{
+    return row + (t >> 1) * 128 + (((t & 1) << 2 ^ x_key(m, t << 2)) << 4);
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// The products of half a step: acc[16-row tile][8 rows of x], and xg[nt]: the lane's x_address of one
+// row of each 8, in the half.
 template <int NT>
 __device__ __forceinline__ void mma_half(float (&acc)[2][NT][4], const HalfStep& w,
-                                         const uint8_t* const (&xg)[NT], int offset, int t)
+                                         const uint32_t (&xg)[NT], int offset, int t)
 {
-    const int swap = (t >> 1) * 16;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint4 b[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            b[nt] = *reinterpret_cast<const uint4*>(xg[nt] + offset + ((j * 16) ^ swap));
+            b[nt] = ld_shared((xg[nt] + offset) ^ (j * 16));
         uint32_t h[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {

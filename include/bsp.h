@@ -316,7 +316,7 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int layout,
  *              aligned, any contents; not shared by calls that can run at the same time.
  * Constraints: K % 64 == 0, K >= 64; N % 8 == 0; M <= 32 (BSP_ERR_UNSUPPORTED_SHAPE).  Up to
  * 8 rows the time is nearly that of reading the weight; 16 rows of a large weight take twice that, 32
- * rows four times.  From some 16 rows of a large weight on, nvfp4_linear is the faster form.
+ * rows four times.  From some 20 rows of a large weight on, nvfp4_linear is the faster form.
  */
 int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
                const float* w_scale, const void* bias_bf16, void* out_bf16, int64_t M, int64_t N,
