@@ -103,7 +103,7 @@ __device__ __forceinline__ float lse_of(float m, float l)
 // item and the beginning of another.  If the tables are so short that every item fits in a run of
 // W::kWhole, and there are CTAs for all, none is cut and nothing joined (517 tokens x 8 heads: 12.9 us,
 // and 13.6 cut in two); else every item has its own runs of W::kMin, if the CTAs suffice for that
-// (9910 tokens x 5 heads: 21 us, 29 in runs of W::kWhole).
+// (9910 tokens x 5 heads: 22 us, 29 in runs of W::kWhole).
 struct SeqWork {
     int32_t first, n, len;       // rows, new tokens, length
     int32_t row_tiles, tile0, tiles;
@@ -437,6 +437,13 @@ __device__ __forceinline__ float from_ordered(int i)
     return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
 }
 
+// A wait's long form as a function of its own: see Cfg::wait.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         uint64_t limit_ns, int* status, int where)
+{
+    return mbar_wait(bar, parity, abort_flag, limit_ns, status, where);
+}
+
 // R: rows of a row tile; ATOMS: 128-byte pieces of a head.
 template <int R, int ATOMS>
 struct Cfg {
@@ -454,6 +461,18 @@ struct Cfg {
     static constexpr int kSlots = std::min(kMaxSlots, (kRoom - kQ - 2 * kP) / kSlot);
     static constexpr int kSmem = 1024 + kSlots * kSlot + kQ + 2 * kP;
     static_assert((R == 8 || R == 16) && kSlots >= 2 && kCols <= 256, "shared and tensor memory");
+    // With 16 rows of a narrow head the code is kept short by calls for the long form of a wait (56 rows of
+    // each of 17 sequences: 93 -> 80 us; 8 new tokens of 9910: 22.1 -> 20.8); with 8 rows those cost
+    // registers (131071 tokens: 60 -> 65 us; 63 where the token threads make none), with wide heads 2 %.
+    static __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                uint64_t limit_ns, int* status, int where)
+    {
+        if constexpr (R == 16 && ATOMS == 1)
+            return mbar_try_wait_for(bar, parity, 20000u) ||
+                   wait_longer(bar, parity, abort_flag, limit_ns, status, where);
+        else
+            return mbar_wait(bar, parity, abort_flag, limit_ns, status, where);
+    }
 };
 
 template <int R>
@@ -546,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             const int e = nseg % kQueue;
             bool room = true;
             if (lane == 0) {
-                room = mbar_wait(seg_free + e, (nseg / kQueue & 1) ^ 1u, abort_flag, p.wait_ns,
+                room = C::wait(seg_free + e, (nseg / kQueue & 1) ^ 1u, abort_flag, p.wait_ns,
                                  p.status, 110);
                 if (room) {
                     if (!more) seg.nrows = -1;
@@ -583,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 for (int kv = 0; kv < 2; ++kv) {
                     bool got = true;
                     if (lane == 0) {
-                        got = mbar_wait(empty + slot, phase, abort_flag, p.wait_ns, p.status, 111);
+                        got = C::wait(empty + slot, phase, abort_flag, p.wait_ns, p.status, 111);
                         if (got) mbar_arrive_expect_tx(full + slot, bytes);
                     }
                     ok = __shfl_sync(0xFFFFFFFFu, got, 0);
@@ -621,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             };
             // O += V^T P^T of tile j of the run
             const auto values = [&](int j, bool fresh) {
-                if (!mbar_wait(full + vslot, vphase, abort_flag, p.wait_ns, p.status, 115) ||
-                    !mbar_wait(p_full + (j & 1), j >> 1 & 1, abort_flag, p.wait_ns, p.status, 116))
+                if (!C::wait(full + vslot, vphase, abort_flag, p.wait_ns, p.status, 115) ||
+                    !C::wait(p_full + (j & 1), j >> 1 & 1, abort_flag, p.wait_ns, p.status, 116))
                     return false;
                 tc_fence_after();
                 const uint32_t a = smem_u32(ring + vslot * C::kSlot);
@@ -643,15 +662,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
             bool ok = true;
             for (int nseg = 0; ok; ++nseg) {
                 const int e = nseg % kQueue;
-                ok = mbar_wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 122);
+                ok = C::wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 122);
                 if (!ok || queue[e].nrows < 0) break;
                 const int begin = queue[e].tile_begin, end = queue[e].tile_end;
                 mbar_arrive(seg_free + e);
-                ok = mbar_wait(&q_full, nseg & 1, abort_flag, p.wait_ns, p.status, 112);
+                ok = C::wait(&q_full, nseg & 1, abort_flag, p.wait_ns, p.status, 112);
                 for (int tile = begin; ok && tile < end; ++tile, ++i) {
-                    ok = mbar_wait(s_free + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
+                    ok = C::wait(s_free + (i & 1), (i >> 1 & 1) ^ 1u, abort_flag, p.wait_ns,
                                    p.status, 113) &&
-                         mbar_wait(full + kslot, kphase, abort_flag, p.wait_ns, p.status, 114);
+                         C::wait(full + kslot, kphase, abort_flag, p.wait_ns, p.status, 114);
                     if (!ok) break;
                     tc_fence_after();
                     uint64_t a = sdesc_kmajor_sw128(smem_u32(ring + kslot * C::kSlot));
@@ -685,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
         Cut cut = {};
         for (int nseg = 0;; ++nseg) {
             const int e = nseg % kQueue;
-            ok = mbar_wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 123) && ok;
+            ok = C::wait(seg_full + e, nseg / kQueue & 1, abort_flag, p.wait_ns, p.status, 123) && ok;
             if (token_any(!ok)) break;
             const Segment seg = queue[e];
             __syncwarp();
@@ -826,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 const bool edge = tile * kTile + kTile - 1 > pos_lo ||
                                   (p.window && tile * kTile <= pos_hi - p.window);
 
-                ok = mbar_wait(s_full + (i & 1), i >> 1 & 1, abort_flag, p.wait_ns, p.status, 117) &&
+                ok = C::wait(s_full + (i & 1), i >> 1 & 1, abort_flag, p.wait_ns, p.status, 117) &&
                      ok;
                 tc_fence_after();
                 __syncwarp();
@@ -901,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                         m[r] = n;
                     }
                     if (tile > seg.tile_begin) {
-                        ok = mbar_wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag,
+                        ok = C::wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag,
                                        p.wait_ns, p.status, 118) &&
                              ok;
                         tc_fence_after();
@@ -960,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 // row sees are cleared, and NaNs of one that only some rows see are taken out and
                 // noted for just those rows.
                 if (!seen || edge) {
-                    ok = mbar_wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 120) && ok;
+                    ok = C::wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 120) && ok;
                     uint8_t* v = ring + slot * C::kSlot + t * 128;
 #pragma unroll 1
                     for (int a = 0; a < ATOMS; ++a)
@@ -1029,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (t == r) sh.m[r] = m[r];
-            ok = mbar_wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag, p.wait_ns, p.status,
+            ok = C::wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag, p.wait_ns, p.status,
                            121) &&
                  ok;
             const bool nans = token_any(any_nan);                 // also: the sums are written
@@ -1292,7 +1311,7 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     st = make_page_map(&tv, v_cache, D, page_size, pages * Hkv, p.box);
     if (st != BSP_OK) return st;
     // Rows of a row tile: 8 when the average sequence has no more, else 16.  (56 rows of each of 17
-    // sequences: 89 us with 16, 99 with 8, which reads the cache from L2 more often, and 115 with 32, which
+    // sequences: 80 us with 16, 99 with 8, which reads the cache from L2 more often, and 115 with 32, which
     // leaves an SM one CTA and nothing to hide its latencies behind.)
     const int64_t rows = p.G * ((T + B - 1) / B);
     p.rows = rows <= 8 ? 8 : 16;
