@@ -238,6 +238,9 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
     Unit unit;
     const int64_t u = blockIdx.x;
     if (!find_unit(p, u, unit)) return;
+    // Units counted by block leave room for a sequence that brings nothing, too.  Neither its length nor
+    // its row of the table is looked at: they may be stale, and the row's pages another sequence's by now.
+    if (unit.n == 0) return;
     const int b = unit.b;
     const int32_t len = unit.len, start = len - unit.n;  // position of the first new token
     if (start < 0 || len > kv_capacity(c)) {

@@ -344,7 +344,8 @@ int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * fp8kv_append stores nothing and fp8kv_attention reads what the table holds; a page outside
  * [0, pages) is not touched (its tokens are neither stored nor attended to).  Such lengths and pages
  * are reported by bsp_last_device_status() as BSP_ERR_INVALID_ARG.  Table entries of pages that a
- * call does not reach are not read.
+ * call does not reach are not read, and of a sequence without new tokens neither the length nor the
+ * table is looked at.
  * Constraints: D % 16 == 0, D <= 256; page_size % 16 == 0, page_size <= 4096; Hq % Hkv == 0,
  * Hq and Hkv <= 4096; B <= 2^20, T <= 2^24, T * Hq <= 2^30; max_pages * page_size <= 2^30.
  */
