@@ -28,6 +28,7 @@ __all__ = [
     "nvfp4_global_scale", "nvfp4_sf_convert", "nvfp4_sf_bytes", "nvfp4_dequantize",
     "bsp_last_device_status", "bsp_set_wait_limit_ms", "bsp_status_string", "bsp_version",
     "bsp_testing_gemm_stall", "bsp_testing_set_gemm_kernel", "bsp_testing_set_quant_kernel",
+    "bsp_testing_set_load_stall",
     "bsp_testing_cvt_range",
 ]
 
@@ -82,6 +83,7 @@ _SIGS = {
     "bsp_version": ([], _c_int),
     "bsp_testing_set_gemm_kernel": ([_c_int], _c_int),
     "bsp_testing_set_quant_kernel": ([_c_int], _c_int),
+    "bsp_testing_set_load_stall": ([ctypes.c_int32], ctypes.c_int32),
     "bsp_testing_cvt_range": ([_c_int, ctypes.c_uint32, _c_i64, _c_vp, _c_vp], _c_int),
     "bsp_testing_gemm_stall": ([_c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64,
                                 _c_i64, _c_i64, _c_i64, _c_i64, _c_vp], _c_int),
@@ -649,6 +651,11 @@ def bsp_testing_set_gemm_kernel(choice: int) -> int:
     if old < 0:
         raise BSPError("bsp_testing_set_gemm_kernel", old)
     return old
+
+
+def bsp_testing_set_load_stall(loads: int) -> int:
+    """Test hook: later fp8kv_attention calls stop after that many loads of a CTA (-1: never)."""
+    return int(lib().bsp_testing_set_load_stall(loads))
 
 
 def bsp_testing_set_quant_kernel(choice: int) -> int:

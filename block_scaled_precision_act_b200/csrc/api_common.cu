@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "bsp_internal.h"
+#include "bsp_testing.h"
 
 namespace {
 
@@ -17,6 +18,7 @@ int g_dev_sms[kMaxDevices];
 int* g_dev_status[kMaxDevices];
 
 std::atomic<int64_t> g_wait_limit_ms{-1};
+std::atomic<int32_t> g_load_stall{INT32_MAX};
 
 void probe_device(int dev)
 {
@@ -76,6 +78,8 @@ uint64_t wait_limit_ns()
     return static_cast<uint64_t>(ms) * 1000000ull;
 }
 
+int32_t load_stall() { return g_load_stall.load(); }
+
 }  // namespace bsp
 
 extern "C" {
@@ -85,6 +89,13 @@ int64_t bsp_set_wait_limit_ms(int64_t ms)
     const int64_t old = static_cast<int64_t>(bsp::wait_limit_ns() / 1000000ull);
     if (ms > 0) g_wait_limit_ms.store(ms);
     return old;
+}
+
+int32_t bsp_testing_set_load_stall(int32_t loads)
+{
+    const int32_t old = bsp::load_stall();
+    g_load_stall.store(loads < 0 ? INT32_MAX : loads);
+    return old == INT32_MAX ? -1 : old;
 }
 
 int bsp_last_device_status(bsp_stream_t stream)

@@ -24,6 +24,9 @@ int* device_status_ptr(int device);
 // Bounded-wait limit for kernels, in nanoseconds.
 uint64_t wait_limit_ns();
 
+// Loads after which a CTA of the decode operators stops loading (bsp_testing_set_load_stall).
+int32_t load_stall();
+
 // Tensor map of a paged cache [groups][tokens][D] of bytes, with boxes of box_tokens x 128 bytes in
 // the 128-byte swizzle (bytes past D are zeros).
 int make_page_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t tokens, uint64_t groups,

@@ -76,6 +76,7 @@ struct AttnParams {
     int32_t box;             // tokens of one load: the largest power of two that divides a page
     int32_t slots;           // of the ring
     bool whole;              // every item fits in a run of W::kWhole and has its own CTA
+    int32_t stop_loads;      // a CTA's loads end after that many (tests of the waits; else never)
     uint64_t wait_ns;
     int* status;
 };
@@ -602,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 for (int kv = 0; kv < 2; ++kv) {
                     bool got = true;
                     if (lane == 0) {
-                        got = C::wait(empty + slot, phase, abort_flag, p.wait_ns, p.status, 111);
+                        got = used < p.stop_loads &&
+                              C::wait(empty + slot, phase, abort_flag, p.wait_ns, p.status, 111);
                         if (got) mbar_arrive_expect_tx(full + slot, bytes);
                     }
                     ok = __shfl_sync(0xFFFFFFFFu, got, 0);
@@ -1020,7 +1022,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     phase ^= 1;
                 }
             }
-            if (!ok) break;
+            // `ok` is each thread's own here (a wait may have run out between two threads' looks), and
+            // what follows is for all of them
+            if (token_any(!ok)) break;
 
             // ---- end of the segment: sums over the tokens, then this thread's d of every row.  This code
             // runs once for many tiles: kept short, it does not wait for its own instructions.
@@ -1303,6 +1307,7 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     p.slot_rows = static_cast<int32_t>(std::min<int64_t>(kMaxRows, T * p.G));
     p.box = 16;
     while (p.box < kTile && page_size % (2 * p.box) == 0) p.box *= 2;
+    p.stop_loads = load_stall();
     p.wait_ns = wait_limit_ns();
     p.status = device_status_ptr(dev);
     CUtensorMap tk, tv;

@@ -2,7 +2,7 @@
  * bsp_testing.h -- test hooks of libbsp.so (not part of the compute path).
  *
  * The pages describe no failure handling; these hooks exist so the bounded waits
- * inside the GEMM kernels can be exercised without faulting or hanging a GPU.
+ * inside the kernels can be exercised without faulting or hanging a GPU.
  */
 #ifndef BSP_TESTING_H_
 #define BSP_TESTING_H_
@@ -30,6 +30,16 @@ int bsp_testing_gemm_stall(int scheme, const uint8_t* a, const uint8_t* a_sf,
                            const float* w_scale, void* out_bf16, int64_t M, int64_t N,
                            int64_t K, int64_t stop_after_stages, int64_t wait_limit_ms,
                            bsp_stream_t stream);
+
+/*
+ * bsp_testing_set_load_stall -- later fp8kv_attention calls of this process stop loading after
+ * `loads` loads of each CTA (two for each tile of 128 tokens: keys, values), so that the waits for the
+ * next one can never complete; a negative count ends that.  Every wait is bounded by
+ * bsp_set_wait_limit_ms(): the call then records BSP_ERR_TIMEOUT in the device status word, waits for
+ * what it has issued and exits, leaving the context usable and its outputs partially written.  Returns
+ * the previous count, -1 for none.
+ */
+int32_t bsp_testing_set_load_stall(int32_t loads);
 
 /*
  * bsp_testing_set_gemm_kernel -- selects the GEMM kernel of later nvfp4_gemm /
