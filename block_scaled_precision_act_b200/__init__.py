@@ -14,6 +14,7 @@ elements, fp32 global scales; fp8r = E4M3 values with an fp32 scale per row.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -91,10 +92,9 @@ _SIGS = {
 
 _lib = None
 
-try:                      # C++ short cut for the calls of a decode step (csrc/fastcall.cpp)
-    from . import _fastcall
-except ImportError:       # not built: the same calls, marshalled in Python
-    _fastcall = None
+# C++ short cut for the calls of a decode step (csrc/fastcall.cpp); lib() loads it.  Not on import: it is
+# linked against libbsp.so, and a process that builds the library must not have mapped an older one.
+_fastcall = None
 
 
 class BSPError(RuntimeError):
@@ -107,7 +107,7 @@ class BSPError(RuntimeError):
 
 def lib() -> ctypes.CDLL:
     """Load ``libbsp.so`` (raises if it has not been built: there is no fallback)."""
-    global _lib
+    global _lib, _fastcall
     if _lib is None:
         if not os.path.exists(library_path):
             raise BSPError("load", -5) from FileNotFoundError(
@@ -118,6 +118,10 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.argtypes = argtypes
             fn.restype = restype
+        try:
+            _fastcall = importlib.import_module("._fastcall", __name__)
+        except ImportError:       # not built: the same calls, marshalled in Python
+            _fastcall = None
         _lib = L
     return _lib
 
