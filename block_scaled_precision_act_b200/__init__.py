@@ -658,7 +658,7 @@ def bsp_testing_set_gemm_kernel(choice: int) -> int:
 
 
 def bsp_testing_set_load_stall(loads: int) -> int:
-    """Test hook: later fp8kv_attention calls stop after that many loads of a CTA (-1: never)."""
+    """Test hook: later fp8kv_attention and nvfp4_gemv calls stop after that many loads of a CTA (-1: never)."""
     return int(lib().bsp_testing_set_load_stall(loads))
 
 

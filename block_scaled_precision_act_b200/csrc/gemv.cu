@@ -47,6 +47,7 @@ struct GemvArgs {
     int32_t steps;               // of K
     int32_t chunk;               // steps of x in shared memory at a time, even
     int64_t total;               // steps of all tiles
+    int32_t stop_loads;          // a CTA's chunks end after that many (tests of the waits; else never)
     uint64_t wait_ns;
     int* status;
 };
@@ -136,11 +137,15 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs 
 
     griddep_wait();
     // Chunk c of the run's steps to its buffer: steps follow one another in the workspace, up to the
-    // last of K.  Thread 0.
+    // last of K.  Thread 0.  Once a wait has run out no more are brought: the buffer's barrier may still
+    // be in the phase of the chunk before, which takes no second arrival.
     const uint32_t pad = -smem_u32(raw) & 127u;
     uint8_t* xs = raw + pad;
     const int step_bytes = M * kStepBytes, buffer = p.chunk * step_bytes;
+    int brought = 0;
     const auto bring = [&](int c) {
+        if (c >= p.stop_loads || *abort_flag) return;
+        brought = c + 1;
         int left = min(p.chunk, run - c * p.chunk);
         int k = static_cast<int>((k0 + static_cast<int64_t>(c) * p.chunk) % steps);
         uint8_t* to = xs + (c & 1) * buffer;
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) nvfp4_gemv_kernel(const GemvArgs 
     }
     // a load that was waited for in vain must land before shared memory is freed
     if (threadIdx.x == 0 && *abort_flag)
-        for (int c = max(0, (run - 1) / p.chunk - 1); c <= (run - 1) / p.chunk; ++c)
+        for (int c = max(0, brought - 2); c < brought; ++c)
             drain_wait(full + (c & 1), c >> 1 & 1, p.wait_ns, p.status);
 }
 
@@ -419,6 +424,7 @@ int nvfp4_gemv(const void* x_bf16, const uint8_t* w_codes, const uint8_t* w_sf,
     a.M = static_cast<int32_t>(M);
     a.steps = l.steps;
     a.total = static_cast<int64_t>(l.tiles) * l.steps;
+    a.stop_loads = load_stall();
     a.wait_ns = wait_limit_ns();
     a.status = device_status_ptr(dev);
     const int threads = std::min(1024, l.steps * (kStepK / 8));

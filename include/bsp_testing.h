@@ -32,9 +32,10 @@ int bsp_testing_gemm_stall(int scheme, const uint8_t* a, const uint8_t* a_sf,
                            bsp_stream_t stream);
 
 /*
- * bsp_testing_set_load_stall -- later fp8kv_attention calls of this process stop loading after
- * `loads` loads of each CTA (two for each tile of 128 tokens: keys, values), so that the waits for the
- * next one can never complete; a negative count ends that.  Every wait is bounded by
+ * bsp_testing_set_load_stall -- later fp8kv_attention and nvfp4_gemv calls of this process stop loading
+ * after `loads` loads of each CTA (attention: two for each tile of 128 tokens, keys and values; gemv, where
+ * it goes by two launches: the chunks of x), so that the waits for the next one can never complete; a
+ * negative count ends that.  Every wait is bounded by
  * bsp_set_wait_limit_ms(): the call then records BSP_ERR_TIMEOUT in the device status word, waits for
  * what it has issued and exits, leaving the context usable and its outputs partially written.  Returns
  * the previous count, -1 for none.

@@ -58,3 +58,27 @@ def test_attention_returns_when_its_loads_stop(case, loads, short_waits):
     got = bsp.fp8kv_attention(q, *args, window=window)
     torch.cuda.synchronize()
     assert bsp.bsp_last_device_status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 40968, 2112), (16, 16384, 8192), (32, 2048, 16384), (9, 136, 98368)])
+@pytest.mark.parametrize("loads", [0, 1, 2])
+def test_gemv_returns_when_its_loads_stop(M, N, K, loads, short_waits):
+    """Sizes that go by two launches.  A CTA without a second or third chunk of x does not notice."""
+    import synth
+    w = synth.bf16_normal((N, K), 0.02, 1).cuda()
+    g = bsp.nvfp4_global_scale(w)
+    codes, sf = bsp.nvfp4_quantize_act(w, g)
+    x = synth.bf16_normal((M, K), 1.0, 2).cuda()
+    want = bsp.nvfp4_gemv(x, codes, sf, g)
+    torch.cuda.synchronize()
+    assert bsp.bsp_last_device_status() == 0
+    bsp.bsp_testing_set_load_stall(loads)
+    bsp.nvfp4_gemv(x, codes, sf, g)
+    torch.cuda.synchronize()
+    status = bsp.bsp_last_device_status()
+    assert status == -6 or (status == 0 and loads > 0)
+    bsp.bsp_testing_set_load_stall(-1)
+    got = bsp.nvfp4_gemv(x, codes, sf, g)
+    torch.cuda.synchronize()
+    assert bsp.bsp_last_device_status() == 0 and torch.equal(got, want)
