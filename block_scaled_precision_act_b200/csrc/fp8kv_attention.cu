@@ -12,15 +12,16 @@
 //   S[128 tokens][3 R] = K Q^T.  A row of q, scaled by a power of two so that its largest element is in
 //   [128, 256), is the sum of three E4M3 rows of q, 16 q and 256 q's rounding rests: each holds four bits,
 //   so a bf16 element (eight bits) is exact, down to 2^-26 of the row's largest.
-//   O[128 d][4 R] = V^T P^T.  A weight in [0, 2^7], times 2^(8 + e_V - e_ref), is rounded once, to f16 (11
-//   bits down to weights of 2^-22, an absolute 2^-33 below), which is exactly the sum of four E5M2
-//   values: an f16 cut to its upper byte is an E5M2, three bits of it, and the rest is an f16 again.
-//   e_ref is a common power of two of the values, no smaller than any block's e_V.
+//   O[128 d][4 R] = V^T P^T.  The operand is p 2^e_V 2^(8 - ref), at most 2^15, rounded once, to f16 (11
+//   bits down to 2^-21 of the row's largest p 2^e_V, an absolute 2^-32 of that below), which is exactly
+//   the sum of four E5M2 values: an f16 cut to its upper byte is an E5M2, three bits of it, and the rest
+//   is an f16 again.  Each row has its own reference for p 2^e_V, beside the one for p: a block of large
+//   values that a row gives no weight takes no bits from it, whatever other rows make of that block.
 // One thread holds one token of a tile: its scores of all rows, so a weight's bytes for all rows and
-// terms are 32 or 64 bytes side by side (the operand's rows are tokens).  The rows' reference
-// maxima move only when a score exceeds one by more than 7 (a factor 2^7 of the weights), which one
-// vote of the 128 threads finds; only then are maxima exchanged and O is rescaled.  The sums of the
-// weights stay in the threads, in fp32, until a run ends.
+// terms are 32 or 64 bytes side by side (the operand's rows are tokens).  The rows' two references are
+// whole numbers (so that every rescaling is exact) and move only when they are exceeded by more than 7
+// (a factor 2^7 of the weights), which one vote of the 128 threads finds; only then are maxima exchanged
+// and O is rescaled.  The sums of the weights stay in the threads, in fp32, until a run ends.
 //
 // Warps: 0 walks over the items and loads the tiles (lanes look up pages and issue one box each), 1
 // issues both products (that of tile i + 1's scores before that of tile i's values), 2-5 are
@@ -480,10 +481,13 @@ template <int R>
 struct TokenShared {
     float row_fac[R];                            // scores: sm_scale log2(e) 2^(row's power)
     int row_pos[R];
-    int wmax[4][R];
-    int we[4];
+    // References of a row, whole numbers: m of its scores (base 2), m + d of its scores plus the value
+    // blocks' exponents.  And what the last change of them was: m's, and the factors of l and O.
+    float m[R], d[R], dm[R], fl[R], fo[R];
+    uint32_t unset;                              // rows whose references are not set yet
+    int smax[4][R], tmax[4][R];
     float wsum[4][R];
-    float m[R], inv[R];                          // of a segment's end
+    float inv[R], unit[R];                       // of a segment's end
     void* to[R];                                 // where the row's output or part goes
     uint32_t nan[R][8];                          // NaN elements of V that a row sees, by d
 };
@@ -819,19 +823,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 }
             }
             for (int k = t; k < R * 8; k += 128) sh.nan[k >> 3][k & 7] = 0;
+            if (t < R) sh.m[t] = sh.d[t] = 0.0f;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
             token_sync();
 
-            float m[R], l[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                m[r] = 0.0f;
-                l[r] = 0.0f;
-            }
-            uint32_t unset = 0xFFFFFFFFu >> (32 - R);             // rows whose reference is not set yet
-            int e_ref = -1, e_top = 0;
+            float l[R] = {};
+            uint32_t unset = 0xFFFFFFFFu >> (32 - R);             // sh.unset
             bool any_nan = false;
 
             for (int tile = seg.tile_begin; tile < seg.tile_end; ++tile, ++i) {
@@ -842,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 block1 = at_block;
                 const int tok = tile * kTile + t;
                 const bool seen = scale.in && tok <= pos_hi;      // by some row, and the page is good
-                const int ev = seen ? min(static_cast<int>(scale.v), kKvMaxExp) : -1;
+                const float ev = seen ? static_cast<float>(min(static_cast<int>(scale.v), kKvMaxExp)) : 0.0f;
                 const float kf = kv_pow2(seen ? min(static_cast<int>(scale.k), kKvMaxExp) : 127);
                 const bool edge = tile * kTile + kTile - 1 > pos_lo ||
                                   (p.window && tile * kTile <= pos_hi - p.window);
@@ -862,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         s[r0 + j] = fmaf(fmaf(fmaf(x[2][j], 0.0625f, x[1][j]), 0.0625f, x[0][j]),
-                                         sh.row_fac[r0 + j] * kf, -m[r0 + j]);
+                                         sh.row_fac[r0 + j] * kf, -sh.m[r0 + j]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -877,49 +876,60 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                         if (tok > pos || (p.window && tok <= pos - p.window)) s[r] = -INFINITY;
                     }
                 }
-                float most = s[0];                                // NaN is no reason to move a reference
+                float most = s[0], most_v = s[0] - sh.d[0];       // NaN is no reason to move a reference
 #pragma unroll
-                for (int r = 1; r < R; ++r) most = fmaxf(most, s[r]);
-                const bool exceed = most > (unset ? -INFINITY : kMaxGrowth) || ev > e_ref ||
-                                    (ev > 0 && ev < e_ref - 10);
+                for (int r = 1; r < R; ++r) {
+                    most = fmaxf(most, s[r]);
+                    most_v = fmaxf(most_v, s[r] - sh.d[r]);
+                }
+                const bool exceed = fmaxf(most, most_v + ev) > (unset ? -INFINITY : kMaxGrowth);
 
                 if (token_any(exceed || !ok)) {
                     if (token_any(!ok)) {                         // a wait ran out
                         ok = false;
                         break;
                     }
-                    // ---- new reference maxima and exponent; O follows
+                    // ---- new references; l and O follow
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        const int v = __reduce_max_sync(
-                            0xFFFFFFFFu, ordered(s[r] == s[r] ? s[r] : -INFINITY));
-                        if (lane == 0) sh.wmax[q][r] = v;
+                        const float x = s[r] == s[r] ? s[r] : -INFINITY;
+                        const int v = __reduce_max_sync(0xFFFFFFFFu, ordered(x));
+                        const int u = __reduce_max_sync(0xFFFFFFFFu, ordered(x - sh.d[r] + ev));
+                        if (lane == 0) {
+                            sh.smax[q][r] = v;
+                            sh.tmax[q][r] = u;
+                        }
                     }
-                    const int we = __reduce_max_sync(0xFFFFFFFFu, ev);
-                    if (lane == 0) sh.we[q] = we;
                     token_sync();
-                    const int e_tile = max(max(sh.we[0], sh.we[1]), max(sh.we[2], sh.we[3]));
-                    int e_new = e_ref;
-                    e_top = max(e_top, e_tile);
-                    if (e_ref < 0 || e_tile > e_ref || (e_tile >= 0 && e_tile < e_ref - 10))
-                        e_new = max(max(e_tile, e_top - 40), 0);
-                    const float ef = e_ref < 0 ? 0.0f : ex2(static_cast<float>(e_ref - e_new));
-                    e_ref = e_new;
-                    float f[R];
+                    if (q == 0) {
+                        bool still = false;
+                        if (lane < R) {
+                            // once to the first maximum, then only up
+                            const bool first = unset >> lane & 1u;
+                            const float least = first ? -INFINITY : 0.0f;
+                            const float v = fmaxf(least, ceilf(from_ordered(
+                                max(max(sh.smax[0][lane], sh.smax[1][lane]),
+                                    max(sh.smax[2][lane], sh.smax[3][lane])))));
+                            const float u = fmaxf(least, ceilf(from_ordered(
+                                max(max(sh.tmax[0][lane], sh.tmax[1][lane]),
+                                    max(sh.tmax[2][lane], sh.tmax[3][lane])))));
+                            still = first && v == -INFINITY;      // nothing seen: all stays 0
+                            const float dm = still ? 0.0f : v, dn = still ? 0.0f : u;
+                            sh.dm[lane] = dm;
+                            sh.m[lane] += dm;
+                            sh.d[lane] += dn - dm;
+                            sh.fl[lane] = first ? 0.0f : ex2(-dm);
+                            sh.fo[lane] = first ? 0.0f : ex2(-dn);
+                        }
+                        const uint32_t left = __ballot_sync(0xFFFFFFFFu, still);
+                        if (lane == 0) sh.unset = left;
+                    }
+                    token_sync();
+                    unset = sh.unset;
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        // how far the reference moves: once to the first maximum, then only up
-                        float v = from_ordered(max(max(sh.wmax[0][r], sh.wmax[1][r]),
-                                                   max(sh.wmax[2][r], sh.wmax[3][r])));
-                        const bool first = unset >> r & 1u, some = v > -INFINITY;
-                        v = first ? (some ? v : 0.0f) : fmaxf(v, 0.0f);
-                        if (some) unset &= ~(1u << r);
-                        const float n = m[r] + v;
-                        f[r] = first ? 0.0f : ex2(m[r] - n);
-                        s[r] += m[r] - n;
-                        l[r] *= f[r];
-                        f[r] *= ef;
-                        m[r] = n;
+                        s[r] -= sh.dm[r];
+                        l[r] *= sh.fl[r];
                     }
                     if (tile > seg.tile_begin) {
                         ok = C::wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag,
@@ -935,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                                 tmem_ld_x8(tlane + C::kOCol + k * R + r0, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] *= f[r0 + j];
+                                for (int j = 0; j < 8; ++j) o[j] *= sh.fo[r0 + j];
                                 tmem_st_x8(tlane + C::kOCol + k * R + r0, o);
                             }
                         tmem_st_wait();
@@ -943,8 +953,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 }
 
                 // ---- weights, their sums, and their four E5M2 terms
-                const int we = 127 + kPShift + ev - e_ref;
-                const float wf = seen && we > 0 ? kv_pow2(we) : 0.0f;
                 uint8_t* pt = ps + (i & 1) * C::kP + t * C::kNO;
                 uint32_t h[R / 2];
 #pragma unroll
@@ -952,7 +960,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     const float p0 = ex2(s[r]), p1 = ex2(s[r + 1]);
                     l[r] += p0;
                     l[r + 1] += p1;
-                    h[r / 2] = pack_f16(p0 * wf, p1 * wf);
+                    h[r / 2] = pack_f16(ex2(s[r] + (ev + kPShift - sh.d[r])),
+                                        ex2(s[r + 1] + (ev + kPShift - sh.d[r + 1])));
                 }
                 uint32_t bytes[4][R / 4];
 #pragma unroll
@@ -1049,9 +1058,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 }
                 sh.wsum[q][row] = l[0];                           // lanes of one row write the same
             }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (t == r) sh.m[r] = m[r];
             ok = C::wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag, p.wait_ns, p.status,
                            121) &&
                  ok;
@@ -1062,7 +1068,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 const int rr = seg.row_base + t, tok = rr / p.G;
                 const int64_t row = static_cast<int64_t>(seg.sw.first + tok) * c.Hq + seg.h * p.G + rr -
                                     tok * p.G;
-                sh.inv[t] = sum == 0.0f ? 0.0f : 1.0f / sum * (1.0f / (1 << kPShift));
+                // the second factor may be subnormal: it comes last
+                sh.inv[t] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                sh.unit[t] = ex2(sh.d[t] - (127 + kPShift));
                 float* part = p.parts + (static_cast<int64_t>(2 * blockIdx.x + seg.begins) *
                                              p.slot_rows +
                                          t) * (c.D + 2);
@@ -1075,7 +1083,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 }
             }
             token_sync();
-            const float unit = kv_pow2(max(e_ref, 0));
 #pragma unroll 1
             for (int a = 0; a < ATOMS; ++a) {
                 const int d = a * 128 + t;
@@ -1091,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     for (int j = 0; j < 8; ++j) {
                         const int r = r0 + j;
                         if (r >= nrows || d >= c.D) break;
-                        float x = ((o[3][j] + o[2][j]) + (o[1][j] + o[0][j])) * sh.inv[r] * unit;
+                        float x = ((o[3][j] + o[2][j]) + (o[1][j] + o[0][j])) * sh.inv[r] * sh.unit[r];
                         if (nans && (sh.nan[r][d >> 5] >> (d & 31) & 1u)) x = NAN;
                         if (seg.whole)
                             static_cast<__nv_bfloat16*>(sh.to[r])[d] = __float2bfloat16_rn(x);
