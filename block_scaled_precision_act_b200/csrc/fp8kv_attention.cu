@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "fp8kv_common.cuh"
 
@@ -67,7 +68,8 @@ struct AttnParams {
     int64_t q_stride;
     __nv_bfloat16* out;
     float* lse;
-    float scale_log2;        // sm_scale * log2(e)
+    float scale_log2;        // sm_scale * log2(e) = scale_log2 2^scale_exp: one below 1 is given in [1, 2),
+    int32_t scale_exp;       // and its power of two goes to the keys' scales
     int32_t window;          // 0: none
     int32_t G;
     int32_t rows;            // R: rows of a row tile
@@ -87,6 +89,12 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^(e - 127), e <= 254, down to the smallest subnormal
+__device__ __forceinline__ float pow2_of(int e)
+{
+    return __int_as_float(e > 0 ? e << 23 : e > -23 ? 1 << (22 + e) : 0);
 }
 
 // log of the sum l of weights exp2(s - m)
@@ -841,8 +849,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 block1 = at_block;
                 const int tok = tile * kTile + t;
                 const bool seen = scale.in && tok <= pos_hi;      // by some row, and the page is good
-                const float ev = seen ? static_cast<float>(min(static_cast<int>(scale.v), kKvMaxExp)) : 0.0f;
-                const float kf = kv_pow2(seen ? min(static_cast<int>(scale.k), kKvMaxExp) : 127);
+                // byte 255 is a NaN: one of a key makes its scores NaN, one of values is noted below
+                const bool nan_v = seen && scale.v == 255;
+                const float ev = seen && !nan_v ? static_cast<float>(scale.v) : 0.0f;
+                const float kf = !seen ? 1.0f : scale.k < 255 ? pow2_of(scale.k + p.scale_exp) : NAN;
                 const bool edge = tile * kTile + kTile - 1 > pos_lo ||
                                   (p.window && tile * kTile <= pos_hi - p.window);
 
@@ -989,6 +999,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 // ---- A masked token's weight is 0, but 0 * NaN is not: the values of a token that no
                 // row sees are cleared, and NaNs of one that only some rows see are taken out and
                 // noted for just those rows.
+                if (nan_v) {
+                    for (int r = 0; r < R; ++r) {
+                        const int pos = sh.row_pos[r];
+                        if (tok <= pos && (p.window == 0 || tok > pos - p.window))
+                            for (int k = 0; k < 8; ++k) atomicOr(&sh.nan[r][k], 0xFFFFFFFFu);
+                    }
+                    any_nan = true;
+                }
                 if (!seen || edge) {
                     ok = C::wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 120) && ok;
                     uint8_t* v = ring + slot * C::kSlot + t * 128;
@@ -1306,7 +1324,9 @@ int fp8kv_attention(const void* q_bf16, int64_t q_stride, const uint8_t* k_cache
     p.q_stride = q_stride;
     p.out = static_cast<__nv_bfloat16*>(out_bf16);
     p.lse = lse;
-    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    const double scale = sm_scale * 1.4426950408889634;
+    if (std::isfinite(scale) && scale != 0.0 && std::fabs(scale) < 1.0) p.scale_exp = std::ilogb(scale);
+    p.scale_log2 = static_cast<float>(std::ldexp(scale, -p.scale_exp));
     p.window = window > (int64_t{1} << 30) ? 0 : static_cast<int32_t>(window);
     p.G = static_cast<int32_t>(Hq / Hkv);
     p.cuts = static_cast<Cut*>(workspace);

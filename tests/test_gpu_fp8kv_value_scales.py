@@ -1,5 +1,5 @@
-"""fp8kv_attention where the value blocks of a sequence differ in scale, against the 64-bit
-reference.
+"""fp8kv_attention where the value blocks of a sequence differ in scale, and the scale bytes that
+fp8kv_append does not make, against the 64-bit reference.
 
 Bounds: those of test_gpu_fp8kv_attention.py, and what they leave out, a product p 2^e (weight times the
 scale of its block) below f16's normal numbers.  The kernel holds p 2^e to half of f16's smallest step,
@@ -40,7 +40,8 @@ def check(b, out, lse, window=0, rows=None, sm=None):
     L = max(b.lens)
     ds = (b.D / 16 + 20) * 2.0 ** -22 * size
     weight = 2 * (2.0 ** -11 + 2.0 ** -20 + ds)[..., None] + (L / 16 + 32) * 2.0 ** -22 + 2.0 ** -20
-    bound = want.abs() * 2.0 ** -8 + weight * mass + least
+    # an output below bf16's normal numbers is off by half of its smallest step, 2^-133
+    bound = want.abs() * 2.0 ** -8 + weight * mass + least + 2.0 ** -134
     rows = list(range(int(b.cu[-1]))) if rows is None else rows
     got = out.cpu().double()
     d = (got - want).abs()
@@ -134,3 +135,43 @@ def test_blocks_of_zeros():
     for page, slot in tokens(b, 0, 128, 256):
         b.v_cache[page, :, slot], b.v_scale[page, :, slot // BLOCK] = 0, 0
     check(b, *call(b))
+
+
+@pytest.mark.parametrize("byte", [0, 1, 246, 247, 250, 254])
+def test_every_finite_scale_byte(byte):
+    """value = code * 2^(byte - 127) up to byte 254; only codes of at most 1, so that sums stay finite."""
+    b = Batch([1, 3], [40, 300], 4, 2, 64, 16, seed=byte)
+    b.k_scale[:], b.v_scale[:] = 118, byte
+    b.v_cache = (b.v_cache & 0x80) | (b.v_cache & 0x7F) % 56
+    check(b, *call(b))
+    b = Batch([1, 3], [40, 300], 4, 2, 64, 16, seed=byte + 1)
+    b.k_scale[:], b.v_scale[:] = byte, 120
+    sm = 2.0 ** (120 - byte)
+    if byte > 1:                                     # sm_scale is an fp32 number
+        check(b, *call(b, sm_scale=sm), sm=sm)
+
+
+def test_a_nan_scale_of_values_reaches_the_rows_that_see_it():
+    for n, L, window, lo, sees in ((6, 114, 0, 112, [4, 5]), (6, 130, 62, 48, [0]), (2, 700, 0, 256, [0, 1])):
+        b = Batch([n], [L], 4, 2, 64, 16, seed=L)
+        page, slot = b.where(0, lo)
+        b.v_scale[page, 1, slot // BLOCK] = 255
+        out, lse = call(b, window=window)
+        assert out[sees, 2:].isnan().all()
+        assert int(out.isnan().sum()) == len(sees) * 2 * 64
+        b.v_scale[page, 1, slot // BLOCK] = 0        # what the reference may not see
+        b.v_cache[page, 1] = 0
+        rest = [r for r in range(n) if r not in sees]
+        if rest:
+            check(b, out, lse, window, rest)
+        want = attention(b, b.D ** -0.5, window)[1]
+        assert torch.allclose(lse.cpu().double(), want, atol=1e-3, rtol=0)
+
+
+def test_a_nan_scale_of_keys_reaches_the_rows_that_see_it():
+    b = Batch([6], [114], 4, 2, 64, 16, seed=9)
+    page, slot = b.where(0, 112)
+    b.k_scale[page, 0, slot // BLOCK] = 255
+    out, lse = call(b)
+    assert out[4:, :2].isnan().all() and lse[4:, :2].isnan().all()
+    assert int(out.isnan().sum()) == 2 * 2 * 64 and int(lse.isnan().sum()) == 4
