@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
             (t.is_k ? c.k : c.v) + (group * c.page_blocks + in_page) * kKvBlock * c.D;
         int e = kv_scale_exp(amax);
         if (lo > 0) {                                    // the block holds earlier tokens
-            const int old = min(static_cast<int>(*scale), kKvMaxExp);
+            const int old = *scale;
             if (e > old) {
                 const int d = e - old;                   // their codes times 2^-d, rounded once
                 const float f = d < 126 ? kv_pow2(127 - d) : 0.0f;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
         }
         __syncwarp();
         if (lane == 0) *scale = static_cast<uint8_t>(e);
-        const float f = kv_pow2(254 - e);                // 2^(127 - e), a normal number for every e
+        const float f = kv_pow2_low(254 - e);            // 2^(127 - e), a normal number for every e made here
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const Slot& w = slot[i];

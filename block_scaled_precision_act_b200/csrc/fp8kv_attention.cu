@@ -91,12 +91,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// 2^(e - 127), e <= 254, down to the smallest subnormal
-__device__ __forceinline__ float pow2_of(int e)
-{
-    return __int_as_float(e > 0 ? e << 23 : e > -23 ? 1 << (22 + e) : 0);
-}
-
 // log of the sum l of weights exp2(s - m)
 __device__ __forceinline__ float lse_of(float m, float l)
 {
@@ -852,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 // byte 255 is a NaN: one of a key makes its scores NaN, one of values is noted below
                 const bool nan_v = seen && scale.v == 255;
                 const float ev = seen && !nan_v ? static_cast<float>(scale.v) : 0.0f;
-                const float kf = !seen ? 1.0f : scale.k < 255 ? pow2_of(scale.k + p.scale_exp) : NAN;
+                const float kf = !seen ? 1.0f : scale.k < 255 ? kv_pow2_low(scale.k + p.scale_exp) : NAN;
                 const bool edge = tile * kTile + kTile - 1 > pos_lo ||
                                   (p.window && tile * kTile <= pos_hi - p.window);
 

@@ -78,6 +78,12 @@ __device__ __forceinline__ float kv_pow2(int e)
     return __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
 }
 
+// The same down to the smallest subnormal, and 0 below it
+__device__ __forceinline__ float kv_pow2_low(int e)
+{
+    return __int_as_float(e > 0 ? e << 23 : e > -23 ? 1 << (22 + e) : 0);
+}
+
 // Four E4M3 bytes -> two pairs of f16 (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
 {

@@ -363,7 +363,7 @@ int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   q_out    [T][Hq][D] bf16, contiguous; may be q itself when that is contiguous.
  * For each block of 16 tokens and head (x: the rotated keys in fp32, or the values):
  *   e = ceil(log2(amax / 448)) + 127 over the new tokens, within [0, 246] (0 when amax is 0); a
- *   block that already holds tokens keeps the larger of e and its own, and codes that it holds
+ *   block that already holds tokens keeps the larger of e and its own (255, a NaN, too), and codes that it holds
  *   move to a raised scale by one rounding; code = E4M3(x * 2^(127 - e)), to nearest even,
  *   saturating at +-448.  Infinities store as +-448 * 2^119, a NaN stores as NaN (only its own
  *   element).
