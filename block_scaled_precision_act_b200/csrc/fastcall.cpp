@@ -52,6 +52,16 @@ struct Args {
         ok = false;
         return nullptr;
     }
+    // a truth value; where asking for it raises, the error is dropped: the Python code meets it again
+    bool truth(int i)
+    {
+        const int v = PyObject_IsTrue(a[i]);
+        if (v < 0) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return v > 0;
+    }
     bool require(bool b)
     {
         ok = ok && b;
@@ -168,9 +178,9 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n)
         const int64_t Hq = q ? q->size(1) : 0;
         const at::Tensor* out = q ? a.maybe(10, at::kBFloat16, T * Hq * c.D) : nullptr;
         const at::Tensor* f = a.maybe(11, at::kFloat, 0);
-        const int inter = PyObject_IsTrue(args[12]);
+        const int inter = a.truth(12);
         const double rope = PyFloat_Check(args[13]) ? PyFloat_AS_DOUBLE(args[13]) : NAN;
-        if (!a.require(inter >= 0 && PyFloat_Check(args[13]))) Py_RETURN_NONE;
+        if (!a.require(PyFloat_Check(args[13]))) Py_RETURN_NONE;
         at::Tensor made;
         if (q && !out) out = &(made = a.make({T, Hq, c.D}, at::kBFloat16));
         if (fp8kv_append(data(q), qs, data(k), ks, data(v), vs, f ? f->data_ptr<float>() : nullptr,
@@ -209,10 +219,10 @@ PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n)
         }
         const at::Tensor* out = a.maybe(10, at::kBFloat16, T * Hq * c.D);
         const at::Tensor* lse = a.maybe(11, at::kFloat, T * Hq);
-        const int want = PyObject_IsTrue(args[12]);
+        const bool want = a.truth(12);
         const int64_t need = fp8kv_attention_workspace_bytes(T, Hq, c.Hkv, c.D);
         const at::Tensor* ws = a.maybe(13, at::kByte, need);
-        if (!a.require(want >= 0 && need >= 0)) Py_RETURN_NONE;
+        if (!a.require(need >= 0)) Py_RETURN_NONE;
         at::Tensor made, made_lse, room;
         if (!out) out = &(made = a.make({T, Hq, c.D}, at::kBFloat16));
         if (want && !lse) lse = &(made_lse = a.make({T, Hq}, at::kFloat));
