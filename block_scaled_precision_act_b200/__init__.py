@@ -561,7 +561,7 @@ def fp8kv_attention(q: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_t
     pages, Hkv, page, D, B, max_pages = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table,
                                                   cu_new, kv_len)
     T, Hq, _, qs = _heads(q, "q", None, D)
-    if Hq % Hkv != 0:
+    if Hkv == 0 or Hq % Hkv != 0:
         raise BSPError(f"argument check (q's {Hq} heads are no multiple of the cache's {Hkv})", -1)
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
