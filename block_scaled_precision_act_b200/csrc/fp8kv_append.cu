@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(kAppendThreads, NS <= 4 ? 3 : 2)
     // its row of the table is looked at: they may be stale, and the row's pages another sequence's by now.
     if (unit.n == 0) return;
     const int b = unit.b;
-    const int32_t len = unit.len, start = len - unit.n;  // position of the first new token
-    if (start < 0 || len > kv_capacity(c)) {
+    const int32_t len = unit.len;
+    if (len < unit.n || len > kv_capacity(c)) {
         if (u == unit.begin && blockIdx.y == 0 && threadIdx.x == 0) kv_report_bad_batch(p.status);
         return;
     }
+    const int32_t start = len - unit.n;                  // position of the first new token
     const int64_t off = u - unit.begin;
     if (p.per != 1 && off > 0 && (start + off) % kKvBlock != 0) return;    // not a block's first token
     const int64_t block = p.per == 1 ? start / kKvBlock + off : (start + off) / kKvBlock;
