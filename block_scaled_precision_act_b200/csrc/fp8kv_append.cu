@@ -190,8 +190,10 @@ __device__ __forceinline__ Task task_of(const AppendParams& p, int task, int64_t
 // Units: sequence b's begin at floor(cu_new[b] * per / 16) + extra * b.  With per = 1, extra = 2 they are
 // its blocks, of which it touches at most floor(n / 16) + 2; with per = 16, extra = 0 they are its
 // tokens, of which the first of each block does the block's work.  The host takes the fewer.
-// The sequence whose units contain unit u is found by all threads at once: one load and one barrier
-// for each blockDim.x sequences, not a chain of dependent loads.
+// The sequence whose units contain unit u is found by all threads at once, one load and one barrier for
+// 256 sequences, not a chain of dependent loads.  More sequences are first narrowed down to that many, by
+// a 256th at a time (the beginnings ascend with cu_new; whatever it holds, the result is looked at again):
+// every CTA does this, so looking at all of 2^20 sequences in each would take minutes.
 struct Unit {
     int64_t begin;               // the sequence's first unit
     int32_t b, first, n, len;
@@ -203,7 +205,19 @@ __device__ __forceinline__ bool find_unit(const AppendParams& p, int64_t u, Unit
     const KvCache& c = p.c;
     if (threadIdx.x == 0) found.b = -1;
     __syncthreads();
-    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+    int from = 0, to = c.B;
+    while (to - from > kAppendThreads) {
+        const int step = (to - from + kAppendThreads - 1) / kAppendThreads;
+        const int at = from + static_cast<int>(threadIdx.x) * step;
+        const bool before =
+            at < to && static_cast<int64_t>(kv_clamp_row(c.cu_new[at], c.T)) * p.per / kKvBlock +
+                               static_cast<int64_t>(p.extra) * at <=
+                           u;
+        from += max(__syncthreads_count(before) - 1, 0) * step;
+        to = min(to, from + step);
+    }
+    const int i = from + static_cast<int>(threadIdx.x);
+    if (i < to) {
         const KvRows r = kv_rows(c, i);
         const int32_t len = c.kv_len[i];
         const int64_t at = static_cast<int64_t>(r.first) * p.per / kKvBlock +
