@@ -62,3 +62,23 @@ def test_very_many(B, every, n):
         unit = torch.exp2(e.double() - 127).repeat_interleave(BLOCK, 1)[..., None]
         assert torch.equal(got[:, :n], encode(sign * x[:, :n] / unit[:, :n]))
         assert (got[:, n:] == 0x55).all()
+
+
+@pytest.mark.parametrize("B", [193, 70000, 1 << 20])
+def test_attention_over_very_many(B):
+    """A few active sequences among B, of one tile each (nothing is cut), against the same ones alone."""
+    b = Batch([2, 1, 3, 1], [100, 1, 128, 57], 8, 2, 64, 16, seed=B)
+    dev = b.to("cuda")
+    want, wlse = bsp.fp8kv_attention(b.q.cuda(), **dev, return_lse=True)
+    at = torch.tensor([0, 5, B // 2, B - 1])
+    n = torch.zeros(B + 1, dtype=torch.int32)
+    n[at + 1] = torch.tensor(b.n, dtype=torch.int32)
+    kv_len = torch.full((B,), 9, dtype=torch.int32)
+    kv_len[at] = b.kv_len
+    table = torch.full((B, b.table.shape[1]), -1, dtype=torch.int32)
+    table[at] = b.table
+    dev.update(cu_new=n.cumsum(0).to(torch.int32).cuda(), kv_len=kv_len.cuda(), block_table=table.cuda())
+    out, lse = bsp.fp8kv_attention(b.q.cuda(), **dev, return_lse=True)
+    torch.cuda.synchronize()
+    assert bsp.bsp_last_device_status() == 0
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
