@@ -86,6 +86,14 @@ cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsigned blo
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// A grid that waits for the one in front (griddep_wait) must not hold tensor memory which that one still
+// asks for.  The GEMMs let their dependents begin before they have theirs: so a CTA of theirs leaves an SM
+// no shared memory for a CTA of the other kernel that takes tensor memory before it waits,
+// fp8kv_attention_kernel, which in turn lets its dependents begin only after it has its own.
+constexpr int kSmemOfSm = 228 * 1024, kSmemOfCta = 1024;        // the latter: reserved for each CTA
+constexpr int kLeastSmemWithTmem = 48 * 1024;
+constexpr int kLeastSmemOfGemm = kSmemOfSm - 2 * kSmemOfCta - kLeastSmemWithTmem;
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline int launch_status()

@@ -465,6 +465,7 @@ struct Cfg {
     static constexpr int kSlots = std::min(kMaxSlots, (kRoom - kQ - 2 * kP) / kSlot);
     static constexpr int kSmem = 1024 + kSlots * kSlot + kQ + 2 * kP;
     static_assert((R == 8 || R == 16) && kSlots >= 2 && kCols <= 256, "shared and tensor memory");
+    static_assert(kSmem >= kLeastSmemWithTmem, "no room beside a GEMM's CTA");
     // With 16 rows of a narrow head the code is kept short by calls for the long form of a wait (56 rows of
     // each of 17 sequences: 93 -> 80 us; 8 new tokens of 9910: 22.1 -> 20.8); with 8 rows those cost
     // registers (131071 tokens: 60 -> 65 us; 63 where the token threads make none), with wide heads 2 %.

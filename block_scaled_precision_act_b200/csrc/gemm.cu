@@ -87,6 +87,7 @@ struct Cfg {
     static constexpr uint32_t IDESC = NVF4 ? idesc_nvf4(kBM, BN) : idesc_e4m3(kBM, BN);
     static_assert(TMEM_USED <= (int)kTmemCols, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(SMEM_BYTES > kLeastSmemOfGemm, "no room for others that take tensor memory");
     static_assert(BN % 128 == 0 && BN <= 256, "tile width");
 };
 
@@ -419,6 +420,7 @@ struct PairCfg {
     static constexpr int SF_BUF = 48;                  // SFA 16 + SFB 32 per K-stage
     static constexpr uint32_t IDESC = NVF4 ? idesc_nvf4(256, 256) : idesc_e4m3(256, 256);
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(SMEM_BYTES > kLeastSmemOfGemm, "no room for others that take tensor memory");
     static_assert(OFF_EPI % 1024 == 0, "epilogue slabs must be 1024-byte aligned");
     static_assert(SF_COL0 + SF_NBUF * SF_BUF <= 512 && (!NVF4 || ACC_STRIDE + 256 <= SF_COL0) &&
                       ACC_STRIDE + 256 <= 512, "TMEM budget");
