@@ -1,0 +1,74 @@
+"""The cache operators over head widths, page sizes and groups that the other tests pass over, queries that
+are not finite, a context of 131071 tokens, and calls that repeat themselves to the last bit."""
+import math
+
+import pytest
+import torch
+
+import block_scaled_precision_act_b200 as bsp
+from kv_reference import Batch
+from test_gpu_fp8kv_append import call as append, check as check_append
+from test_gpu_fp8kv_attention import NAMES, call, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D", [16, 32, 48, 144, 160, 176, 208, 224, 240])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 3), (10, 2)])
+def test_head_widths(D, Hq, Hkv):
+    b = Batch([2, 9, 0, 33], [150, 9, 40, 290], Hq, Hkv, D, 48, seed=D)
+    rot = D // 32 * 16
+    q, got = append(b, rot, D % 32 == 0)
+    check_append(b, q, got, rot, D % 32 == 0)
+    check(b, *call(b))
+    assert bsp.bsp_last_device_status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 48, 80, 96, 112, 144, 240, 1040, 4096])
+@pytest.mark.parametrize("window", [0, 77])
+def test_page_sizes(page, window):
+    b = Batch([1, 5, 20], [700, 129, 257], 8, 2, 64, page, seed=page, spare=1)
+    q, got = append(b, 64)
+    check_append(b, q, got, 64)
+    check(b, *call(b, window=window), window=window)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(64, 1, [1, 3]), (100, 1, [2, 1]), (96, 96, [1, 1]), (21, 7, [17, 1])])
+def test_groups(Hq, Hkv, n):
+    b = Batch(n, [210, 300], Hq, Hkv, 64, 32, seed=Hq)
+    check(b, *call(b))
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_queries_that_are_not_finite(D):
+    """An infinity or a NaN in a head of a row gives NaN there; every other head and row keeps its value
+    within the bounds.  (Not to the last bit: when the references of a tile's rows move, and so the
+    numbers that a score is rounded next to, depends on all rows of the tile.  The bounds hold for any.)"""
+    b = Batch([3, 1], [45, 300], 8, 2, D, 16, seed=D)
+    clean, lse = call(b)
+    finite = b.q.clone()
+    b.q[1, 2, 5], b.q[1, 6, 0], b.q[3, 7, D - 1] = math.nan, math.inf, -math.inf
+    out, lse2 = call(b)
+    bad = torch.zeros((4, 8), dtype=torch.bool)
+    bad[1, 2], bad[1, 6], bad[3, 7] = True, True, True
+    assert out.cpu()[bad].isnan().all() and lse2.cpu()[bad].isnan().all()
+    b.q = finite
+    out[bad.cuda()], lse2[bad.cuda()] = clean[bad.cuda()], lse[bad.cuda()]
+    check(b, out, lse2)
+
+
+def test_a_long_context():
+    b = Batch([1], [131071], 8, 1, 128, 64, seed=3)
+    check(b, *call(b))
+
+
+@pytest.mark.parametrize("n,lens,Hq,Hkv,D", [([1] * 40, [100 * i + 1 for i in range(40)], 32, 8, 128),
+                                             ([4] * 6, [3000] * 6, 16, 16, 64), ([1], [20000], 16, 2, 256)])
+def test_repeated_calls_give_the_same_bits(n, lens, Hq, Hkv, D):
+    b = Batch(n, lens, Hq, Hkv, D, 64, seed=1)
+    dev = b.to("cuda")
+    q, args = b.q.cuda(), [dev[x] for x in NAMES]
+    want = bsp.fp8kv_attention(q, *args, return_lse=True)
+    for _ in range(50):
+        got = bsp.fp8kv_attention(q, *args, return_lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
