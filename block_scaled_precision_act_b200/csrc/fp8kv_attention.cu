@@ -1003,6 +1003,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     any_nan = true;
                 }
                 if (!seen || edge) {
+                    // This wait is for one fill of the slot among many, by parity: the fill before it must
+                    // be known to be over, or the wait is taken for done while that one is under way.  With
+                    // three slots or more it was a fill that the scores of an earlier tile needed; with two
+                    // it is the values of the tile before, whose product has to be over anyway before the
+                    // slot is filled again.
+                    if (C::kSlots == 2 && tile > seg.tile_begin)
+                        ok = C::wait(p_done + ((i - 1) & 1), (i - 1) >> 1 & 1, abort_flag, p.wait_ns,
+                                     p.status, 119) &&
+                             ok;
                     ok = C::wait(full + slot, phase, abort_flag, p.wait_ns, p.status, 120) && ok;
                     uint8_t* v = ring + slot * C::kSlot + t * 128;
 #pragma unroll 1

@@ -72,3 +72,31 @@ def test_repeated_calls_give_the_same_bits(n, lens, Hq, Hkv, D):
     for _ in range(50):
         got = bsp.fp8kv_attention(q, *args, return_lse=True)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("D,Hq,n,window", [(256, 4, 1, 0), (192, 16, 1, 0), (144, 2, 5, 0), (256, 16, 2, 300)])
+def test_wide_heads_beside_other_traffic(D, Hq, n, window):
+    """Heads of two pieces, whose tiles have two slots: the values of the last tile, whose masked tokens
+    hold NaN, are cleared after those of the tile before are used.  Loads are made late by copies on
+    another stream; the call gives the same bits each time."""
+    lens = [129 + 61 * i for i in range(40)]
+    b = Batch([n] * 40, lens, Hq, 2, D, 64, seed=D + n, spare=0)
+    for s, L in enumerate(lens):
+        for t in range(L, -(-L // 64) * 64):
+            page, slot = b.where(s, t)
+            b.k_cache[page, :, slot], b.v_cache[page, :, slot] = 0x7F, 0x7F
+    dev = b.to("cuda")
+    q, args = b.q.cuda(), [dev[x] for x in NAMES]
+    want, lse = bsp.fp8kv_attention(q, *args, window=window, return_lse=True)
+    check(b, want, lse, window=window)
+    side = torch.cuda.Stream()
+    big = torch.empty((2, 1 << 28), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                big[0].copy_(big[1])
+        for _ in range(20):
+            got = bsp.fp8kv_attention(q, *args, window=window)
+            assert torch.equal(got, want)
+    torch.cuda.synchronize()
