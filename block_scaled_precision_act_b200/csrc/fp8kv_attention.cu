@@ -18,10 +18,10 @@
 //   is an f16 again.  Each row has its own reference for p 2^e_V, beside the one for p: a block of large
 //   values that a row gives no weight takes no bits from it, whatever other rows make of that block.
 // One thread holds one token of a tile: its scores of all rows, so a weight's bytes for all rows and
-// terms are 32 or 64 bytes side by side (the operand's rows are tokens).  The rows' two references are
-// whole numbers (so that every rescaling is exact) and move only when they are exceeded by more than 7
-// (a factor 2^7 of the weights), which one vote of the 128 threads finds; only then are maxima exchanged
-// and O is rescaled.  The sums of the weights stay in the threads, in fp32, until a run ends.
+// terms are 32 or 64 bytes side by side (the operand's rows are tokens).  The rows' two references
+// move only when they are exceeded by more than 7 (a factor 2^7 of the weights), which one vote of the
+// 128 threads finds; only then are maxima exchanged and O is rescaled.  The sums of the weights stay in
+// the threads, in fp32, until a run ends.
 //
 // Warps: 0 walks over the items and loads the tiles (lanes look up pages and issue one box each), 1
 // issues both products (that of tile i + 1's scores before that of tile i's values), 2-5 are
@@ -484,9 +484,11 @@ template <int R>
 struct TokenShared {
     float row_fac[R];                            // scores: sm_scale log2(e) 2^(row's power)
     int row_pos[R];
-    // References of a row, whole numbers: m of its scores (base 2), m + d of its scores plus the value
-    // blocks' exponents.  And what the last change of them was: m's, and the factors of l and O.
-    float m[R], d[R], dm[R], fl[R], fo[R];
+    // References of a row: m of its scores (base 2), m + d of its scores plus the value blocks' exponents,
+    // d the whole number above `top`, the largest of these (less m) when they last moved.  The largest
+    // weight is 1 and its product with a power of two exact then.  And what the last change of the
+    // references was: m's, and the factors of l and O.
+    float m[R], d[R], top[R], dm[R], fl[R], fo[R];
     uint32_t unset;                              // rows whose references are not set yet
     int smax[4][R], tmax[4][R];
     float wsum[4][R];
@@ -494,6 +496,20 @@ struct TokenShared {
     void* to[R];                                 // where the row's output or part goes
     uint32_t nan[R][8];                          // NaN elements of V that a row sees, by d
 };
+
+// All elements of a token's values are NaN: so are those of every row that sees it.  (A call: rare, and the
+// code of a tile stays short.)
+template <int R>
+__device__ __noinline__ void note_nan_values(TokenShared<R>& sh, int tok, int window)
+{
+#pragma unroll 1
+    for (int r = 0; r < R; ++r) {
+        const int pos = sh.row_pos[r];
+        if (tok > pos || (window && tok <= pos - window)) continue;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) atomicOr(&sh.nan[r][k], 0xFFFFFFFFu);
+    }
+}
 
 template <int R, int ATOMS>
 __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
@@ -826,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 }
             }
             for (int k = t; k < R * 8; k += 128) sh.nan[k >> 3][k & 7] = 0;
-            if (t < R) sh.m[t] = sh.d[t] = 0.0f;
+            if (t < R) sh.m[t] = sh.d[t] = sh.top[t] = 0.0f;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
@@ -899,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     for (int r = 0; r < R; ++r) {
                         const float x = s[r] == s[r] ? s[r] : -INFINITY;
                         const int v = __reduce_max_sync(0xFFFFFFFFu, ordered(x));
-                        const int u = __reduce_max_sync(0xFFFFFFFFu, ordered(x - sh.d[r] + ev));
+                        const int u = __reduce_max_sync(0xFFFFFFFFu, ordered(x + ev));
                         if (lane == 0) {
                             sh.smax[q][r] = v;
                             sh.tmax[q][r] = u;
@@ -911,20 +927,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                         if (lane < R) {
                             // once to the first maximum, then only up
                             const bool first = unset >> lane & 1u;
-                            const float least = first ? -INFINITY : 0.0f;
-                            const float v = fmaxf(least, ceilf(from_ordered(
-                                max(max(sh.smax[0][lane], sh.smax[1][lane]),
-                                    max(sh.smax[2][lane], sh.smax[3][lane])))));
-                            const float u = fmaxf(least, ceilf(from_ordered(
-                                max(max(sh.tmax[0][lane], sh.tmax[1][lane]),
-                                    max(sh.tmax[2][lane], sh.tmax[3][lane])))));
+                            float v = from_ordered(max(max(sh.smax[0][lane], sh.smax[1][lane]),
+                                                       max(sh.smax[2][lane], sh.smax[3][lane])));
+                            float u = from_ordered(max(max(sh.tmax[0][lane], sh.tmax[1][lane]),
+                                                       max(sh.tmax[2][lane], sh.tmax[3][lane])));
                             still = first && v == -INFINITY;      // nothing seen: all stays 0
-                            const float dm = still ? 0.0f : v, dn = still ? 0.0f : u;
-                            sh.dm[lane] = dm;
-                            sh.m[lane] += dm;
-                            sh.d[lane] += dn - dm;
-                            sh.fl[lane] = first ? 0.0f : ex2(-dm);
-                            sh.fo[lane] = first ? 0.0f : ex2(-dn);
+                            if (still) v = u = 0.0f;
+                            if (!first) v = fmaxf(v, 0.0f), u = fmaxf(u, sh.top[lane]);
+                            const float d = ceilf(u - v), old = sh.d[lane];
+                            sh.dm[lane] = v;
+                            sh.m[lane] += v;
+                            sh.top[lane] = u - v;
+                            sh.d[lane] = d;
+                            sh.fl[lane] = first ? 0.0f : ex2(-v);
+                            sh.fo[lane] = first ? 0.0f : ex2(old - d - v);
                         }
                         const uint32_t left = __ballot_sync(0xFFFFFFFFu, still);
                         if (lane == 0) sh.unset = left;
@@ -995,11 +1011,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                 // row sees are cleared, and NaNs of one that only some rows see are taken out and
                 // noted for just those rows.
                 if (nan_v) {
-                    for (int r = 0; r < R; ++r) {
-                        const int pos = sh.row_pos[r];
-                        if (tok <= pos && (p.window == 0 || tok > pos - p.window))
-                            for (int k = 0; k < 8; ++k) atomicOr(&sh.nan[r][k], 0xFFFFFFFFu);
-                    }
+                    note_nan_values(sh, tok, p.window);
                     any_nan = true;
                 }
                 if (!seen || edge) {
