@@ -84,7 +84,7 @@ def build_fastcall(run, force: bool) -> None:
                                                              INCLUDE]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = FASTCALL + f".tmp{os.getpid()}"
-    run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+    run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra",
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
          *[x for d in inc for x in ("-isystem", d)], src, "-o", tmp, "-L", libs, "-lc10",
          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L", PKG, "-l:libbsp.so",
