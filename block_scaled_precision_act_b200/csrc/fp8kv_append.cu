@@ -11,8 +11,9 @@
 // atomics are needed.  The angles are the same for every head: the CTA makes them once, in
 // shared memory.  They are multiplied and reduced to half a turn in 64 bits (a position near
 // 2^20 times an fp32 frequency leaves few correct digits of the angle in 32), then sincospif.
-// 12300 tokens of 32 + 8 + 8 heads of 128: 58 us (4.4 TB/s), bound by instructions and loads by turns; one
-// token 4.6 us, 192 sequences of one token 7.8 us, bound by the chain of launch, batch, angles, store.
+// 12300 tokens of 32 + 8 + 8 heads of 128: 59 us (4.3 TB/s): a warp's loads, the CTA's angles, the rotation
+// and the stores come one after the other, and two or three CTAs on an SM hide that in part; one token 4.8
+// us, 192 sequences of one token 7.9 us, bound by the chain of launch, batch, angles, store.
 #include <cuda_bf16.h>
 
 #include <algorithm>

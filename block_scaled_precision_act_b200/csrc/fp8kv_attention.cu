@@ -30,7 +30,7 @@
 // three CTAs share an SM (two where tensor or shared memory has no room for more): one's waits, and its
 // beginnings and ends of items, hide behind the others' tiles.
 // 131071 tokens, 64 heads on 8: 60 us (4.5 TB/s over all, 6.5 inside a run); 64 ragged sequences, 32 on 8:
-// 90 us (4.4 TB/s); 517 tokens, 32 on 8: 12.8 us, the latency of five tiles and of the two ends.
+// 89 us (4.4 TB/s); 517 tokens, 32 on 8: 12.4 us, the latency of five tiles and of the two ends.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -3,9 +3,10 @@
 //
 // What bounds it is reading the weight, 9/16 byte for each, and next to it decoding what was read: 14
 // instructions for 8 weights of a lane keep the schedulers busy in half of the cycles, and the loads
-// that four warps on each can have in flight bring 5.4 TB/s (131072 x 8192, one row: 111 us).  With more rows
-// the products come on top (16384 x 12288, 16 rows: 40 us, 2.9 TB/s; three CTAs on an SM, whose registers
-// spill, took a quarter longer).  Where all CTAs run at once it goes another way (gemv_direct.cu).
+// that four warps on each can have in flight bring 5.4 TB/s (131072 x 8192, one row: 112 us at 1965 MHz, and
+// 122 to 126 after a tenth of a second of such calls, when the power limit holds the SMs at 1.75 GHz).  With
+// more rows the products come on top (16384 x 12288, 16 rows: 40 us, 2.9 TB/s; three CTAs on an SM, whose
+// registers spill, took a quarter longer).  Where all CTAs run at once it goes another way (gemv_direct.cu).
 //
 // Two kernels.  nvfp4_gemv_rows_kernel writes x in f16, times a power of two for each row, to the
 // workspace, in the order in which shared memory will hold it.  nvfp4_gemv_kernel: the 256-element K

@@ -12,7 +12,8 @@ The module only marshals: forward() is one nvfp4_linear call (activation quantiz
 FP4 GEMM) or fp8r_quantize_rows + fp8r_gemm, all in libbsp.so.  An nvfp4 module with
 `weight_only_rows` = r > 0 sends inputs of at most r rows (single tokens of a decode step; 32
 at most) to nvfp4_gemv instead, which reads the same weight and does not quantize the
-activations.  `weight_scale` is kept in the checkpoint's row-major [N][K/16] layout (the
+activations; with 16 to 26 rows or more of a large weight (see nvfp4_gemv in bsp.h) that takes
+longer than quantizing them.  `weight_scale` is kept in the checkpoint's row-major [N][K/16] layout (the
 state-dict form); the tensor-core layout the GEMM reads is built from it on the device once
 and rebuilt after a load.
 """
