@@ -169,16 +169,17 @@ def _stream(stream):
     return int(stream)
 
 
-def _scratch(nbytes: int, device, stream):
-    """A call's own workspace, allocated for the stream that the call runs on: its memory may be
-    given away as soon as the call returns, and then only to work behind the call's kernels."""
+def _new(shape, dtype, device, stream):
+    """A tensor that a call makes for itself or returns, allocated for the stream that the call runs on.
+    The memory of one from the current stream's pool may still be in use there by work that was queued
+    before, and that of a workspace is given away as soon as the call returns."""
     if stream is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _dtype(t, dt, what):
@@ -439,10 +440,10 @@ def nvfp4_gemv(x: torch.Tensor, w_codes, w_sf, w_scale, bias=None, out=None, wor
     N, _ = _mat(w_codes, torch.uint8, "w_codes", K // 2)
     _nvfp4_operands(0, N, K, None, None, w_sf, w_scale, bias)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _new((M, N), torch.bfloat16, x.device, stream)
     _buf(out, torch.bfloat16, "out", M * N)
     if workspace is None:
-        workspace = _scratch(nvfp4_gemv_workspace_bytes(M, N, K), x.device, stream)
+        workspace = _new((nvfp4_gemv_workspace_bytes(M, N, K),), torch.uint8, x.device, stream)
     _buf(workspace, torch.uint8, "workspace", 0)
     _check("nvfp4_gemv",
            lib().nvfp4_gemv(_ptr(x), _ptr(w_codes), _ptr(w_sf), _ptr(w_scale), _ptr(bias),
@@ -525,7 +526,7 @@ def fp8kv_append(k: torch.Tensor, v: torch.Tensor, k_cache, v_cache, k_scale, v_
     if q is not None:
         _, Hq, _, qs = _heads(q, "q", T, D)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            q_out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
         _buf(q_out, torch.bfloat16, "q_out", T * Hq * D)
     else:
         q_out = None
@@ -564,13 +565,14 @@ def fp8kv_attention(q: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_t
     if Hkv == 0 or Hq % Hkv != 0:
         raise BSPError(f"argument check (q's {Hq} heads are no multiple of the cache's {Hkv})", -1)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
     _buf(out, torch.bfloat16, "out", T * Hq * D)
     if lse is None and return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((T, Hq), torch.float32, q.device, stream)
     _buf(lse, torch.float32, "lse", T * Hq)
     if workspace is None:
-        workspace = _scratch(fp8kv_attention_workspace_bytes(T, Hq, Hkv, D), q.device, stream)
+        workspace = _new((fp8kv_attention_workspace_bytes(T, Hq, Hkv, D),), torch.uint8, q.device,
+                         stream)
     _buf(workspace, torch.uint8, "workspace", 0)
     _check("fp8kv_attention",
            lib().fp8kv_attention(_rows_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
