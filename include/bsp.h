@@ -358,7 +358,8 @@ int64_t nvfp4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *            *_stride: elements between tokens (% 8 == 0, at least heads * D), so that the three
  *            may lie in one projection's output.
  *   inv_freq [rot / 2] fp32 (device), rot % 16 == 0, 0 <= rot <= D: the first rot elements of each
- *            head are rotated by theta = position * inv_freq[j], taken in 64 bits; any scaling for
+ *            head are rotated by theta = position * inv_freq[j], taken in 64 bits and reduced there to
+ *            an fp32 number of half turns (off by 10^-7 radians at most); any scaling for
  *            long contexts is in the frequencies.  Pairs are (j, j + rot / 2), or (2j, 2j + 1) with
  *            interleaved = 1.  cos and sin are multiplied by rope_scale.
  *   q_out    [T][Hq][D] bf16, contiguous; may be q itself when that is contiguous.
