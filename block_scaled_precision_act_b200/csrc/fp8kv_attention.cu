@@ -14,8 +14,9 @@
 //   so a bf16 element (eight bits) is exact, down to 2^-26 of the row's largest.
 //   O[128 d][4 R] = V^T P^T.  The operand is p 2^e_V 2^(8 - ref), at most 2^15, rounded once, to f16 (11
 //   bits down to 2^-21 of the row's largest p 2^e_V, an absolute 2^-32 of that below), which is exactly
-//   the sum of four E5M2 values: an f16 cut to its upper byte is an E5M2, three bits of it, and the rest
-//   is an f16 again.  Each row has its own reference for p 2^e_V, beside the one for p: a block of large
+//   the sum of an E5M2, 1/8, 1/64 and 1/512 of others: an f16 cut to its upper byte is an E5M2, three bits
+//   of it, and the rest, times 8, is an f16 again, whose last bit comes within E5M2's range in time (2^-24
+//   512 = 2^-15; without the factors what lies below 2^-16 would be cut off).  Each row has its own reference for p 2^e_V, beside the one for p: a block of large
 //   values that a row gives no weight takes no bits from it, whatever other rows make of that block.
 // One thread holds one token of a tile: its scores of all rows, so a weight's bytes for all rows and
 // terms are 32 or 64 bytes side by side (the operand's rows are tokens).  The rows' two references
@@ -426,6 +427,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -991,7 +999,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     for (int j = 0; j < R / 4; ++j)
                         bytes[k][j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
 #pragma unroll
-                    for (int j = 0; j < R / 2; ++j) h[j] = sub_f16x2(h[j], h[j] & 0xFF00FF00u);
+                    for (int j = 0; j < R / 2; ++j)               // the rest, times 8
+                        h[j] = mul_f16x2(sub_f16x2(h[j], h[j] & 0xFF00FF00u), 0x48004800u);
                 }
                 // 16-byte chunks of the token's row, swizzled over its 32 or 64 bytes
                 if constexpr (R == 8) {
@@ -1132,7 +1141,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<R, ATOMS>::kCtas)
                     for (int j = 0; j < 8; ++j) {
                         const int r = r0 + j;
                         if (r >= nrows || d >= c.D) break;
-                        float x = ((o[3][j] + o[2][j]) + (o[1][j] + o[0][j])) * sh.inv[r] * sh.unit[r];
+                        const float sum = fmaf(fmaf(fmaf(o[3][j], 0.125f, o[2][j]), 0.125f, o[1][j]),
+                                               0.125f, o[0][j]);
+                        float x = sum * sh.inv[r] * sh.unit[r];
                         if (nans && (sh.nan[r][d >> 5] >> (d & 31) & 1u)) x = NAN;
                         if (seg.whole)
                             static_cast<__nv_bfloat16*>(sh.to[r])[d] = __float2bfloat16_rn(x);

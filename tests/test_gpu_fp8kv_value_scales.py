@@ -175,3 +175,34 @@ def test_a_nan_scale_of_keys_reaches_the_rows_that_see_it():
     out, lse = call(b)
     assert out[4:, :2].isnan().all() and lse[4:, :2].isnan().all()
     assert int(out.isnan().sum()) == 2 * 2 * 64 and int(lse.isnan().sum()) == 4
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 16), (256, 4)])
+@pytest.mark.parametrize("gap", [6, 12, 18, 22, 24, 26, 28, 30])
+def test_elements_that_only_small_blocks_have(D, Hq, gap):
+    """A block 2^gap larger has all of the weight that the others have, but its values are zero for every
+    other d: there the small blocks make the result, with products of 2^-gap of the row's largest."""
+    b = Batch([2], [300], Hq, 2 if Hq == 4 else 1, D, 16, seed=gap)
+    level(b)
+    raise_values(b, 0, 144, 160, gap)
+    for page, slot in tokens(b, 0, 144, 160):
+        b.v_cache[page, :, slot, ::2] = 0
+    check(b, *call(b))
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 2), (128, 8), (192, 4)])
+@pytest.mark.parametrize("bits", [8, 12, 14, 16, 18, 20, 22, 24, 26, 28])
+def test_one_token_against_many(D, Hq, bits):
+    """One token has 2^bits times the weight of each of 20000 others, whose values are not zero on
+    average: what is cut off of each would add up."""
+    L = 20000
+    b = Batch([1], [L], Hq, 1, D, 64, seed=bits, spare=0)
+    level(b)
+    b.q = torch.ones_like(b.q)
+    b.k_cache[:] = 0
+    page, slot = b.where(0, 12345)
+    b.k_cache[page, :, slot] = 0x38                  # 1, times 2^-8 and sm
+    sm = bits * math.log(2) * 2.0 ** (127 - 118) / D
+    b.v_cache = b.v_cache & 0x7F
+    b.v_cache[page, :, slot, ::2] = 0                # for every other d the many make the result
+    check(b, *call(b, sm_scale=sm), sm=sm)
