@@ -11,7 +11,8 @@
 // elements (the key scale multiplies the scores, the value scale the weights).
 //   S[128 tokens][3 R] = K Q^T.  A row of q, scaled by a power of two so that its largest element is in
 //   [128, 256), is the sum of three E4M3 rows of q, 16 q and 256 q's rounding rests: each holds four bits,
-//   so a bf16 element (eight bits) is exact, down to 2^-26 of the row's largest.
+//   so a bf16 element (eight bits) is exact down to 2^-17 of the row's largest, and off by 2^-25 of that (2^-18,
+//   half of E4M3's smallest step over 256) at most.
 //   O[128 d][4 R] = V^T P^T.  The operand is p 2^e_V 2^(8 - ref), at most 2^15, rounded once, to f16 (11
 //   bits down to 2^-21 of the row's largest p 2^e_V, an absolute 2^-32 of that below), which is exactly
 //   the sum of an E5M2, 1/8, 1/64 and 1/512 of others: an f16 cut to its upper byte is an E5M2, three bits
@@ -31,7 +32,7 @@
 // three CTAs share an SM (two where tensor or shared memory has no room for more): one's waits, and its
 // beginnings and ends of items, hide behind the others' tiles.
 // 131071 tokens, 64 heads on 8: 60 us (4.5 TB/s over all, 6.5 inside a run); 64 ragged sequences, 32 on 8:
-// 89 us (4.4 TB/s); 517 tokens, 32 on 8: 12.4 us, the latency of five tiles and of the two ends.
+// 88 us (4.5 TB/s); 517 tokens, 32 on 8: 12.5 us, the latency of five tiles and of the two ends.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -388,7 +388,7 @@ int fp8kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64
  *   q_bf16  [T][Hq][D], q_stride elements between tokens (% 8 == 0).
  *   out     [T][Hq][D] bf16, contiguous; lse [T][Hq] fp32 or NULL: log of sum_t p_t.
  *   A row that sees no token gives zeros and lse = -infinity.  Softmax statistics and sums are
- *   fp32; q is held to 2^-26 of the largest element of its head (bf16 elements above 2^-18 of that
+ *   fp32; q is held to 2^-25 of the largest element of its head (bf16 elements above 2^-17 of that
  *   exactly), and a weight p times the scale of its block of values is rounded once, to 11 bits, or to
  *   2^-32 of the row's largest such product where it is below 2^-21 of that.  All scale bytes are
  *   read as 2^(byte - 127), 255 as NaN.  What masked tokens hold (NaN, stale bytes, stale scales of blocks

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_scaled_precision_act_b200 as bsp
-from kv_reference import Batch
+from kv_reference import Batch, attention
 from test_gpu_fp8kv_append import call as append, check as check_append
 from test_gpu_fp8kv_attention import NAMES, call, check
 
@@ -55,6 +55,34 @@ def test_queries_that_are_not_finite(D):
     b.q = finite
     out[bad.cuda()], lse2[bad.cuda()] = clean[bad.cuda()], lse[bad.cuda()]
     check(b, out, lse2)
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 8), (256, 2)])
+@pytest.mark.parametrize("power", [0, 8, 12, 16, 18, 20, 22, 24, 26, 30, 100])
+def test_a_huge_element_of_q_against_zero_keys(D, Hq, power):
+    """The scores come from the other elements, which are held to 2^-25 of the huge one: exact while that
+    is below the last bit of all of them."""
+    b = Batch([1, 2], [90, 300], Hq, 2, D, 16, seed=power)
+    b.q = (torch.randint(128, 256, b.q.shape, generator=b.g) * torch.exp2(
+        torch.randint(-9, -6, b.q.shape, generator=b.g))).bfloat16() * torch.sign(b.q)
+    b.q[..., 3] = 2.0 ** power
+    b.k_cache[..., 3] = 0
+    b.v_cache[..., ::2] &= 0x7F
+    out, lse = call(b)
+    want, wlse, mass, size = attention(b, D ** -0.5, 0)
+    # all others are at least 1/4: exact down to 2^-17 of the largest, off by 2^-25 of it below
+    off = 0.0 if power <= 15 else 2.0 ** (power - 25)
+    k1 = torch.zeros_like(size)                      # largest sum |k| that a row sees
+    for s in range(2):
+        k = b.values("k", s, b.lens[s]).abs().sum(-1).amax(-1).repeat_interleave(Hq // 2)
+        k1[int(b.cu[s]):int(b.cu[s + 1])] = k
+    ds = (D / 16 + 20) * 2.0 ** -22 * size + off * k1 * D ** -0.5
+    if float(ds.max()) > 0.25:                       # nothing is left of the others
+        assert out.isfinite().all()
+        return
+    assert ((lse.cpu().double() - wlse).abs() <= ds + 2.0 ** -20 + 2.0 ** -22 * wlse.abs()).all()
+    weight = torch.expm1(2 * ds)[..., None] + 2 * (2.0 ** -11 + 2.0 ** -20) + (300 / 16 + 32) * 2.0 ** -22
+    assert ((out.cpu().double() - want).abs() <= want.abs() * 2.0 ** -8 + weight * mass).all()
 
 
 def test_a_long_context():
